@@ -473,6 +473,148 @@ int moe_forward_packed_noalloc(const void *x, const int32_t *ids, const float *w
                                int dtype, int T, int K, int E, int d, int f, int tm, float *out,
                                moe_stream_t stream);
 
+/*
+ * ---- Dense operators beside the routed layer ----
+ *
+ * The router's own product and the dense (shared) expert that every token
+ * takes, with the gradients that train them: a matrix product with bias,
+ * activation and residual; the router's balance losses with the gradient of
+ * its logits; an activation whose inputs are kept for the backward pass in 8
+ * bits. Conventions as above (device pointers, the caller's stream and
+ * workspace, no host wait, argument checks before any HIP call); in addition
+ *  - matrices are row-major with a row stride in elements (ld >= row length,
+ *    at most 2^20) and a 16-byte aligned first element; every size from 1 on
+ *    is served, rows that are not whole 16-byte chunks at the price of a copy
+ *    in the workspace;
+ *  - products are accumulated and epilogues computed in fp32 and rounded once
+ *    to the result's type;
+ *  - a workspace is needed only where its size is not 0 (then 256-byte
+ *    aligned); it starts with any contents, and calls that may overlap need
+ *    one each;
+ *  - results do not depend on timing: the same call gives the same bits.
+ */
+
+/* Activations: relu max(z, 0); silu z / (1 + exp(-z)); gelu z Phi(z), Phi the
+ * normal distribution function (erf form). NaN gives NaN. */
+enum moe_act { MOE_ACT_NONE = 0, MOE_ACT_RELU = 1, MOE_ACT_SILU = 2, MOE_ACT_GELU = 3 };
+
+/*
+ * moe_linear -- out = act(x W + bias) + residual: router logits (fp32 out,
+ * the input of moe_route_topk), or a projection of a dense expert, whose last
+ * product adds the routed layer's output (residual = moe_forward's out, fp32).
+ * In:  x [T][d] stride ldx, w [d][n] stride ldw (input index, then output
+ *      index, as the expert weights), bias [n] or NULL: all of dtype;
+ *      residual [T][n] stride ldr of residual_dtype (dtype or MOE_F32) or
+ *      NULL. It may be out itself (same type and stride).
+ * Out: out [T][n] stride ldo of out_dtype (dtype or MOE_F32). Only columns
+ *      [0, n) of its rows are written.
+ * workspace: moe_linear_workspace() bytes (padded copies of operands whose
+ *      stride or row length is not a multiple of 16 bytes; fp32 partial sums
+ *      when few tiles are cut along d).
+ * Errors: MOE_EINVAL for T, d or n < 1, a stride below the row length or above
+ *      2^20, a bad dtype or act, NULL or misaligned pointers, a small
+ *      workspace, more than 2^31 tiles of 128 x 128; MOE_EHIP on a failed launch.
+ */
+int moe_linear_workspace(int T, int d, int n, int64_t ldx, int64_t ldw, int dtype, size_t *bytes);
+int moe_linear(const void *x, int64_t ldx, const void *w, int64_t ldw, const void *bias,
+               const void *residual, int64_t ldr, int residual_dtype, int dtype, int act, int T,
+               int d, int n, void *workspace, size_t ws_bytes, void *out, int64_t ldo,
+               int out_dtype, moe_stream_t stream);
+
+/*
+ * moe_linear_backward -- the gradients of z = x W + bias from dz [T][n] (of
+ * dtype, stride lddz):
+ *   dx = dz W^T [T][d] (dtype),  dw = x^T dz [d][n],  db = sum over t of dz [n]
+ * (dw and db of grad_dtype: dtype or MOE_F32). A NULL dx, dw or db is not
+ * computed, and an operand that only it reads (w for dx, x for dw) may be
+ * NULL; one at least is asked for. With an activation behind z, dz is what
+ * moe_act_backward gives; the residual's gradient is the output's own.
+ * grads (workspace size): the MOE_GRAD_ bits of what is asked for.
+ * Errors: as moe_linear.
+ */
+enum moe_grad { MOE_GRAD_X = 1, MOE_GRAD_W = 2, MOE_GRAD_BIAS = 4 };
+int moe_linear_backward_workspace(int T, int d, int n, int64_t ldx, int64_t ldw, int64_t lddz,
+                                  int dtype, int grads, size_t *bytes);
+int moe_linear_backward(const void *x, int64_t ldx, const void *w, int64_t ldw, const void *dz,
+                        int64_t lddz, int dtype, int T, int d, int n, void *workspace,
+                        size_t ws_bytes, void *dx, int64_t lddx, void *dw, int64_t lddw, void *db,
+                        int grad_dtype, moe_stream_t stream);
+
+/*
+ * moe_balance_loss -- the router's auxiliary losses over a batch of T tokens.
+ * p_t = softmax of token t's logits; a token is valid if one of its ids is in
+ * [0, E) (padding has ids -1); n_t valid tokens, c_e entries routed to expert
+ * e, n_a their sum:
+ *   prob[e] = (1 / n_t) sum over valid t of p_te
+ *   loss[0] = E sum_e (c_e / n_a) prob[e]               (balance)
+ *   loss[1] = (1 / n_t) sum over valid t of (log sum_e exp(logits_te))^2   (z)
+ * NaN and -inf logits are absent experts (p = 0); a row of only such logits
+ * adds nothing to prob and the z loss. +inf gives NaN. With no valid token
+ * both losses and prob are 0.
+ * In:  logits [T][E] fp32, ids [T*K] (moe_route_topk's).
+ * Out: cnt [E+2] int32: c_e, then n_t at cnt[E] and n_a at cnt[E+1];
+ *      prob [E] fp32; loss [2] fp32.
+ * Errors: as moe_route_topk; MOE_EINVAL also for a small workspace.
+ */
+int moe_balance_workspace(int T, int E, int K, size_t *bytes);
+int moe_balance_loss(const float *logits, const int32_t *ids, int T, int E, int K, void *workspace,
+                     size_t ws_bytes, int32_t *cnt, float *prob, float *loss, moe_stream_t stream);
+
+/*
+ * moe_route_backward -- the gradient of the router logits, of both the losses
+ * above and the renormalised weights of moe_route_topk, in one pass:
+ *   dlogits_te = p_te (dloss[0] (E / n_t) (c_e / n_a - sum_j c_j / n_a p_tj)
+ *                      + dloss[1] (2 / n_t) lse_t)              for valid t
+ *                + sum over t's entries k with id e: w_k (dw_k - sum_j w_j dw_j)
+ * (the sum over j: t's entries with a valid id; 0 elsewhere).
+ * In:  logits, ids, as above; w [T*K] fp32 (moe_route_topk's weights) and dw
+ *      [T*K] fp32 their gradient, or dw NULL (w is then not read): no second
+ *      term; cnt [E+2] from moe_balance_loss; dloss [2] fp32, the gradient of
+ *      the training loss by loss[0] and loss[1], on the device, or NULL: no
+ *      first term. Not both NULL. Values of w and dw at invalid ids are not used.
+ * Out: dlogits [T][E] of dtype (MOE_F32, or the type of the router's product,
+ *      whose moe_linear_backward takes it as dz). Every element is written.
+ * Errors: as moe_route_topk.
+ */
+int moe_route_backward(const float *logits, const int32_t *ids, const float *w, const float *dw,
+                       const int32_t *cnt, const float *dloss, int T, int E, int K, void *dlogits,
+                       int dtype, moe_stream_t stream);
+
+/*
+ * moe_act_forward -- h = act(g) * u (gated: SwiGLU with MOE_ACT_SILU), or h =
+ * act(g) with u NULL; and, unless g8 is NULL, the checkpoint its backward
+ * starts from: 8 bits an element instead of g and u themselves.
+ * Checkpoint of a matrix z [T][f]: rows are cut into blocks of
+ * MOE_ACT8_BLOCK columns (the last may be shorter); a block has one scale byte
+ * s and each element one e4m3 code (4 exponent bits, bias 7, 3 fraction bits,
+ * largest 448, 0x7f NaN) and stands for code * 2^(s - 127) exactly. With M the
+ * block's largest finite magnitude, s - 127 is the least e with M <= 448 * 2^e,
+ * within [-110, 120] (-110 for M = 0); the code is z * 2^-e rounded once
+ * (nearest, ties to even). Elements that are not finite have code 0x7f. The
+ * relative error is at most 2^-4 for magnitudes of at least 2^(e-6), and below
+ * that the absolute error is at most 2^(e-10).
+ * In:  g, u [T][f] of dtype, strides ldg, ldu. act: not MOE_ACT_NONE.
+ * Out: h [T][f] of dtype, stride ldh; g8 [T][f] codes and gs [T][ceil(f / 32)]
+ *      scales, contiguous (g8 16-byte aligned); u8 and us likewise, given
+ *      exactly when g8 and u are.
+ * Errors: MOE_EINVAL for T or f < 1, a bad stride, dtype or act, NULL or
+ *      misaligned pointers, a checkpoint given in part; MOE_EHIP on a failed launch.
+ *
+ * moe_act_backward -- from that checkpoint (g, u: the values it stands for)
+ * and dh [T][f] of dtype:
+ *   dg = dh * u * act'(g),  du = dh * act(g),  h = act(g) * u
+ * (u8, us and du NULL: dg = dh * act'(g), h = act(g)). relu'(0) = 0.
+ * h may be NULL; it is the operand x of the following product's dw. Errors: as above.
+ */
+#define MOE_ACT8_BLOCK 32
+int moe_act_forward(const void *g, int64_t ldg, const void *u, int64_t ldu, int dtype, int act,
+                    int T, int f, void *h, int64_t ldh, uint8_t *g8, uint8_t *gs, uint8_t *u8,
+                    uint8_t *us, moe_stream_t stream);
+int moe_act_backward(const uint8_t *g8, const uint8_t *gs, const uint8_t *u8, const uint8_t *us,
+                     const void *dh, int64_t lddh, int dtype, int act, int T, int f, void *dg,
+                     int64_t lddg, void *du, int64_t lddu, void *h, int64_t ldh,
+                     moe_stream_t stream);
+
 /* Static description of a status code. */
 const char *moe_status_str(int status);
 

@@ -28,6 +28,9 @@ STATUS = {0: "ok", 1: "invalid argument", 2: "unsupported", 3: "HIP runtime erro
 NOALLOC_WORKSPACE_BYTES = 64 << 20  # MOE_NOALLOC_WORKSPACE_BYTES
 META_FIELDS = ("nent", "nblk", "nr", "nt", "nactive", "maxcnt", "nskip", "nbad", "tm", "E", "K")
 META_N = 11
+ACTS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3}  # enum moe_act
+MOE_GRAD_X, MOE_GRAD_W, MOE_GRAD_BIAS = 1, 2, 4
+ACT8_BLOCK = 32  # MOE_ACT8_BLOCK
 STAGES = ("hist", "scan", "place", "gather", "worklist", "gateup", "down", "combine")
 TORCH_DTYPE = {MOE_F32: torch.float32, MOE_F16: torch.float16, MOE_BF16: torch.bfloat16}
 DTYPE_OF = {torch.float32: MOE_F32, torch.float16: MOE_F16, torch.bfloat16: MOE_BF16}
@@ -84,6 +87,17 @@ _SIGS = {
                                  SZ, P, SZ, P, P],
     "moe_forward_packed_timed": [P, P, P, P, P, P, I32, I32, I32, I32, I32, I32, I32, P, SZ, P, P,
                                  P],
+    "moe_linear_workspace": [I32, I32, I32, I64, I64, I32, ctypes.POINTER(ctypes.c_size_t)],
+    "moe_linear": [P, I64, P, I64, P, P, I64, I32, I32, I32, I32, I32, I32, P, SZ, P, I64, I32, P],
+    "moe_linear_backward_workspace": [I32, I32, I32, I64, I64, I64, I32, I32,
+                                      ctypes.POINTER(ctypes.c_size_t)],
+    "moe_linear_backward": [P, I64, P, I64, P, I64, I32, I32, I32, I32, P, SZ, P, I64, P, I64, P,
+                            I32, P],
+    "moe_balance_workspace": [I32, I32, I32, ctypes.POINTER(ctypes.c_size_t)],
+    "moe_balance_loss": [P, P, I32, I32, I32, P, SZ, P, P, P, P],
+    "moe_route_backward": [P, P, P, P, P, P, I32, I32, I32, P, I32, P],
+    "moe_act_forward": [P, I64, P, I64, I32, I32, I32, I32, P, I64, P, P, P, P, P],
+    "moe_act_backward": [P, P, P, P, P, I64, I32, I32, I32, I32, P, I64, P, I64, P, I64, P],
     "moe_forward_packed_noalloc": [P, P, P, P, P, P, I32, I32, I32, I32, I32, I32, I32, P, P],
 }
 
@@ -122,6 +136,36 @@ def _dev(t, name):
     if not t.is_contiguous():
         raise ValueError(f"{name}: expected a contiguous tensor")
     return t.data_ptr()
+
+
+def _mat(t, name, shape=None, dtype=None):
+    """(device address, row stride) of a row-major GPU matrix [R, C]; (None, 0) for None"""
+    if t is None:
+        return None, 0
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name}: expected a GPU tensor")
+    if t.dim() != 2 or (shape is not None and tuple(t.shape) != tuple(shape)):
+        raise ValueError(f"{name}: expected a matrix{'' if shape is None else ' ' + str(tuple(shape))}, "
+                         f"got {tuple(t.shape)}")
+    if dtype is not None and t.dtype not in (dtype if isinstance(dtype, tuple) else (dtype,)):
+        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+    rows, cols = t.shape
+    if cols > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name}: expected contiguous rows")
+    ld = t.stride(0) if rows > 1 else max(cols, 1)
+    if ld < cols:
+        raise ValueError(f"{name}: overlapping rows")
+    return t.data_ptr(), ld
+
+
+def _vec(t, name, n, dtype):
+    """device address of a contiguous GPU array of n elements (or None)"""
+    if t is None:
+        return None
+    p = _dev(t, name)
+    if t.numel() != n or t.dtype != dtype:
+        raise ValueError(f"{name}: expected {n} elements of {dtype}, got {tuple(t.shape)} {t.dtype}")
+    return p
 
 
 def _host(t, name):
@@ -423,3 +467,246 @@ def forward_host(x, ids, w, hw_gate, hw_up, hw_down, tm: int = 16, packed: bool 
     moe_forward_host_weights(x, ids, w, hw_gate, hw_up, hw_down, packed, dtype, T, K, E, d, f, tm,
                              slots, cache, workspace, out, stream)
     return out, cache, workspace
+
+
+# ---------------------------------------------- dense operators (C entry points) --
+
+def moe_linear_workspace(T: int, d: int, n: int, ldx: int, ldw: int, dtype: int) -> int:
+    v = ctypes.c_size_t()
+    _check("moe_linear_workspace",
+           lib().moe_linear_workspace(T, d, n, ldx, ldw, dtype, ctypes.byref(v)))
+    return v.value
+
+
+def moe_linear_backward_workspace(T, d, n, ldx, ldw, lddz, dtype: int, grads: int) -> int:
+    v = ctypes.c_size_t()
+    _check("moe_linear_backward_workspace",
+           lib().moe_linear_backward_workspace(T, d, n, ldx, ldw, lddz, dtype, grads,
+                                               ctypes.byref(v)))
+    return v.value
+
+
+def moe_balance_workspace(T: int, E: int, K: int) -> int:
+    v = ctypes.c_size_t()
+    _check("moe_balance_workspace", lib().moe_balance_workspace(T, E, K, ctypes.byref(v)))
+    return v.value
+
+
+# The short-named helpers take row-major GPU matrices (rows may be strided),
+# check shapes and types, allocate what is not given, on the stream that the
+# kernels run on, and launch on the tensors' device. `workspace` may be kept
+# from call to call; it is replaced when it is too small.
+
+class _Launch:
+    """Stream, device and workspace of one call whose tensors lie on t's device."""
+
+    def __init__(self, t, stream):
+        if not isinstance(t, torch.Tensor) or not t.is_cuda:
+            raise TypeError("expected a GPU tensor")
+        self.device, self.stream, self.on = t.device, stream, None
+        if t.device.index != torch.cuda.current_device():
+            self.on = torch.cuda.device(t.device)
+
+    def __enter__(self):
+        if self.on is not None:
+            self.on.__enter__()
+        if self.stream is None:
+            self.torch_stream = None
+            self.handle = torch.cuda.current_stream().cuda_stream
+        else:
+            self.handle = _stream(self.stream)
+            self.torch_stream = (self.stream if hasattr(self.stream, "cuda_stream")
+                                 else torch.cuda.ExternalStream(self.handle))
+        return self
+
+    def __exit__(self, *exc):
+        if self.on is not None:
+            self.on.__exit__(*exc)
+
+    def same(self, **tensors):
+        """the tensors that are given lie on this call's device"""
+        for name, t in tensors.items():
+            if t is not None and t.device != self.device:
+                raise ValueError(f"{name}: on {t.device}, expected {self.device}")
+
+    def empty(self, shape, dtype):
+        if self.torch_stream is None:
+            return torch.empty(shape, dtype=dtype, device=self.device)
+        with torch.cuda.stream(self.torch_stream):
+            return torch.empty(shape, dtype=dtype, device=self.device)
+
+    def workspace(self, given, need):
+        if given is not None and given.numel() * given.element_size() >= need:
+            return given
+        return self.empty((need,), torch.uint8)
+
+
+def linear(x, w, bias=None, residual=None, act: str = "none", out_dtype=None, workspace=None,
+           out=None, stream=None):
+    """out = act(x w + bias) + residual for x [T, d], w [d, n] of one type, in out_dtype
+    (x's type, or torch.float32); returns (out, workspace). residual may be out itself."""
+    dtype = DTYPE_OF[x.dtype]
+    (T, d), n = x.shape, w.shape[1]
+    with _Launch(x, stream) as at:
+        at.same(w=w, bias=bias, residual=residual, out=out, workspace=workspace)
+        px, ldx = _mat(x, "x")
+        pw, ldw = _mat(w, "w", (d, n), x.dtype)
+        pr, ldr = _mat(residual, "residual", (T, n), (x.dtype, torch.float32))
+        if out is None:
+            out = at.empty((T, n), out_dtype or x.dtype)
+        elif out_dtype is not None and out.dtype != out_dtype:
+            raise TypeError(f"out: expected {out_dtype}, got {out.dtype}")
+        po, ldo = _mat(out, "out", (T, n), (x.dtype, torch.float32))
+        workspace = at.workspace(workspace, moe_linear_workspace(T, d, n, ldx, ldw, dtype))
+        _check("moe_linear", lib().moe_linear(
+            px, ldx, pw, ldw, _vec(bias, "bias", n, x.dtype), pr, ldr,
+            dtype if residual is None else DTYPE_OF[residual.dtype], dtype, ACTS[act], T, d, n,
+            workspace.data_ptr(), workspace.numel() * workspace.element_size(), po, ldo,
+            DTYPE_OF[out.dtype], at.handle))
+    return out, workspace
+
+
+def linear_backward(x, w, dz, grads=("dx", "dw", "db"), grad_dtype=None, workspace=None, dx=None,
+                    dw=None, db=None, stream=None):
+    """Gradients of z = x w + bias from dz [T, n]: dx [T, d] (dz's type), dw [d, n] and db
+    [n] in grad_dtype (dz's type, or torch.float32). `grads` names what is computed; a
+    given dx, dw or db is filled. x may be None without dw, w without dx (not both).
+    Returns (dict of the gradients, workspace)."""
+    dtype = DTYPE_OF[dz.dtype]
+    T, n = dz.shape
+    if x is None and w is None:
+        raise ValueError("x and w are both None")
+    d = x.shape[1] if x is not None else w.shape[0]
+    want = {"dx": dx, "dw": dw, "db": db}
+    if not grads or set(grads) - set(want):
+        raise ValueError(f"grads: expected some of dx, dw, db, got {grads}")
+    with _Launch(dz, stream) as at:
+        at.same(x=x, w=w, dx=dx, dw=dw, db=db, workspace=workspace)
+        px, ldx = _mat(x, "x", (T, d), dz.dtype)
+        pw, ldw = _mat(w, "w", (d, n), dz.dtype)
+        pz, lddz = _mat(dz, "dz")
+        if ("dw" in grads and x is None) or ("dx" in grads and w is None):
+            raise ValueError("dw needs x, dx needs w")
+        if grad_dtype is None:
+            grad_dtype = next((g.dtype for g in (dw, db) if g is not None), dz.dtype)
+        shapes = {"dx": ((T, d), dz.dtype), "dw": ((d, n), grad_dtype), "db": ((n,), grad_dtype)}
+        got = {k: want[k] if want[k] is not None else at.empty(*shapes[k])
+               for k in ("dx", "dw", "db") if k in grads}
+        pdx, lddx = _mat(got.get("dx"), "dx", (T, d), dz.dtype)
+        pdw, lddw = _mat(got.get("dw"), "dw", (d, n), grad_dtype)
+        pdb = _vec(got.get("db"), "db", n, grad_dtype)
+        mask = ((MOE_GRAD_X if pdx else 0) | (MOE_GRAD_W if pdw else 0) |
+                (MOE_GRAD_BIAS if pdb else 0))
+        need = moe_linear_backward_workspace(T, d, n, ldx, ldw, lddz, dtype, mask)
+        workspace = at.workspace(workspace, need)
+        _check("moe_linear_backward", lib().moe_linear_backward(
+            px, ldx, pw, ldw, pz, lddz, dtype, T, d, n, workspace.data_ptr(),
+            workspace.numel() * workspace.element_size(), pdx, lddx, pdw, lddw, pdb,
+            DTYPE_OF[grad_dtype], at.handle))
+    return got, workspace
+
+
+def balance_loss(logits, ids, workspace=None, cnt=None, prob=None, loss=None, stream=None):
+    """Router losses of logits [T, E] fp32 and ids [T, K] int32. Returns (dict, workspace):
+    loss [2] (balance, z), cnt [E + 2] int32 (entries per expert, valid tokens, valid
+    entries), prob [E] (mean probability over the valid tokens)."""
+    T, E = logits.shape
+    K = ids.shape[1]
+    with _Launch(logits, stream) as at:
+        at.same(ids=ids, cnt=cnt, prob=prob, loss=loss, workspace=workspace)
+        cnt = at.empty((E + 2,), torch.int32) if cnt is None else cnt
+        prob = at.empty((E,), torch.float32) if prob is None else prob
+        loss = at.empty((2,), torch.float32) if loss is None else loss
+        workspace = at.workspace(workspace, moe_balance_workspace(T, E, K))
+        _check("moe_balance_loss", lib().moe_balance_loss(
+            _vec(logits, "logits", T * E, torch.float32), _vec(ids, "ids", T * K, torch.int32), T,
+            E, K, workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+            _vec(cnt, "cnt", E + 2, torch.int32), _vec(prob, "prob", E, torch.float32),
+            _vec(loss, "loss", 2, torch.float32), at.handle))
+    return {"loss": loss, "cnt": cnt, "prob": prob}, workspace
+
+
+def route_backward(logits, ids, w, dw, cnt, dloss, out_dtype=None, out=None, stream=None):
+    """Gradient of the router logits [T, E] from dw [T, K], the gradient of route()'s weights
+    w (None: no such term), and dloss [2], the gradient by balance_loss()'s two losses
+    (None: no such term); cnt as balance_loss() gave it. out_dtype: fp32, or the type of
+    the router's product."""
+    T, E = logits.shape
+    K = ids.shape[1]
+    with _Launch(logits, stream) as at:
+        at.same(ids=ids, w=w, dw=dw, cnt=cnt, dloss=dloss, out=out)
+        if out is None:
+            out = at.empty((T, E), out_dtype or torch.float32)
+        elif out_dtype is not None and out.dtype != out_dtype:
+            raise TypeError(f"out: expected {out_dtype}, got {out.dtype}")
+        _check("moe_route_backward", lib().moe_route_backward(
+            _vec(logits, "logits", T * E, torch.float32), _vec(ids, "ids", T * K, torch.int32),
+            _vec(w, "w", T * K, torch.float32), _vec(dw, "dw", T * K, torch.float32),
+            _vec(cnt, "cnt", E + 2, torch.int32), _vec(dloss, "dloss", 2, torch.float32), T, E, K,
+            _vec(out, "out", T * E, out.dtype), DTYPE_OF[out.dtype], at.handle))
+    return out
+
+
+def act_forward(g, u=None, act: str = "silu", ckpt=None, h=None, stream=None):
+    """h = act(g) * u (or act(g)) for matrices [T, f]. ckpt: None (nothing kept), True (a
+    new 8-bit checkpoint) or an earlier call's, which is overwritten. Returns (h, ckpt);
+    a checkpoint is a dict of e4m3 codes g8, u8 [T, f] and scale bytes gs, us [T,
+    ceil(f / 32)], code * 2^(scale - 127) the values they stand for."""
+    T, f = g.shape
+    with _Launch(g, stream) as at:
+        at.same(u=u, h=h)
+        pg, ldg = _mat(g, "g")
+        pu, ldu = _mat(u, "u", (T, f), g.dtype)
+        h = at.empty((T, f), g.dtype) if h is None else h
+        ph, ldh = _mat(h, "h", (T, f), g.dtype)
+        if ckpt is True:
+            nb = -(-f // ACT8_BLOCK)
+            ckpt = {}
+            for k in ("g", "u")[:1 if u is None else 2]:
+                ckpt[k + "8"] = at.empty((T, f), torch.float8_e4m3fn)
+                ckpt[k + "s"] = at.empty((T, nb), torch.uint8)
+        g8, gs, u8, us = _ckpt(at, ckpt, T, f, u is not None)
+        _check("moe_act_forward", lib().moe_act_forward(
+            pg, ldg, pu, ldu, DTYPE_OF[g.dtype], ACTS[act], T, f, ph, ldh, g8, gs, u8, us,
+            at.handle))
+    return h, ckpt
+
+
+def act_backward(ckpt, dh, act: str = "silu", dg=None, du=None, h=None, need_h: bool = True,
+                 stream=None):
+    """From act_forward()'s checkpoint and dh [T, f]: a dict of dg, du (if there was a u) and
+    h, the forward's output as the checkpoint gives it (not with need_h=False)."""
+    T, f = dh.shape
+    gated = "u8" in ckpt
+    with _Launch(dh, stream) as at:
+        at.same(dg=dg, du=du, h=h)
+        if du is not None and not gated:
+            raise ValueError("du: the checkpoint has no u")
+        pz, lddh = _mat(dh, "dh")
+        new = lambda t: at.empty((T, f), dh.dtype) if t is None else t  # noqa: E731
+        got = {"dg": new(dg)}
+        if gated:
+            got["du"] = new(du)
+        if need_h or h is not None:
+            got["h"] = new(h)
+        pdg, lddg = _mat(got["dg"], "dg", (T, f), dh.dtype)
+        pdu, lddu = _mat(got.get("du"), "du", (T, f), dh.dtype)
+        ph, ldh = _mat(got.get("h"), "h", (T, f), dh.dtype)
+        g8, gs, u8, us = _ckpt(at, ckpt, T, f, gated)
+        _check("moe_act_backward", lib().moe_act_backward(
+            g8, gs, u8, us, pz, lddh, DTYPE_OF[dh.dtype], ACTS[act], T, f, pdg, lddg, pdu, lddu,
+            ph, ldh, at.handle))
+    return got
+
+
+def _ckpt(at, ckpt, T, f, gated):
+    """device addresses g8, gs, u8, us of a checkpoint (None where there is none)"""
+    if ckpt is None:
+        return None, None, None, None
+    if ("u8" in ckpt) != gated:
+        raise ValueError("ckpt: made for another kind of activation (with or without u)")
+    at.same(**ckpt)
+    nb = -(-f // ACT8_BLOCK)
+    one = lambda k: (_vec(ckpt[k + "8"], k + "8", T * f, torch.float8_e4m3fn),  # noqa: E731
+                     _vec(ckpt[k + "s"], k + "s", T * nb, torch.uint8))
+    return one("g") + (one("u") if gated else (None, None))

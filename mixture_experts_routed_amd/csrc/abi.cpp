@@ -7,22 +7,12 @@
 
 #include <new>
 
-#include "../../include/moe_routed.h"
+#include "checks.hpp"
 #include "launch.hpp"
 
 namespace {
 
-constexpr int64_t kI32Max = 2147483647;
-
-bool aligned(const void *p, size_t a) { return p && (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
-int elem_bytes(int dtype) { return dtype == MOE_F32 ? 4 : 2; }
-
-bool dtype_ok(int dtype) { return dtype == MOE_F32 || dtype == MOE_F16 || dtype == MOE_BF16; }
-
 size_t round_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
-
-hipStream_t as_stream(moe_stream_t s) { return static_cast<hipStream_t>(s); }
 
 int plan_sizes(int T, int K, int E, int tm, moe_plan_sizes_t *o)
 {

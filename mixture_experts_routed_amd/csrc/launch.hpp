@@ -127,4 +127,52 @@ hipError_t launch_cache_stage(const CacheState &c, const int32_t *cnt, const voi
                               const void *hg, const void *hu, const void *hd, int64_t max_new,
                               hipStream_t s);
 
+// ---- dense product with its gradients (linear.hip) ----
+// Element types are the C ABI's codes; strides count elements. Null pointers
+// are absent operands (bias, residual) or gradients that are not asked for.
+struct LinearCall {
+    const void *x, *w, *bias, *residual;
+    void *out;
+    int64_t ldx, ldw, ldr, ldo;
+    int dtype, res_dtype, out_dtype, act;
+    int T, d, n;
+};
+struct LinearBackwardCall {
+    const void *x, *w, *dz;
+    void *dx, *dw, *db;
+    int64_t ldx, ldw, lddz, lddx, lddw;
+    int dtype, grad_dtype;
+    int T, d, n;
+};
+// byte offsets inside the workspace: padded copies of operands, split-K planes
+struct LinearSpace {
+    int64_t x, w, part, total;
+};
+struct LinearBackwardSpace {
+    int64_t x, w, dz, part, total;
+    int db_blocks;  // blocks of rows of the column sums
+};
+LinearSpace linear_space(int T, int d, int n, int64_t ldx, int64_t ldw, int dtype);
+LinearBackwardSpace linear_backward_space(int T, int d, int n, int64_t ldx, int64_t ldw,
+                                          int64_t lddz, int dtype, bool dx, bool dw, bool db);
+hipError_t launch_linear(const LinearCall &c, void *ws, hipStream_t s);
+hipError_t launch_linear_backward(const LinearBackwardCall &c, void *ws, hipStream_t s);
+
+// ---- router losses and the gradient of the logits (balance.hip) ----
+int64_t balance_workspace(int T, int E);
+hipError_t launch_balance_loss(const float *logits, const int32_t *ids, int T, int E, int K,
+                               int32_t *cnt, float *prob, float *loss, void *ws, hipStream_t s);
+hipError_t launch_route_backward(const float *logits, const int32_t *ids, const float *w,
+                                 const float *dw, const int32_t *cnt, const float *dloss, int T,
+                                 int E, int K, void *dlogits, int dtype, hipStream_t s);
+
+// ---- activation with its 8-bit checkpoint (act.hip) ----
+hipError_t launch_act_forward(const void *g, int64_t ldg, const void *u, int64_t ldu, int dtype,
+                              int act, int T, int f, void *h, int64_t ldh, uint8_t *g8, uint8_t *gs,
+                              uint8_t *u8, uint8_t *us, hipStream_t s);
+hipError_t launch_act_backward(const uint8_t *g8, const uint8_t *gs, const uint8_t *u8,
+                               const uint8_t *us, const void *dh, int64_t lddh, int dtype, int act,
+                               int T, int f, void *dg, int64_t lddg, void *du, int64_t lddu,
+                               void *h, int64_t ldh, hipStream_t s);
+
 }  // namespace moe

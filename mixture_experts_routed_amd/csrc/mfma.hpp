@@ -1,0 +1,84 @@
+// Device-side pieces of the dense operators (products, activations, their
+// gradients): buffer descriptors, element conversion, activations.
+#pragma once
+
+#include "common.hpp"
+
+namespace moe {
+
+// A buffer resource over `bytes` bytes from `base` (word 3: raw buffer of the
+// gfx9 family); a load at an offset past them returns zeros and touches no
+// memory, kOutside is past any of them.
+constexpr uint32_t kOutside = 0x80000000u;
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const void *base, uint32_t bytes)
+{
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(base), (short)0, (int)bytes,
+                                             0x00020000);
+}
+
+typedef __attribute__((address_space(3))) void *lds_ptr_t;
+
+// ---- element types ---------------------------------------------------------
+
+__device__ __forceinline__ float to_f32(float v) { return v; }
+__device__ __forceinline__ float to_f32(_Float16 v) { return (float)v; }
+__device__ __forceinline__ float to_f32(__bf16 v) { return (float)v; }
+
+// one rounding to nearest even (none for float)
+template <typename T> __device__ __forceinline__ T from_f32(float v) { return (T)v; }
+
+// N consecutive elements as floats. The address is a multiple of the vector's size.
+template <typename T, int N> struct Vec {
+    typedef T type __attribute__((ext_vector_type(N)));
+    static __device__ __forceinline__ void load(const T *p, float (&v)[N])
+    {
+        const type x = *reinterpret_cast<const type *>(p);
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] = to_f32(x[i]);
+    }
+    static __device__ __forceinline__ void store(T *p, const float (&v)[N])
+    {
+        type x;
+#pragma unroll
+        for (int i = 0; i < N; ++i) x[i] = from_f32<T>(v[i]);
+        *reinterpret_cast<type *>(p) = x;
+    }
+};
+
+// ---- activations (in 32 bits) ----------------------------------------------
+// silu(z) = z s, s = 1 / (1 + e^-z); gelu(z) = z Phi(z), Phi(z) = erfc(-z / sqrt 2) / 2
+// (erfc, not 1 + erf: for negative z the sum would cancel). NaN stays NaN.
+
+enum : int { kActNone = 0, kActRelu = 1, kActSilu = 2, kActGelu = 3 };
+
+__device__ __forceinline__ float act_apply(float z, int act)
+{
+    switch (act) {
+    case kActRelu: return z < 0.f ? 0.f : z;
+    case kActSilu: return z / (1.f + expf(-z));
+    case kActGelu: return 0.5f * z * erfcf(-0.70710678118654752f * z);
+    default: return z;
+    }
+}
+
+// a = act(z), the return value act'(z):
+//   relu' = [z > 0]; silu' = s (1 + z (1 - s)); gelu' = Phi(z) + z phi(z)
+__device__ __forceinline__ float act_slope(float z, int act, float &a)
+{
+    switch (act) {
+    case kActRelu: a = z < 0.f ? 0.f : z; return z > 0.f ? 1.f : z <= 0.f ? 0.f : z;
+    case kActSilu: {
+        const float s = 1.f / (1.f + expf(-z));
+        a = z * s;
+        return s * (1.f + z * (1.f - s));
+    }
+    case kActGelu: {
+        const float c = 0.5f * erfcf(-0.70710678118654752f * z);
+        a = z * c;
+        return c + z * (0.39894228040143268f * expf(-0.5f * z * z));
+    }
+    default: a = z; return 1.f;
+    }
+}
+
+}  // namespace moe
