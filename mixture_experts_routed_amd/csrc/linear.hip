@@ -8,19 +8,27 @@
 //   forward  A = x rows,     B = W columns
 //   dx       A = dz rows,    B = W rows
 //   dw       A = x columns,  B = dz columns
-// A workgroup computes a BM x BN tile in K-steps of 128 bytes of k (64 values
-// of the 16-bit types, 32 of fp32). A step's operands go from memory straight
-// into one of two LDS buffers (buffer loads with the LDS flag), one step ahead
-// of the matrix instructions that read the other. In LDS the 16-byte chunks
-// are permuted so that the reads of a wavefront meet every bank once:
-//   rows:     chunk c of row r (8 chunks, 128 bytes) sits at c ^ ((r >> 1) & 7)
-//   columns:  the 16 columns that one lane group reads (32 bytes of the 16-bit
-//             types, 64 of fp32) are a segment; segment s of row k sits at
-//             s ^ f(k), f taking 8 (4) values over the rows read together.
+// A workgroup of 4 wavefronts computes a BM x BN tile in K-steps of 64 bytes of
+// k (32 values of the 16-bit types, 16 of fp32). Five LDS buffers hold the
+// operands of five steps: those of step s + 4 are loaded (straight from memory
+// into LDS, no registers) while the matrix instructions of step s run, on
+// fragments that were read into registers during step s - 1; one barrier a
+// step. The loads are written in assembly so that the compiler does not count
+// them: it would let every LDS read wait for all loads in flight. They have no
+// register result; the kernel waits for them itself, by count.
+// In LDS the 16-byte chunks are permuted so that the reads of a wavefront
+// spread over the banks:
+//   rows:     chunk c of row r (4 chunks, 64 bytes) sits at c ^ ((r >> 1) & 3)
+//   columns:  the columns that a lane group reads together (16 of the 16-bit
+//             types, 32 of fp32) are a segment; segment s of row k sits at
+//             s ^ 2 (k & 3) (fp32: s ^ ((k >> 2) & 1)), so that the rows that are
+//             read together lie in different banks.
 // Columns of the 16-bit types are read with the transposing LDS load (4 rows x
 // 16 columns per 16 lanes), so no operand is rearranged in memory or registers.
 // The matrix instruction is given B's fragment first: a lane then holds 4
-// consecutive columns of one output row, which the epilogue stores together.
+// consecutive columns of one output row. The epilogue passes the accumulators
+// through LDS, so that a lane finishes and stores 8 consecutive columns and a
+// row is written in whole lines (and its code exists once, not per register).
 //
 // Operands whose rows are not whole 16-byte chunks (a stride or a contiguous
 // length that is not a multiple of 8, fp32: 4) are first copied into rows
@@ -36,33 +44,59 @@ namespace moe {
 
 namespace {
 
-constexpr int kStepBytes = 128;  // bytes of k per K-step of a row operand
+constexpr int kStepBytes = 64;  // bytes of k per K-step of a row operand
+constexpr int kBuffers = 5;     // steps whose operands LDS holds
 
+typedef float float16_t __attribute__((ext_vector_type(16)));
+
+// D[32][32] += A[32][16] B[16][32] (fp32: four of k = 2): lane l holds row
+// (column) l & 31 of A (B) with k = 8 (l >> 5) .. + 7 (fp32: 4 (l >> 5) .. + 3,
+// element j of both operands meeting in the j-th instruction), and of D column
+// l & 31, rows 8 q + 4 (l >> 5) .. + 3 in registers 4 q .. 4 q + 3. A wavefront
+// alone on its SIMD issues the 32x32 form at full rate, the 16x16 form at 0.6
+// of it (2.4 against 1.4 PFLOP/s over the GPU).
+// in_place is the same in assembly, with the accumulator in accumulation
+// registers: a tile that takes all 256 of them leaves the compiler none to
+// move them through, and it then copies accumulators around the instructions.
+// Its operands come from LDS reads and its results are first read long after
+// (the kernel waits there), so that no wait states are missing.
 template <typename T> struct Mma;
 template <> struct Mma<_Float16> {
-    static __device__ __forceinline__ float4_t run(uint4 a, uint4 b, float4_t c)
+    static __device__ __forceinline__ void run(uint4 a, uint4 b, float16_t &c)
     {
-        return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8_t, a),
-                                                      __builtin_bit_cast(half8_t, b), c, 0, 0, 0);
+        c = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(half8_t, a),
+                                                   __builtin_bit_cast(half8_t, b), c, 0, 0, 0);
+    }
+    static __device__ __forceinline__ void in_place(uint4 a, uint4 b, float16_t &c)
+    {
+#ifdef __HIP_DEVICE_COMPILE__
+        asm("v_mfma_f32_32x32x16_f16 %0, %1, %2, %0"
+            : "+a"(c)
+            : "v"(__builtin_bit_cast(half8_t, a)), "v"(__builtin_bit_cast(half8_t, b)));
+#endif
     }
 };
 template <> struct Mma<__bf16> {
-    static __device__ __forceinline__ float4_t run(uint4 a, uint4 b, float4_t c)
+    static __device__ __forceinline__ void run(uint4 a, uint4 b, float16_t &c)
     {
-        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a),
-                                                       __builtin_bit_cast(bf16x8_t, b), c, 0, 0, 0);
+        c = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, a),
+                                                    __builtin_bit_cast(bf16x8_t, b), c, 0, 0, 0);
+    }
+    static __device__ __forceinline__ void in_place(uint4 a, uint4 b, float16_t &c)
+    {
+#ifdef __HIP_DEVICE_COMPILE__
+        asm("v_mfma_f32_32x32x16_bf16 %0, %1, %2, %0"
+            : "+a"(c)
+            : "v"(__builtin_bit_cast(bf16x8_t, a)), "v"(__builtin_bit_cast(bf16x8_t, b)));
+#endif
     }
 };
-// fp32: lane group q of 16 lanes holds k = 4q .. 4q+3 of a 16-wide step; the
-// instruction takes one k per group, so element j of both operands meets in
-// the j-th of four
 template <> struct Mma<float> {
-    static __device__ __forceinline__ float4_t run(uint4 a, uint4 b, float4_t c)
+    static __device__ __forceinline__ void run(uint4 a, uint4 b, float16_t &c)
     {
         const float4_t x = __builtin_bit_cast(float4_t, a), y = __builtin_bit_cast(float4_t, b);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) c = __builtin_amdgcn_mfma_f32_16x16x4f32(x[j], y[j], c, 0, 0, 0);
-        return c;
+        for (int j = 0; j < 4; ++j) c = __builtin_amdgcn_mfma_f32_32x32x2f32(x[j], y[j], c, 0, 0, 0);
     }
 };
 
@@ -76,7 +110,7 @@ struct Epilogue {
     void *out;
     int64_t ldr, ldo;
     int res_f32, out_f32, act;
-    int vec;               // rows of out and residual take 4 columns at a time
+    int vec;               // rows of out and residual start at 16-byte boundaries
 };
 
 struct GemmArg {
@@ -92,272 +126,460 @@ struct GemmArg {
 
 namespace {
 
-// 4 consecutive columns c..c+3 of row r (those below N)
-template <typename T>
-__device__ __forceinline__ void finish4(const Epilogue &e, int64_t r, int c, int N, float4_t z)
+template <int W> __device__ __forceinline__ void act_all(float (&v)[W], int act)
 {
-    float v[4] = {z[0], z[1], z[2], z[3]};
-    if (e.vec && c + 4 <= N) {
-        if (e.bias) {
-            float b[4];
-            Vec<T, 4>::load(static_cast<const T *>(e.bias) + c, b);
+    switch (act) {
+    case kActRelu:
 #pragma unroll
-            for (int i = 0; i < 4; ++i) v[i] += b[i];
-        }
+        for (int i = 0; i < W; ++i) v[i] = act_apply(v[i], kActRelu);
+        break;
+    case kActSilu:
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = act_apply(v[i], e.act);
-        if (e.residual) {
-            float q[4];
-            if (e.res_f32)
-                Vec<float, 4>::load(static_cast<const float *>(e.residual) + r * e.ldr + c, q);
-            else
-                Vec<T, 4>::load(static_cast<const T *>(e.residual) + r * e.ldr + c, q);
+        for (int i = 0; i < W; ++i) v[i] = act_apply(v[i], kActSilu);
+        break;
+    case kActGelu:
 #pragma unroll
-            for (int i = 0; i < 4; ++i) v[i] += q[i];
-        }
-        if (e.out_f32)
-            Vec<float, 4>::store(static_cast<float *>(e.out) + r * e.ldo + c, v);
-        else
-            Vec<T, 4>::store(static_cast<T *>(e.out) + r * e.ldo + c, v);
-        return;
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        if (c + i >= N) break;
-        float s = v[i];
-        if (e.bias) s += to_f32(static_cast<const T *>(e.bias)[c + i]);
-        s = act_apply(s, e.act);
-        if (e.residual)
-            s += e.res_f32 ? static_cast<const float *>(e.residual)[r * e.ldr + c + i]
-                           : to_f32(static_cast<const T *>(e.residual)[r * e.ldr + c + i]);
-        if (e.out_f32)
-            static_cast<float *>(e.out)[r * e.ldo + c + i] = s;
-        else
-            static_cast<T *>(e.out)[r * e.ldo + c + i] = from_f32<T>(s);
+        for (int i = 0; i < W; ++i) v[i] = act_apply(v[i], kActGelu);
+        break;
+    default: break;
     }
 }
 
+// 8 elements from a 16-byte aligned address
+template <typename T> __device__ __forceinline__ void load8(const T *p, float (&v)[8])
+{
+    if constexpr (sizeof(T) == 2) {
+        Vec<T, 8>::load(p, v);
+    } else {
+        float a[4], b[4];
+        Vec<T, 4>::load(p, a);
+        Vec<T, 4>::load(p + 4, b);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            v[i] = a[i];
+            v[4 + i] = b[i];
+        }
+    }
+}
+template <typename T> __device__ __forceinline__ void store8(T *p, const float (&v)[8])
+{
+    if constexpr (sizeof(T) == 2) {
+        Vec<T, 8>::store(p, v);
+    } else {
+        const float a[4] = {v[0], v[1], v[2], v[3]}, b[4] = {v[4], v[5], v[6], v[7]};
+        Vec<T, 4>::store(p, a);
+        Vec<T, 4>::store(p + 4, b);
+    }
+}
+
+// columns c .. c + 7 of row r (those below N); c is a multiple of 8
+template <typename T>
+__device__ __forceinline__ void finish8(const Epilogue &e, int64_t r, int c, int N, float (&v)[8])
+{
+    const int64_t ro = r * e.ldo + c, rr = r * e.ldr + c;
+    const bool whole = e.vec && c + 8 <= N;
+    if (e.bias) {
+        const T *b = static_cast<const T *>(e.bias) + c;
+        if (c + 8 <= N) {
+            float q[8];
+            load8<T>(b, q);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] += q[i];
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (c + i < N) v[i] += to_f32(b[i]);
+        }
+    }
+    act_all<8>(v, e.act);
+    if (e.residual) {
+        if (whole) {
+            float q[8];
+            if (e.res_f32)
+                load8<float>(static_cast<const float *>(e.residual) + rr, q);
+            else
+                load8<T>(static_cast<const T *>(e.residual) + rr, q);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] += q[i];
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (c + i < N)
+                    v[i] += e.res_f32 ? static_cast<const float *>(e.residual)[rr + i]
+                                      : to_f32(static_cast<const T *>(e.residual)[rr + i]);
+        }
+    }
+    if (whole) {
+        if (e.out_f32)
+            store8<float>(static_cast<float *>(e.out) + ro, v);
+        else
+            store8<T>(static_cast<T *>(e.out) + ro, v);
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        if (c + i < N) {
+            if (e.out_f32)
+                static_cast<float *>(e.out)[ro + i] = v[i];
+            else
+                static_cast<T *>(e.out)[ro + i] = from_f32<T>(v[i]);
+        }
+}
+
+// LDS byte address of a shared object
+__device__ __forceinline__ uint32_t lds_at(const void *p)
+{
+#ifdef __HIP_DEVICE_COMPILE__
+    return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const char *)p;
+#else
+    (void)p;
+    return 0;
+#endif
+}
+
+typedef int int4v __attribute__((ext_vector_type(4)));
+
+// Buffer resource words (as buffer_of). A range of 0 bytes makes every load zeros.
+__device__ __forceinline__ int4v rsrc_of(const char *base, uint32_t bytes)
+{
+    const uint64_t a = reinterpret_cast<uint64_t>(base);
+    return int4v{(int)(uint32_t)a, (int)((uint32_t)(a >> 32) & 0xffffu), (int)bytes, 0x00020000};
+}
+
+// 64 lanes x 16 bytes from the buffer at each lane's `off` to LDS at `to` + 16 lane;
+// counted by vmcnt, which the compiler does not know of here. Sets m0, which
+// nothing else in these kernels uses (a clobber of it cannot be declared).
+__device__ __forceinline__ void load_to_lds(uint32_t to, uint32_t off, int4v rsrc)
+{
+#ifdef __HIP_DEVICE_COMPILE__
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+                 :
+                 : "s"(to), "v"(off), "s"(rsrc)
+                 : "memory");
+#else
+    (void)to, (void)off, (void)rsrc;
+#endif
+}
+
 // One operand's part of a workgroup's tile: ROWS output rows (or columns) of
-// it, NTH threads; COL: the operand is in columns form.
-template <typename T, bool COL, int ROWS, int NTH>
+// it, NTH threads; COL: the operand is in columns form; NF: 32-row fragments
+// of a wavefront. Loads of successive K-steps are issued in order: advance()
+// makes the next step current.
+template <typename T, bool COL, int ROWS, int NTH, int NF>
 struct Operand {
     static constexpr int ES = sizeof(T), EPC = 16 / ES, BK = kStepBytes / ES;
-    static constexpr int CHUNKS = ROWS * 8;             // 16-byte chunks of a step
-    static constexpr int LOADS = CHUNKS / NTH;          // per thread
-    static constexpr int CPR = COL ? ROWS / EPC : 8;    // chunks per LDS row
+    static constexpr int BYTES = ROWS * kStepBytes;     // of a step
+    static constexpr int CHUNKS = BYTES / 16;
+    static constexpr int LOADS = CHUNKS / NTH;          // per thread and step
+    static constexpr int CPR = COL ? ROWS / EPC : kStepBytes / 16;  // chunks per LDS row
+    static constexpr int SEG = ES == 2 ? 2 : 8;         // columns form: chunks per segment
     static_assert(CHUNKS % NTH == 0, "whole loads");
+    static_assert(!COL || ROWS >= 128, "the permutation needs 8 (fp32: 2) segments");
 
     // the permutation of row k's segments (columns form)
     static __device__ __forceinline__ int seg_xor(int k)
     {
-        return ES == 2 ? ((k & 3) | ((k >> 1) & 4)) : ((k >> 2) & 3);
+        return ES == 2 ? (k & 3) << 1 : (k >> 2) & 1;
     }
 
-    const char *base;   // first byte of the tile's rows (rows form: at k = 0)
+    const char *base;    // rows form: the tile's first row; columns: the current step's first row
     int64_t ld;
-    int have;           // rows (columns) of the operand from the tile's first on
-    int K;              // values of k that it holds (rows form: a multiple of EPC)
+    uint32_t bytes;      // range of the current step's loads
+    uint32_t full, tail; // columns form: bytes of a whole step; of a row's part of the tile
+    int left;            // values of k from the current step on
+    int kc;              // rows form: the k within a step of this thread's chunks
     uint32_t off[LOADS];
-    int kc;             // rows form: the k within a step of this thread's chunks
+    uint32_t at[COL ? NF : 1];  // LDS byte of this lane's fragments in a buffer
 
-    __device__ __forceinline__ void init(const char *p, int64_t ld_, int first, int total, int K_,
-                                         int tid)
+    // K: values of k that the operand holds (rows form: a multiple of EPC); the
+    // first step starts at k0
+    __device__ __forceinline__ void init(const char *p, int64_t ld_, int first, int total, int K,
+                                         int k0, int tid, int frag0)
     {
         ld = ld_;
-        K = K_;
-        have = total - first;
-        base = COL ? p + (int64_t)first * ES : p + (int64_t)first * ld;
+        left = K - k0 + BK;  // (advance() comes before the first step)
+        const int have = min(ROWS, total - first);
         kc = 0;
+        if (COL) {
+            base = p + (int64_t)first * ES + ((int64_t)k0 - BK) * ld;
+            tail = (uint32_t)(have * ES);
+            full = (uint32_t)((BK - 1) * ld) + tail;
+        } else {
+            base = p + (int64_t)first * ld;
+            bytes = (uint32_t)((have - 1) * ld) + (uint32_t)(K * ES);
+        }
 #pragma unroll
         for (int i = 0; i < LOADS; ++i) {
             const int q = i * NTH + tid;
             const int r = q / CPR, c = q % CPR;
             if (COL) {
-                constexpr int SEG = ES == 2 ? 2 : 4;  // chunks per segment
                 const int lc = ((c / SEG) ^ seg_xor(r)) * SEG + c % SEG;
                 off[i] = lc * EPC < have ? (uint32_t)r * (uint32_t)ld + (uint32_t)lc * 16u : kOutside;
             } else {
-                const int lc = c ^ ((r >> 1) & 7);  // the same for every i
+                const int lc = c ^ ((r >> 1) & 3);  // the same for every i
                 kc = lc * EPC;
-                off[i] = r < have ? (uint32_t)r * (uint32_t)ld + (uint32_t)lc * 16u : kOutside;
+                off[i] = r < have ? (uint32_t)r * (uint32_t)ld + (uint32_t)lc * 16u +
+                                        (uint32_t)((k0 - BK) * ES)
+                                  : kOutside;
+            }
+        }
+        const int lane = tid & 63;
+        if (!COL) {
+            const int r = frag0 * 32 + (lane & 31);
+            at[0] = (uint32_t)(r * kStepBytes + ((lane >> 5) ^ ((r >> 1) & 3)) * 16);
+        } else {
+#pragma unroll
+            for (int i = 0; i < NF; ++i) {
+                if (ES == 2) {
+                    const int k = 8 * (lane >> 5) + ((lane >> 2) & 3);
+                    const int seg = (2 * (frag0 + i) + ((lane >> 4) & 1)) ^ seg_xor(k);
+                    at[i] = (uint32_t)((k * ROWS + seg * 16) * 2 + (lane & 3) * 8);
+                } else {
+                    const int k = 4 * (lane >> 5);
+                    at[i] = (uint32_t)((k * ROWS + ((frag0 + i) ^ seg_xor(k)) * 32 + (lane & 31)) * 4);
+                }
             }
         }
     }
 
-    // the loads of the step that starts at k0 into the LDS buffer L; k past K gives zeros
-    // (device pass only: with this body in a member function, the host pass of
-    // the compiler leaves out the launch stubs of some of the kernel's instances)
-    __device__ __forceinline__ void issue(uint4 *L, int k0, int wave) const
+    __device__ __forceinline__ void advance()
+    {
+        left -= BK;
+        if (COL) {
+            base += (int64_t)BK * ld;
+            bytes = left >= BK ? full : left > 0 ? (uint32_t)((left - 1) * ld) + tail : 0u;
+        } else {
+            // (a row past the operand's end stays outside: the range ends below 2^31)
+#pragma unroll
+            for (int i = 0; i < LOADS; ++i) off[i] += kStepBytes;
+        }
+    }
+
+    // the i-th load of the current step into the buffer at `to`; k past the end reads zeros
+    __device__ __forceinline__ void issue(uint32_t to, int i, int wave) const
+    {
+        const bool cut = !COL && kc >= left;
+        load_to_lds(to + (uint32_t)(i * NTH + wave * 64) * 16u, cut ? kOutside : off[i],
+                    rsrc_of(base, bytes));
+    }
+
+    // fragment i of this wavefront, k-group g (half a step), from the buffer at L (LDS byte)
+    __device__ __forceinline__ uint4 frag(uint32_t L, int i, int g) const
     {
 #ifdef __HIP_DEVICE_COMPILE__
-        __amdgpu_buffer_rsrc_t r;
-        if (COL) {
-            const int rows = min(BK, K - k0);
-            const int64_t bytes = (int64_t)(rows - 1) * ld + (int64_t)min(have, ROWS) * ES;
-            r = buffer_of(base + (int64_t)k0 * ld, rows > 0 ? (uint32_t)bytes : 0u);
-        } else {
-            const int64_t bytes = (int64_t)(min(have, ROWS) - 1) * ld + (int64_t)(K - k0) * ES;
-            r = buffer_of(base + (int64_t)k0 * ES, K > k0 ? (uint32_t)bytes : 0u);
-        }
-        const bool cut = !COL && k0 + kc >= K;
-#pragma unroll
-        for (int i = 0; i < LOADS; ++i)
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_ptr_t)(L + i * NTH + wave * 64), 16,
-                                                     cut ? kOutside : off[i], 0, 0, 0);
-#endif
-    }
-
-    // MFMA fragment of the 16 rows (columns) from `first` of the tile, k-group
-    // ks of the step: 16-bit: lane l holds row first + (l & 15), k = 32 ks +
-    // 8 (l >> 4) .. + 7; fp32: k = 16 ks + 4 (l >> 4) .. + 3
-    static __device__ __forceinline__ uint4 frag(const uint4 *L, int first, int ks, int lane)
-    {
-        if (!COL) {
-            const int r = first + (lane & 15), c = 4 * ks + (lane >> 4);
-            return L[r * 8 + (c ^ ((r >> 1) & 7))];
-        }
-        if constexpr (ES == 2) {
+        if constexpr (!COL) {
+            // chunk 2 g + (l >> 5): the permutation's bit 1 changes with g
+            typedef uint32_t u4 __attribute__((ext_vector_type(4)));
+            typedef __attribute__((address_space(3))) const u4 *p;
+            const u4 v = ((p)(uintptr_t)(L + (at[0] ^ (uint32_t)(g * 32))))[i * 2 * kStepBytes];
+            return make_uint4(v[0], v[1], v[2], v[3]);
+        } else if constexpr (ES == 2) {
             typedef short s4 __attribute__((ext_vector_type(4)));
-            typedef __attribute__((address_space(3))) s4 *p4;
-            const uint16_t *h = reinterpret_cast<const uint16_t *>(L);
-            s4 v[2];
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int k = 32 * ks + 8 * (lane >> 4) + 4 * i + ((lane >> 2) & 3);
-                const int seg = (first >> 4) ^ seg_xor(k);
-                v[i] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                    (p4)(const_cast<uint16_t *>(h) + k * ROWS + seg * 16 + (lane & 3) * 4));
-            }
-            const uint2 a = __builtin_bit_cast(uint2, v[0]), b = __builtin_bit_cast(uint2, v[1]);
+            typedef __attribute__((address_space(3))) s4 *p;
+            const p q = (p)(uintptr_t)(L + at[i]) + g * 4 * ROWS;  // 16 rows per group
+            const s4 v = __builtin_amdgcn_ds_read_tr16_b64_v4i16(q);
+            const s4 w = __builtin_amdgcn_ds_read_tr16_b64_v4i16(q + ROWS);  // 4 rows on
+            const uint2 a = __builtin_bit_cast(uint2, v), b = __builtin_bit_cast(uint2, w);
             return make_uint4(a.x, a.y, b.x, b.y);
         } else {
-            const uint32_t *w = reinterpret_cast<const uint32_t *>(L);
-            uint32_t v[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int k = 16 * ks + 4 * (lane >> 4) + j;
-                v[j] = w[k * ROWS + ((first >> 4) ^ seg_xor(k)) * 16 + (lane & 15)];
-            }
-            return make_uint4(v[0], v[1], v[2], v[3]);
+            typedef __attribute__((address_space(3))) const uint32_t *p;
+            const p q = (p)(uintptr_t)(L + at[i]) + g * 8 * ROWS;
+            return make_uint4(q[0], q[ROWS], q[2 * ROWS], q[3 * ROWS]);
         }
+#else
+        return make_uint4(0, 0, 0, 0);
+#endif
     }
 };
 
-// WM x WN wavefronts, each (BM / WM) x (BN / WN) of the tile
+// WM x WN = 4 wavefronts, each (BM / WM) x (BN / WN) of the tile
 template <typename T, bool AC, bool BC, int BM, int BN, int WM, int WN>
-__global__ __launch_bounds__(WM *WN * 64) void k_gemm(const GemmArg p)
+__global__ __launch_bounds__(256, (BM + BN > 256 ? 1 : 2)) void k_gemm(const GemmArg p)
 {
     constexpr int NTH = WM * WN * 64, BK = kStepBytes / (int)sizeof(T);
-    constexpr int TM = BM / WM / 16, TN = BN / WN / 16;
-    constexpr int KS = 2;  // k-groups of a step
-    __shared__ uint4 L0[(BM + BN) * 8], L1[(BM + BN) * 8];
+    constexpr int TM = BM / WM / 32, TN = BN / WN / 32;
+    constexpr bool BIG = TM * TN == 16;  // accumulators take all accumulation registers
+    typedef Operand<T, AC, BM, NTH, TM> OpA;
+    typedef Operand<T, BC, BN, NTH, TN> OpB;
+    constexpr uint32_t BUF = (BM + BN) * kStepBytes;
+    constexpr int LOADS = OpA::LOADS + OpB::LOADS;   // of a thread per step
+    constexpr int LEFT = LOADS * (kBuffers - 3);     // still in flight at a step's end
+    __shared__ uint4 lds[kBuffers * BUF / 16];
+    static_assert(NTH == 256 && LEFT < 64, "4 wavefronts; vmcnt has 6 bits");
     const int lb = xcd_logical_block(p.mt * p.nt * p.split);
     if (lb < 0) return;  // whole workgroup: no barrier reached
     const int tile = lb / p.split, split = lb - tile * p.split;
-    const int tm = tile / p.nt, tn = tile - tm * p.nt;
+    // 8 rows of tiles at a time, so that the tiles that one XCD works on share
+    // both operands
+    const int band = tile / (8 * p.nt), in = tile - band * 8 * p.nt;
+    const int bh = min(8, p.mt - band * 8);
+    const int tn = in / bh, tm = band * 8 + in - tn * bh;
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wave / WN, wn = wave - wm * WN;
+    const int s0 = split * p.steps;
+    const int s1 = min(s0 + p.steps, (p.K + BK - 1) / BK);
 
-    Operand<T, AC, BM, NTH> a;
-    Operand<T, BC, BN, NTH> b;
+    OpA a;
+    OpB b;
     // (the rows of a row operand hold k up to its padded length)
-    a.init(p.A, p.lda, tm * BM, AC ? p.a_cols : p.M, AC ? p.K : p.a_cols, tid);
-    b.init(p.B, p.ldb, tn * BN, BC ? p.b_cols : p.N, BC ? p.K : p.b_cols, tid);
+    a.init(p.A, p.lda, tm * BM, AC ? p.a_cols : p.M, AC ? p.K : p.a_cols, s0 * BK, tid, wm * TM);
+    b.init(p.B, p.ldb, tn * BN, BC ? p.b_cols : p.N, BC ? p.K : p.b_cols, s0 * BK, tid, wn * TN);
 
-    float4_t acc[TM][TN];
+    float16_t acc[TM][TN];
 #pragma unroll
     for (int i = 0; i < TM; ++i)
 #pragma unroll
-        for (int j = 0; j < TN; ++j) acc[i][j] = float4_t{0.f, 0.f, 0.f, 0.f};
+        for (int j = 0; j < TN; ++j)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
 
-    const int s0 = split * p.steps;
-    const int s1 = min(s0 + p.steps, (p.K + BK - 1) / BK);
-    auto issue = [&](uint4 *L, int s) {
-        a.issue(L, s * BK, wave);
-        b.issue(L + BM * 8, s * BK, wave);
+    const uint32_t base = lds_at(lds);
+    uint32_t rd = base, wr = base;  // buffers of the step to read and the step to load
+    auto next = [&](uint32_t q) { return q + BUF == base + kBuffers * BUF ? base : q + BUF; };
+    auto load = [&](int i) {
+        if (i == 0) a.advance();
+        if (i == OpA::LOADS) b.advance();
+        // (a resource word may come from a vector instruction: 5 wait states)
+        if (i == 0 || i == OpA::LOADS) asm volatile("s_nop 4" ::: "memory");
+        if (i < OpA::LOADS)
+            a.issue(wr, i, wave);
+        else
+            b.issue(wr + OpA::BYTES, i - OpA::LOADS, wave);
+        if (i == LOADS - 1) wr = next(wr);
     };
-    // this wavefront's loads landed and its LDS reads done; then all of them
-    auto meet = [&]() { asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory"); };
-    auto compute = [&](const uint4 *L) {
+    // fragments of the two k-groups of a step: those of one are read while the
+    // matrix instructions of the other run, in the order in which they are needed
+    uint4 fa[2][TM], fb[2][TN];
+    auto read = [&](int g, int q) {
+        if (q == 0 || q > TN)
+            fa[g][q == 0 ? 0 : q - TN] = a.frag(rd, q == 0 ? 0 : q - TN, g);
+        else
+            fb[g][q - 1] = b.frag(rd + OpA::BYTES, q - 1, g);
+    };
+    // matrix instructions of k-group g, between them the fragments of the other
+    // group and half of the loads of step s + 4
+    constexpr int GAP = TM * TN / (TM + TN), HALF = LOADS / 2;
+    static_assert(GAP * (TM + TN) == TM * TN && HALF * 2 == LOADS && HALF * 4 <= TM * TN * 2, "");
+    auto group = [&](int g) {
 #pragma unroll
-        for (int ks = 0; ks < KS; ++ks) {
-            uint4 fa[TM], fb[TN];
-#pragma unroll
-            for (int i = 0; i < TM; ++i)
-                fa[i] = Operand<T, AC, BM, NTH>::frag(L, (wm * TM + i) * 16, ks, lane);
-#pragma unroll
-            for (int j = 0; j < TN; ++j)
-                fb[j] = Operand<T, BC, BN, NTH>::frag(L + BM * 8, (wn * TN + j) * 16, ks, lane);
-#pragma unroll
-            for (int i = 0; i < TM; ++i)
-#pragma unroll
-                for (int j = 0; j < TN; ++j) acc[i][j] = Mma<T>::run(fb[j], fa[i], acc[i][j]);
+        for (int q = 0; q < TM * TN; ++q) {
+            if (q % GAP == 0) read(1 - g, q / GAP);
+            if (q % (TM * TN / HALF) == 0) load(g * HALF + q / (TM * TN / HALF));
+            if constexpr (BIG)
+                Mma<T>::in_place(fb[g][q % TN], fa[g][q / TN], acc[q / TN][q % TN]);
+            else
+                Mma<T>::run(fb[g][q % TN], fa[g][q / TN], acc[q / TN][q % TN]);
+            __builtin_amdgcn_sched_barrier(0);
         }
     };
     if (s0 < s1) {
-        issue(L0, s0);
-        meet();
-        for (int s = s0; s < s1; s += 2) {
-            if (s + 1 < s1) issue(L1, s + 1);
-            compute(L0);
-            meet();
-            if (s + 1 >= s1) break;
-            if (s + 2 < s1) issue(L0, s + 2);
-            compute(L1);
-            meet();
+#pragma unroll
+        for (int q = 0; q < kBuffers - 1; ++q)
+#pragma unroll
+            for (int i = 0; i < LOADS; ++i) load(i);
+        asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" : : "n"(LEFT) : "memory");
+#pragma unroll
+        for (int q = 0; q < TM + TN; ++q) read(0, q);
+        // Group 0 reads group 1 of its step, group 1 reads group 0 of the next.
+        // At a step's end this wavefront's loads of step s + 2 have landed, and
+        // with the barrier everyone's. The buffer that is loaded during step s
+        // was last read in group 0 of step s - 1, by reads that the matrix
+        // instructions of its group 1 waited for, before its barrier. A step
+        // past the end of k reads zeros.
+        for (int s = s0; s < s1; ++s) {
+            group(0);
+            rd = next(rd);
+            group(1);
+            asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" : : "n"(LEFT) : "memory");
+            __builtin_amdgcn_sched_barrier(0);
         }
+        // nothing in flight into LDS, and every wavefront done with it; the last
+        // matrix results readable
+        asm volatile("s_nop 15\n\ts_nop 15\n\ts_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+        __builtin_amdgcn_sched_barrier(0);
     }
 
+    const int row0 = tm * BM + wm * TM * 32, col0 = tn * BN + wn * TN * 32;
+    if (p.split > 1) {
+        float *plane = p.part + (int64_t)split * p.M * p.N;
 #pragma unroll
-    for (int i = 0; i < TM; ++i) {
-        const int m = tm * BM + (wm * TM + i) * 16 + (lane & 15);
-        if (m >= p.M) continue;
+        for (int i = 0; i < TM; ++i) {
+            const int m = row0 + i * 32 + (lane & 31);
 #pragma unroll
-        for (int j = 0; j < TN; ++j) {
-            const int n = tn * BN + (wn * TN + j) * 16 + 4 * (lane >> 4);
-            if (n >= p.N) continue;
-            if (p.split > 1) {
-                float *o = p.part + ((int64_t)split * p.M + m) * p.N + n;
-                if (n + 4 <= p.N && (p.N & 3) == 0)
-                    *reinterpret_cast<float4_t *>(o) = acc[i][j];
-                else
-                    for (int q = 0; q < 4 && n + q < p.N; ++q) o[q] = acc[i][j][q];
-            } else {
-                finish4<T>(p.e, m, n, p.N, acc[i][j]);
-            }
+            for (int j = 0; j < TN; ++j)
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const int n = col0 + j * 32 + 8 * q + 4 * (lane >> 5);
+                    if (m >= p.M || n >= p.N) continue;
+                    float *o = plane + (int64_t)m * p.N + n;
+                    const float16_t &c = acc[i][j];
+                    const float4_t v = {c[4 * q], c[4 * q + 1], c[4 * q + 2], c[4 * q + 3]};
+                    if (n + 4 <= p.N && (p.N & 3) == 0)
+                        *reinterpret_cast<float4_t *>(o) = v;
+                    else
+#pragma unroll
+                        for (int r = 0; r < 4; ++r)
+                            if (n + r < p.N) o[r] = v[r];
+                }
+        }
+        return;
+    }
+    // Each wavefront's own part of LDS holds 64 of its rows; rows are padded by
+    // 4 floats, which spreads the rows of a store over the banks.
+    constexpr int COLS = TN * 32, PITCH = COLS + 4, RG = 2, LPR = COLS / 8;
+    static_assert(RG * 32 * PITCH * 4 * 4 <= (int)(kBuffers * BUF) && TM % RG == 0, "fits");
+    float *mine = reinterpret_cast<float *>(lds) + wave * (RG * 32 * PITCH);
+#pragma unroll
+    for (int h = 0; h < TM; h += RG) {
+#pragma unroll
+        for (int i = 0; i < RG; ++i)
+#pragma unroll
+            for (int j = 0; j < TN; ++j)
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const float16_t &c = acc[h + i][j];
+                    *reinterpret_cast<float4_t *>(mine + (i * 32 + (lane & 31)) * PITCH + j * 32 +
+                                                  8 * q + 4 * (lane >> 5)) =
+                        float4_t{c[4 * q], c[4 * q + 1], c[4 * q + 2], c[4 * q + 3]};
+                }
+        // (LDS operations of one wavefront stay in order)
+#pragma unroll 1
+        for (int r = lane / LPR; r < RG * 32; r += 64 / LPR) {
+            const int m = row0 + h * 32 + r, n = col0 + (lane % LPR) * 8;
+            if (m >= p.M || n >= p.N) continue;
+            float v[8];
+            load8<float>(mine + r * PITCH + (lane % LPR) * 8, v);
+            finish8<T>(p.e, m, n, p.N, v);
         }
     }
 }
 
 // The split products' partial planes added in split order, then the epilogue:
-// one thread per 4 columns of a row.
+// one thread per 8 columns of a row.
 template <typename T>
 __global__ __launch_bounds__(256) void k_gemm_reduce(const float *__restrict__ part, int M, int N,
                                                      int split, const Epilogue e)
 {
-    const int per = (N + 3) / 4;
+    const int per = (N + 7) / 8;
     const int64_t total = (int64_t)M * per;
     for (int64_t q = (int64_t)blockIdx.x * 256 + threadIdx.x; q < total;
          q += (int64_t)gridDim.x * 256) {
         const int64_t r = q / per;
-        const int c = (int)(q - r * per) * 4;
-        float4_t z = {0.f, 0.f, 0.f, 0.f};
+        const int c = (int)(q - r * per) * 8;
+        float v[8] = {};
         const float *s = part + r * N + c;
-        if ((N & 3) == 0) {
-            for (int i = 0; i < split; ++i) {
-                z += *reinterpret_cast<const float4_t *>(s);
-                s += (int64_t)M * N;
-            }
-        } else {
-            for (int i = 0; i < split; ++i) {
+        for (int i = 0; i < split; ++i, s += (int64_t)M * N) {
+            float z[8];
+            if (c + 8 <= N && (N & 3) == 0)
+                load8<float>(s, z);
+            else
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    if (c + j < N) z[j] += s[j];
-                s += (int64_t)M * N;
-            }
+                for (int j = 0; j < 8; ++j) z[j] = c + j < N ? s[j] : 0.f;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] += z[j];
         }
-        finish4<T>(e, r, c, N, z);
+        finish8<T>(e, r, c, N, v);
     }
 }
 
@@ -425,9 +647,8 @@ __global__ __launch_bounds__(256) void k_colsum_join(const float *__restrict__ p
 
 // ---- host side ---------------------------------------------------------------
 
-constexpr int kBM = 128, kBN = 128;
 constexpr int kSlots = 512;       // workgroups of a 128 x 128 tile that the GPU holds at once
-constexpr int kMinSplitSteps = 4;
+constexpr int kMinSplitSteps = 8;
 
 int elem_size(int dtype) { return dtype == 0 ? 4 : 2; }
 int64_t up(int64_t v, int64_t a) { return (v + a - 1) / a * a; }
@@ -435,6 +656,7 @@ int64_t div_up(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 struct Product {
     int64_t mt, nt;
+    int tile;  // 128 or 256 rows and columns
     int split, steps;
     int64_t part_bytes;
 };
@@ -442,10 +664,11 @@ struct Product {
 Product product_of(int64_t M, int64_t N, int64_t K, int dtype)
 {
     Product z;
-    z.mt = div_up(M, kBM);
-    z.nt = div_up(N, kBN);
     const int64_t steps = div_up(K, kStepBytes / elem_size(dtype));
-    int64_t s = kSlots / (z.mt * z.nt);
+    z.tile = dtype != 0 && div_up(M, 256) * div_up(N, 256) >= 192 ? 256 : 128;
+    z.mt = div_up(M, z.tile);
+    z.nt = div_up(N, z.tile);
+    int64_t s = (z.tile == 256 ? kSlots / 2 : kSlots) / (z.mt * z.nt);
     s = s < steps / kMinSplitSteps ? s : steps / kMinSplitSteps;
     s = s < 1 ? 1 : s;
     z.steps = (int)div_up(steps, s);
@@ -522,19 +745,24 @@ hipError_t launch_product(const Matrix &A, const Matrix &B, int M, int N, int K,
     g.part = part;
     g.e = e;
     const dim3 grid((unsigned)up(z.mt * z.nt * z.split, 8)), block(256);
-    hipLaunchKernelGGL((k_gemm<T, AC, BC, kBM, kBN, 2, 2>), grid, block, 0, s, g);
+    if constexpr (sizeof(T) == 2) {
+        if (z.tile == 256)
+            hipLaunchKernelGGL((k_gemm<T, AC, BC, 256, 256, 2, 2>), grid, block, 0, s, g);
+        else
+            hipLaunchKernelGGL((k_gemm<T, AC, BC, 128, 128, 2, 2>), grid, block, 0, s, g);
+    } else {
+        hipLaunchKernelGGL((k_gemm<T, AC, BC, 128, 128, 2, 2>), grid, block, 0, s, g);
+    }
     if (z.split > 1) {
-        const int64_t quads = (int64_t)M * ((N + 3) / 4);
-        const dim3 rgrid((unsigned)(quads / 256 + 1 < 8192 ? quads / 256 + 1 : 8192));
+        const int64_t parts = (int64_t)M * ((N + 7) / 8);
+        const dim3 rgrid((unsigned)(parts / 256 + 1 < 8192 ? parts / 256 + 1 : 8192));
         hipLaunchKernelGGL(k_gemm_reduce<T>, rgrid, dim3(256), 0, s, part, M, N, z.split, e);
     }
     return hipGetLastError();
 }
 
-bool rows_take_4(const void *p, int64_t ld, int es)
-{
-    return !p || (ld % 4 == 0 && reinterpret_cast<uintptr_t>(p) % (4 * es) == 0);
-}
+// rows that start at 16-byte boundaries (p itself is 16-byte aligned)
+bool rows_aligned(const void *p, int64_t ld, int es) { return !p || ld * es % 16 == 0; }
 
 template <typename T>
 hipError_t linear_t(const LinearCall &c, char *ws, hipStream_t s)
@@ -556,8 +784,8 @@ hipError_t linear_t(const LinearCall &c, char *ws, hipStream_t s)
     e.res_f32 = c.res_dtype == 0;
     e.out_f32 = c.out_dtype == 0;
     e.act = c.act;
-    e.vec = rows_take_4(c.out, c.ldo, e.out_f32 ? 4 : es) &&
-            rows_take_4(c.residual, c.ldr, e.res_f32 ? 4 : es);
+    e.vec = rows_aligned(c.out, c.ldo, e.out_f32 ? 4 : es) &&
+            rows_aligned(c.residual, c.ldr, e.res_f32 ? 4 : es);
     return launch_product<T, false, true>(X, W, c.T, c.n, c.d,
                                           product_of(c.T, c.n, c.d, c.dtype),
                                           reinterpret_cast<float *>(ws + z.part), e, s);
@@ -585,7 +813,7 @@ hipError_t linear_backward_t(const LinearBackwardCall &c, char *ws, hipStream_t 
         e.out = c.dx;
         e.ldo = c.lddx;
         e.out_f32 = es == 4;
-        e.vec = rows_take_4(c.dx, c.lddx, es);
+        e.vec = rows_aligned(c.dx, c.lddx, es);
         rc = launch_product<T, false, false>(D, W, c.T, c.d, c.n,
                                              product_of(c.T, c.d, c.n, c.dtype), part, e, s);
         if (rc != hipSuccess) return rc;
@@ -594,7 +822,7 @@ hipError_t linear_backward_t(const LinearBackwardCall &c, char *ws, hipStream_t 
         e.out = c.dw;
         e.ldo = c.lddw;
         e.out_f32 = c.grad_dtype == 0;
-        e.vec = rows_take_4(c.dw, c.lddw, e.out_f32 ? 4 : es);
+        e.vec = rows_aligned(c.dw, c.lddw, e.out_f32 ? 4 : es);
         rc = launch_product<T, true, true>(X, D, c.d, c.n, c.T,
                                            product_of(c.d, c.n, c.T, c.dtype), part, e, s);
         if (rc != hipSuccess) return rc;

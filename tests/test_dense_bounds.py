@@ -8,32 +8,32 @@ for."""
 import numpy as np
 import pytest
 
-STEP = 128  # bytes of k per step of a row operand
+STEP = 64  # bytes of k per step of a row operand
 
 
 def seg_xor(k, es):
-    return ((k & 3) | ((k >> 1) & 4)) if es == 2 else ((k >> 2) & 3)
+    return (k & 3) << 1 if es == 2 else (k >> 2) & 1
 
 
 def stage(col, es, rows, nth, have, ld, K, k0):
     """LDS chunk -> byte offset from the descriptor's base (or None: zeros), as
     Operand::init / issue compute it; ld in bytes"""
     epc, bk = 16 // es, STEP // es
-    cpr = rows // epc if col else 8
+    cpr = rows // epc if col else STEP // 16
     out = {}
     if col:
         nrow = min(bk, K - k0)
         limit = (nrow - 1) * ld + min(have, rows) * es if nrow > 0 else 0
     else:
         limit = (min(have, rows) - 1) * ld + (K - k0) * es if K > k0 else 0
-    for q in range(rows * 8):
+    for q in range(rows * STEP // 16):
         r, c = q // cpr, q % cpr
         if col:
-            seg = 2 if es == 2 else 4
+            seg = 2 if es == 2 else 8
             lc = ((c // seg) ^ seg_xor(r, es)) * seg + c % seg
             off = r * ld + lc * 16 if lc * epc < have else None
         else:
-            lc = c ^ ((r >> 1) & 7)
+            lc = c ^ ((r >> 1) & 3)
             off = r * ld + lc * 16 if r < have and k0 + lc * epc < K else None
         if off is not None and off >= limit:
             off = None  # past the descriptor: zeros
@@ -45,35 +45,35 @@ def stage(col, es, rows, nth, have, ld, K, k0):
     return out
 
 
-def frag(col, es, rows, first, ks, lane):
-    """LDS (chunk, element) of the fragment's elements, in order"""
+def frag(col, es, rows, i, g, lane):
+    """LDS (chunk, element) of the elements of fragment i (32 rows), k-group g, in order"""
     epc = 16 // es
     if not col:
-        r, c = first + (lane & 15), 4 * ks + (lane >> 4)
-        q = r * 8 + (c ^ ((r >> 1) & 7))
-        return [(q, i) for i in range(epc)]
+        r, c = 32 * i + (lane & 31), 2 * g + (lane >> 5)
+        q = r * 4 + (c ^ ((r >> 1) & 3))
+        return [(q, e) for e in range(epc)]
     got = []
     if es == 2:
-        for i in range(2):
+        for half in range(2):
             for j in range(4):
-                # the transposing load: element j of lane l is element (l & 3)... of the
-                # lane group's row j, column l & 15
+                # the transposing load gives lane l, element j: what lane 4 j + (l & 15) / 4
+                # of its 16 lanes points at, element l & 3
                 src = (lane & ~15) | (4 * j + ((lane & 15) >> 2))
-                k = 32 * ks + 8 * (src >> 4) + 4 * i + ((src >> 2) & 3)
-                seg = (first >> 4) ^ seg_xor(k, es)
-                at = k * rows + seg * 16 + (src & 3) * 4 + (lane & 3)
+                k = 8 * (src >> 5) + ((src >> 2) & 3)
+                seg = (2 * i + ((src >> 4) & 1)) ^ seg_xor(k, es)
+                at = (k + 4 * half + 16 * g) * rows + seg * 16 + (src & 3) * 4 + (lane & 3)
                 got.append((at // 8, at % 8))
     else:
         for j in range(4):
-            k = 16 * ks + 4 * (lane >> 4) + j
-            at = k * rows + ((first >> 4) ^ seg_xor(k, es)) * 16 + (lane & 15)
+            k = 4 * (lane >> 5)
+            at = (k + j + 8 * g) * rows + (i ^ seg_xor(k, es)) * 32 + (lane & 31)
             got.append((at // 4, at % 4))
     return got
 
 
 @pytest.mark.parametrize("col", [False, True])
 @pytest.mark.parametrize("es", [2, 4])
-@pytest.mark.parametrize("rows,nth", [(128, 256), (256, 512)])
+@pytest.mark.parametrize("rows,nth", [(128, 256), (256, 256)])
 @pytest.mark.parametrize("have,K,k0", [(10 ** 6, 10 ** 6, 0), (24, 40, 0), (8, 200, 128),
                                        (10 ** 6, 64, 64), (17, 65, 0), (129, 65, 64), (9, 1, 0)])
 def test_fragments_are_the_elements_they_stand_for(col, es, rows, nth, have, K, k0):
@@ -85,20 +85,44 @@ def test_fragments_are_the_elements_they_stand_for(col, es, rows, nth, have, K, 
         K = -(-K // epc) * epc
     ld = (max(K, 512) if not col else max(min(have, 4096), 512)) * es
     lds = stage(col, es, rows, nth, have, ld, K, k0)
-    for first in range(0, rows, 16):
-        for ks in range(2):
-            for lane in (0, 1, 5, 15, 16, 31, 38, 63):
+    half = bk // 2  # values of k in a group
+    for i in range(rows // 32):
+        for g in range(2):
+            for lane in (0, 1, 5, 15, 16, 31, 32, 38, 49, 63):
                 per = 8 if es == 2 else 4
-                for i, (q, el) in enumerate(frag(col, es, rows, first, ks, lane)):
-                    r = first + (lane & 15)                       # row or column of the tile
-                    k = per * 4 * ks + per * (lane >> 4) + i      # k within the step
+                for e, (q, el) in enumerate(frag(col, es, rows, i, g, lane)):
+                    r = 32 * i + (lane & 31)              # row or column of the tile
+                    k = half * g + per * (lane >> 5) + e  # k within the step
                     off = lds[q]
-                    live = r < have and k0 + k < K
-                    if not live:
-                        # zeros, or (16-byte chunks are whole by construction) never stored
-                        assert off is None or r >= have or k0 + k >= K
-                        if r < have and k0 + k >= K:
-                            assert off is None  # the reduction must see zeros
+                    if r >= have or k0 + k >= K:
+                        assert off is None                # the reduction must see zeros
                         continue
                     want = k * ld + r * es if col else r * ld + k * es
-                    assert off is not None and off + el * es == want, (first, ks, lane, i)
+                    assert off is not None and off + el * es == want, (i, g, lane, e)
+
+
+@pytest.mark.parametrize("es", [2, 4])
+@pytest.mark.parametrize("col", [False, True])
+@pytest.mark.parametrize("rows", [128, 256])
+def test_reads_spread_over_the_banks(col, es, rows):
+    """the lanes that the LDS serves together touch 32-bit banks evenly: 8 lanes of
+    16 bytes (rows), 32 lanes of 8 bytes (columns, 16-bit types), 64 lanes of 4
+    bytes (fp32), each at most once a bank of 64"""
+    for g in range(2):
+        for i in range(rows // 32):
+            if not col:
+                groups = [[r * 64 + (((2 * g + (l >> 5)) ^ ((r >> 1) & 3)) * 16) + 4 * w
+                           for l in range(8 * p, 8 * p + 8) for r in [32 * i + (l & 31)]
+                           for w in range(4)] for p in range(8)]
+            elif es == 2:
+                groups = [[((8 * (l >> 5) + ((l >> 2) & 3) + 16 * g) * rows
+                            + ((2 * i + ((l >> 4) & 1)) ^ seg_xor((l >> 2) & 3, 2)) * 16) * 2
+                           + (l & 3) * 8 + 4 * w
+                           for l in range(32 * p, 32 * p + 32) for w in range(2)] for p in range(2)]
+            else:
+                groups = [[((4 * (l >> 5) + 8 * g) * rows
+                            + (i ^ seg_xor(4 * (l >> 5), 4)) * 32 + (l & 31)) * 4
+                           for l in range(64)]]
+            for at in groups:
+                banks = [(b // 4) % 64 for b in at]
+                assert len(set(banks)) == len(banks)

@@ -76,6 +76,22 @@ def test_linear_sizes(T, d, n, dtype):
     check_linear(T, d, n, dtype, "f32")
 
 
+# enough tiles for the large tile in the forward product, dx and dw (16-bit types)
+LARGE = [(3900, 40, 3100), (3841, 200, 3328), (3900, 3100, 40), (40, 3900, 3100), (333, 3841, 3333)]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("T,d,n", LARGE)
+def test_linear_large(T, d, n, dtype):
+    check_linear(T, d, n, dtype, dtype, "silu", residual="f32")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("T,d,n", LARGE)
+def test_linear_backward_large(T, d, n, dtype):
+    check_backward(T, d, n, dtype, "f32")
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
 @pytest.mark.parametrize("kind", ["none", "relu", "silu", "gelu"])
 @pytest.mark.parametrize("out_f32,residual", [(False, None), (False, "own"), (True, "f32"),
