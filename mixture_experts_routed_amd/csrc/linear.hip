@@ -8,17 +8,20 @@
 //   forward  A = x rows,     B = W columns
 //   dx       A = dz rows,    B = W rows
 //   dw       A = x columns,  B = dz columns
-// A workgroup of 4 wavefronts computes a BM x BN tile in K-steps of 64 bytes of
-// k (32 values of the 16-bit types, 16 of fp32). Five LDS buffers hold the
-// operands of five steps: those of step s + 4 are loaded (straight from memory
-// into LDS, no registers) while the matrix instructions of step s run, on
-// fragments that were read into registers during step s - 1; one barrier a
-// step. The loads are written in assembly so that the compiler does not count
-// them: it would let every LDS read wait for all loads in flight. They have no
-// register result; the kernel waits for them itself, by count.
+// A workgroup of 4 wavefronts computes a BM x BN tile in K-steps of 128 bytes
+// of k (64 values of the 16-bit types, 32 of fp32), whole lines of a row
+// operand. Two LDS buffers hold two steps. A step is four k-groups; the
+// fragments of a group are read into registers three groups before its matrix
+// instructions, so a step's buffer is read out after its first group and its
+// memory loads for the step after next go out from then on (straight into LDS,
+// no registers): they have until the end of the next step's first group, which
+// is where the only barrier of a step stands. The loads are written in
+// assembly so that the compiler does not count them: it would let every LDS
+// read wait for all loads in flight. They have no register result; the kernel
+// waits for them itself.
 // In LDS the 16-byte chunks are permuted so that the reads of a wavefront
 // spread over the banks:
-//   rows:     chunk c of row r (4 chunks, 64 bytes) sits at c ^ ((r >> 1) & 3)
+//   rows:     chunk c of row r (8 chunks, 128 bytes) sits at c ^ ((r >> 1) & 7)
 //   columns:  the columns that a lane group reads together (16 of the 16-bit
 //             types, 32 of fp32) are a segment; segment s of row k sits at
 //             s ^ 2 (k & 3) (fp32: s ^ ((k >> 2) & 1)), so that the rows that are
@@ -44,8 +47,8 @@ namespace moe {
 
 namespace {
 
-constexpr int kStepBytes = 64;  // bytes of k per K-step of a row operand
-constexpr int kBuffers = 5;     // steps whose operands LDS holds
+constexpr int kStepBytes = 128;  // bytes of k per K-step of a row operand
+constexpr int kGroups = 4;       // k-groups of a step
 
 typedef float float16_t __attribute__((ext_vector_type(16)));
 
@@ -289,7 +292,7 @@ struct Operand {
     int left;            // values of k from the current step on
     int kc;              // rows form: the k within a step of this thread's chunks
     uint32_t off[LOADS];
-    uint32_t at[COL ? NF : 1];  // LDS byte of this lane's fragments in a buffer
+    uint32_t at[COL ? NF : kGroups];  // LDS byte of this lane's fragments in a buffer
 
     // K: values of k that the operand holds (rows form: a multiple of EPC); the
     // first step starts at k0
@@ -316,7 +319,7 @@ struct Operand {
                 const int lc = ((c / SEG) ^ seg_xor(r)) * SEG + c % SEG;
                 off[i] = lc * EPC < have ? (uint32_t)r * (uint32_t)ld + (uint32_t)lc * 16u : kOutside;
             } else {
-                const int lc = c ^ ((r >> 1) & 3);  // the same for every i
+                const int lc = c ^ ((r >> 1) & 7);  // the same for every i
                 kc = lc * EPC;
                 off[i] = r < have ? (uint32_t)r * (uint32_t)ld + (uint32_t)lc * 16u +
                                         (uint32_t)((k0 - BK) * ES)
@@ -326,7 +329,9 @@ struct Operand {
         const int lane = tid & 63;
         if (!COL) {
             const int r = frag0 * 32 + (lane & 31);
-            at[0] = (uint32_t)(r * kStepBytes + ((lane >> 5) ^ ((r >> 1) & 3)) * 16);
+#pragma unroll
+            for (int g = 0; g < kGroups; ++g)
+                at[g] = (uint32_t)(r * kStepBytes + ((2 * g + (lane >> 5)) ^ ((r >> 1) & 7)) * 16);
         } else {
 #pragma unroll
             for (int i = 0; i < NF; ++i) {
@@ -363,15 +368,14 @@ struct Operand {
                     rsrc_of(base, bytes));
     }
 
-    // fragment i of this wavefront, k-group g (half a step), from the buffer at L (LDS byte)
+    // fragment i of this wavefront, k-group g, from the buffer at L (LDS byte)
     __device__ __forceinline__ uint4 frag(uint32_t L, int i, int g) const
     {
 #ifdef __HIP_DEVICE_COMPILE__
         if constexpr (!COL) {
-            // chunk 2 g + (l >> 5): the permutation's bit 1 changes with g
             typedef uint32_t u4 __attribute__((ext_vector_type(4)));
             typedef __attribute__((address_space(3))) const u4 *p;
-            const u4 v = ((p)(uintptr_t)(L + (at[0] ^ (uint32_t)(g * 32))))[i * 2 * kStepBytes];
+            const u4 v = ((p)(uintptr_t)(L + at[g]))[i * 2 * kStepBytes];
             return make_uint4(v[0], v[1], v[2], v[3]);
         } else if constexpr (ES == 2) {
             typedef short s4 __attribute__((ext_vector_type(4)));
@@ -403,9 +407,8 @@ __global__ __launch_bounds__(256, (BM + BN > 256 ? 1 : 2)) void k_gemm(const Gem
     typedef Operand<T, BC, BN, NTH, TN> OpB;
     constexpr uint32_t BUF = (BM + BN) * kStepBytes;
     constexpr int LOADS = OpA::LOADS + OpB::LOADS;   // of a thread per step
-    constexpr int LEFT = LOADS * (kBuffers - 3);     // still in flight at a step's end
-    __shared__ uint4 lds[kBuffers * BUF / 16];
-    static_assert(NTH == 256 && LEFT < 64, "4 wavefronts; vmcnt has 6 bits");
+    __shared__ uint4 lds[2 * BUF / 16];
+    static_assert(NTH == 256 && LOADS < 64, "4 wavefronts; vmcnt has 6 bits");
     const int lb = xcd_logical_block(p.mt * p.nt * p.split);
     if (lb < 0) return;  // whole workgroup: no barrier reached
     const int tile = lb / p.split, split = lb - tile * p.split;
@@ -435,37 +438,39 @@ __global__ __launch_bounds__(256, (BM + BN > 256 ? 1 : 2)) void k_gemm(const Gem
             for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
 
     const uint32_t base = lds_at(lds);
-    uint32_t rd = base, wr = base;  // buffers of the step to read and the step to load
-    auto next = [&](uint32_t q) { return q + BUF == base + kBuffers * BUF ? base : q + BUF; };
-    auto load = [&](int i) {
+    auto load = [&](uint32_t to, int i) {
         if (i == 0) a.advance();
         if (i == OpA::LOADS) b.advance();
         // (a resource word may come from a vector instruction: 5 wait states)
         if (i == 0 || i == OpA::LOADS) asm volatile("s_nop 4" ::: "memory");
         if (i < OpA::LOADS)
-            a.issue(wr, i, wave);
+            a.issue(to, i, wave);
         else
-            b.issue(wr + OpA::BYTES, i - OpA::LOADS, wave);
-        if (i == LOADS - 1) wr = next(wr);
+            b.issue(to + OpA::BYTES, i - OpA::LOADS, wave);
     };
-    // fragments of the two k-groups of a step: those of one are read while the
-    // matrix instructions of the other run, in the order in which they are needed
-    uint4 fa[2][TM], fb[2][TN];
-    auto read = [&](int g, int q) {
+    // fragments of the four k-groups, read in the order in which they are needed
+    uint4 fa[kGroups][TM], fb[kGroups][TN];
+    auto read = [&](uint32_t from, int g, int q) {
         if (q == 0 || q > TN)
-            fa[g][q == 0 ? 0 : q - TN] = a.frag(rd, q == 0 ? 0 : q - TN, g);
+            fa[g][q == 0 ? 0 : q - TN] = a.frag(from, q == 0 ? 0 : q - TN, g);
         else
-            fb[g][q - 1] = b.frag(rd + OpA::BYTES, q - 1, g);
+            fb[g][q - 1] = b.frag(from + OpA::BYTES, q - 1, g);
     };
-    // matrix instructions of k-group g, between them the fragments of the other
-    // group and half of the loads of step s + 4
-    constexpr int GAP = TM * TN / (TM + TN), HALF = LOADS / 2;
-    static_assert(GAP * (TM + TN) == TM * TN && HALF * 2 == LOADS && HALF * 4 <= TM * TN * 2, "");
-    auto group = [&](int g) {
+    // matrix instructions of k-group g; between them the fragments of the group
+    // three further on, from the buffer `from`, and, in groups 1 and 2, the
+    // loads of the step after next
+    constexpr int MMAS = TM * TN, GAP = MMAS / (TM + TN), LGROUPS = 2;
+    static_assert(GAP * (TM + TN) == MMAS && LOADS <= LGROUPS * MMAS * 2, "");
+    auto group = [&](int g, uint32_t from, uint32_t to) {
 #pragma unroll
-        for (int q = 0; q < TM * TN; ++q) {
-            if (q % GAP == 0) read(1 - g, q / GAP);
-            if (q % (TM * TN / HALF) == 0) load(g * HALF + q / (TM * TN / HALF));
+        for (int q = 0; q < MMAS; ++q) {
+            if (q % GAP == 0) read(from, (g + 3) % kGroups, q / GAP);
+            if (g >= 1 && g <= LGROUPS) {
+                const int at = (g - 1) * MMAS + q;
+#pragma unroll
+                for (int i = at * LOADS / (LGROUPS * MMAS); i < (at + 1) * LOADS / (LGROUPS * MMAS); ++i)
+                    load(to, i);
+            }
             if constexpr (BIG)
                 Mma<T>::in_place(fb[g][q % TN], fa[g][q / TN], acc[q / TN][q % TN]);
             else
@@ -475,24 +480,28 @@ __global__ __launch_bounds__(256, (BM + BN > 256 ? 1 : 2)) void k_gemm(const Gem
     };
     if (s0 < s1) {
 #pragma unroll
-        for (int q = 0; q < kBuffers - 1; ++q)
+        for (int i = 0; i < LOADS; ++i) load(base, i);
 #pragma unroll
-            for (int i = 0; i < LOADS; ++i) load(i);
-        asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" : : "n"(LEFT) : "memory");
+        for (int i = 0; i < LOADS; ++i) load(base + BUF, i);
+        asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" : : "n"(LOADS) : "memory");
 #pragma unroll
-        for (int q = 0; q < TM + TN; ++q) read(0, q);
-        // Group 0 reads group 1 of its step, group 1 reads group 0 of the next.
-        // At a step's end this wavefront's loads of step s + 2 have landed, and
-        // with the barrier everyone's. The buffer that is loaded during step s
-        // was last read in group 0 of step s - 1, by reads that the matrix
-        // instructions of its group 1 waited for, before its barrier. A step
-        // past the end of k reads zeros.
+        for (int g = 0; g < 3; ++g)
+#pragma unroll
+            for (int q = 0; q < TM + TN; ++q) read(base, g, q);
+        uint32_t cur = base, other = base + BUF;
+        // A step past the end of k reads zeros.
         for (int s = s0; s < s1; ++s) {
-            group(0);
-            rd = next(rd);
-            group(1);
-            asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" : : "n"(LEFT) : "memory");
+            group(0, cur, 0);
+            // this step's buffer is read out by this wavefront and the next step's
+            // loads have landed; with the barrier, by and for everyone
+            asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
             __builtin_amdgcn_sched_barrier(0);
+            group(1, other, cur);
+            group(2, other, cur);
+            group(3, other, cur);
+            const uint32_t c = cur;
+            cur = other;
+            other = c;
         }
         // nothing in flight into LDS, and every wavefront done with it; the last
         // matrix results readable
@@ -525,10 +534,10 @@ __global__ __launch_bounds__(256, (BM + BN > 256 ? 1 : 2)) void k_gemm(const Gem
         }
         return;
     }
-    // Each wavefront's own part of LDS holds 64 of its rows; rows are padded by
+    // Each wavefront's own part of LDS holds 32 of its rows; rows are padded by
     // 4 floats, which spreads the rows of a store over the banks.
-    constexpr int COLS = TN * 32, PITCH = COLS + 4, RG = 2, LPR = COLS / 8;
-    static_assert(RG * 32 * PITCH * 4 * 4 <= (int)(kBuffers * BUF) && TM % RG == 0, "fits");
+    constexpr int COLS = TN * 32, PITCH = COLS + 4, RG = 1, LPR = COLS / 8;
+    static_assert(RG * 32 * PITCH * 4 * 4 <= (int)(2 * BUF) && TM % RG == 0, "fits");
     float *mine = reinterpret_cast<float *>(lds) + wave * (RG * 32 * PITCH);
 #pragma unroll
     for (int h = 0; h < TM; h += RG) {
@@ -648,7 +657,7 @@ __global__ __launch_bounds__(256) void k_colsum_join(const float *__restrict__ p
 // ---- host side ---------------------------------------------------------------
 
 constexpr int kSlots = 512;       // workgroups of a 128 x 128 tile that the GPU holds at once
-constexpr int kMinSplitSteps = 8;
+constexpr int kMinSplitSteps = 4;
 
 int elem_size(int dtype) { return dtype == 0 ? 4 : 2; }
 int64_t up(int64_t v, int64_t a) { return (v + a - 1) / a * a; }

@@ -8,7 +8,7 @@ for."""
 import numpy as np
 import pytest
 
-STEP = 64  # bytes of k per step of a row operand
+STEP = 128  # bytes of k per step of a row operand
 
 
 def seg_xor(k, es):
@@ -33,7 +33,7 @@ def stage(col, es, rows, nth, have, ld, K, k0):
             lc = ((c // seg) ^ seg_xor(r, es)) * seg + c % seg
             off = r * ld + lc * 16 if lc * epc < have else None
         else:
-            lc = c ^ ((r >> 1) & 3)
+            lc = c ^ ((r >> 1) & 7)
             off = r * ld + lc * 16 if r < have and k0 + lc * epc < K else None
         if off is not None and off >= limit:
             off = None  # past the descriptor: zeros
@@ -50,7 +50,7 @@ def frag(col, es, rows, i, g, lane):
     epc = 16 // es
     if not col:
         r, c = 32 * i + (lane & 31), 2 * g + (lane >> 5)
-        q = r * 4 + (c ^ ((r >> 1) & 3))
+        q = r * 8 + (c ^ ((r >> 1) & 7))
         return [(q, e) for e in range(epc)]
     got = []
     if es == 2:
@@ -85,14 +85,14 @@ def test_fragments_are_the_elements_they_stand_for(col, es, rows, nth, have, K, 
         K = -(-K // epc) * epc
     ld = (max(K, 512) if not col else max(min(have, 4096), 512)) * es
     lds = stage(col, es, rows, nth, have, ld, K, k0)
-    half = bk // 2  # values of k in a group
+    size = bk // 4  # values of k in a group
     for i in range(rows // 32):
-        for g in range(2):
+        for g in range(4):
             for lane in (0, 1, 5, 15, 16, 31, 32, 38, 49, 63):
                 per = 8 if es == 2 else 4
                 for e, (q, el) in enumerate(frag(col, es, rows, i, g, lane)):
                     r = 32 * i + (lane & 31)              # row or column of the tile
-                    k = half * g + per * (lane >> 5) + e  # k within the step
+                    k = size * g + per * (lane >> 5) + e  # k within the step
                     off = lds[q]
                     if r >= have or k0 + k >= K:
                         assert off is None                # the reduction must see zeros
@@ -108,10 +108,10 @@ def test_reads_spread_over_the_banks(col, es, rows):
     """the lanes that the LDS serves together touch 32-bit banks evenly: 8 lanes of
     16 bytes (rows), 32 lanes of 8 bytes (columns, 16-bit types), 64 lanes of 4
     bytes (fp32), each at most once a bank of 64"""
-    for g in range(2):
+    for g in range(4):
         for i in range(rows // 32):
             if not col:
-                groups = [[r * 64 + (((2 * g + (l >> 5)) ^ ((r >> 1) & 3)) * 16) + 4 * w
+                groups = [[r * 128 + (((2 * g + (l >> 5)) ^ ((r >> 1) & 7)) * 16) + 4 * w
                            for l in range(8 * p, 8 * p + 8) for r in [32 * i + (l & 31)]
                            for w in range(4)] for p in range(8)]
             elif es == 2:
