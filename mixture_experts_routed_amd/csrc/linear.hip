@@ -10,15 +10,16 @@
 //   dw       A = x columns,  B = dz columns
 // A workgroup of 4 wavefronts computes a BM x BN tile in K-steps of 128 bytes
 // of k (64 values of the 16-bit types, 32 of fp32), whole lines of a row
-// operand. Two LDS buffers hold two steps. A step is four k-groups; the
-// fragments of a group are read into registers three groups before its matrix
-// instructions, so a step's buffer is read out after its first group and its
-// memory loads for the step after next go out from then on (straight into LDS,
-// no registers): they have until the end of the next step's first group, which
-// is where the only barrier of a step stands. The loads are written in
-// assembly so that the compiler does not count them: it would let every LDS
-// read wait for all loads in flight. They have no register result; the kernel
-// waits for them itself.
+// operand. LDS holds three steps of A and two of B. A step is four k-groups;
+// the fragments of a group are read into registers three groups before its
+// matrix instructions, so a step's buffers are read out after its first group,
+// and from then on the memory loads of B's step after next and of A's third
+// step on go out into them (straight into LDS, no registers). They have until
+// the end of the next step's (A: the one after it) first group, which is where
+// the only barrier of a step stands. The loads are written in assembly so that
+// the compiler does not count them: it would let every LDS read wait for all
+// loads in flight. They have no register result; the kernel waits for them
+// itself.
 // In LDS the 16-byte chunks are permuted so that the reads of a wavefront
 // spread over the banks:
 //   rows:     chunk c of row r (8 chunks, 128 bytes) sits at c ^ ((r >> 1) & 7)
@@ -405,10 +406,9 @@ __global__ __launch_bounds__(256, (BM + BN > 256 ? 1 : 2)) void k_gemm(const Gem
     constexpr bool BIG = TM * TN == 16;  // accumulators take all accumulation registers
     typedef Operand<T, AC, BM, NTH, TM> OpA;
     typedef Operand<T, BC, BN, NTH, TN> OpB;
-    constexpr uint32_t BUF = (BM + BN) * kStepBytes;
-    constexpr int LOADS = OpA::LOADS + OpB::LOADS;   // of a thread per step
-    __shared__ uint4 lds[2 * BUF / 16];
-    static_assert(NTH == 256 && LOADS < 64, "4 wavefronts; vmcnt has 6 bits");
+    constexpr uint32_t LDS_BYTES = 3 * OpA::BYTES + 2 * OpB::BYTES;
+    __shared__ uint4 lds[LDS_BYTES / 16];
+    static_assert(NTH == 256 && 3 * OpA::LOADS + 2 * OpB::LOADS < 64, "4 wavefronts; vmcnt has 6 bits");
     const int lb = xcd_logical_block(p.mt * p.nt * p.split);
     if (lb < 0) return;  // whole workgroup: no barrier reached
     const int tile = lb / p.split, split = lb - tile * p.split;
@@ -437,39 +437,49 @@ __global__ __launch_bounds__(256, (BM + BN > 256 ? 1 : 2)) void k_gemm(const Gem
 #pragma unroll
             for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
 
-    const uint32_t base = lds_at(lds);
-    auto load = [&](uint32_t to, int i) {
-        if (i == 0) a.advance();
-        if (i == OpA::LOADS) b.advance();
-        // (a resource word may come from a vector instruction: 5 wait states)
-        if (i == 0 || i == OpA::LOADS) asm volatile("s_nop 4" ::: "memory");
-        if (i < OpA::LOADS)
-            a.issue(to, i, wave);
-        else
-            b.issue(to + OpA::BYTES, i - OpA::LOADS, wave);
+    // LDS: three steps of A, then two of B
+    const uint32_t base = lds_at(lds), base_b = base + 3 * OpA::BYTES;
+    // (a resource word may come from a vector instruction: 5 wait states)
+    auto load_a = [&](uint32_t to, int i) {
+        if (i == 0) {
+            a.advance();
+            asm volatile("s_nop 4" ::: "memory");
+        }
+        a.issue(to, i, wave);
+    };
+    auto load_b = [&](uint32_t to, int i) {
+        if (i == 0) {
+            b.advance();
+            asm volatile("s_nop 4" ::: "memory");
+        }
+        b.issue(to, i, wave);
     };
     // fragments of the four k-groups, read in the order in which they are needed
     uint4 fa[kGroups][TM], fb[kGroups][TN];
-    auto read = [&](uint32_t from, int g, int q) {
+    auto read = [&](uint32_t la, uint32_t lb_, int g, int q) {
         if (q == 0 || q > TN)
-            fa[g][q == 0 ? 0 : q - TN] = a.frag(from, q == 0 ? 0 : q - TN, g);
+            fa[g][q == 0 ? 0 : q - TN] = a.frag(la, q == 0 ? 0 : q - TN, g);
         else
-            fb[g][q - 1] = b.frag(from + OpA::BYTES, q - 1, g);
+            fb[g][q - 1] = b.frag(lb_, q - 1, g);
     };
     // matrix instructions of k-group g; between them the fragments of the group
-    // three further on, from the buffer `from`, and, in groups 1 and 2, the
-    // loads of the step after next
-    constexpr int MMAS = TM * TN, GAP = MMAS / (TM + TN), LGROUPS = 2;
-    static_assert(GAP * (TM + TN) == MMAS && LOADS <= LGROUPS * MMAS * 2, "");
-    auto group = [&](int g, uint32_t from, uint32_t to) {
+    // three further on, from la and lb_, and the memory loads: B's of the step
+    // after next in group 1, A's of the third step on in groups 2 and 3
+    constexpr int MMAS = TM * TN, GAP = MMAS / (TM + TN);
+    static_assert(GAP * (TM + TN) == MMAS, "");
+    auto group = [&](int g, uint32_t la, uint32_t lb_, uint32_t ta, uint32_t tb) {
 #pragma unroll
         for (int q = 0; q < MMAS; ++q) {
-            if (q % GAP == 0) read(from, (g + 3) % kGroups, q / GAP);
-            if (g >= 1 && g <= LGROUPS) {
-                const int at = (g - 1) * MMAS + q;
+            if (q % GAP == 0) read(la, lb_, (g + 3) % kGroups, q / GAP);
+            if (g == 1)
 #pragma unroll
-                for (int i = at * LOADS / (LGROUPS * MMAS); i < (at + 1) * LOADS / (LGROUPS * MMAS); ++i)
-                    load(to, i);
+                for (int i = q * OpB::LOADS / MMAS; i < (q + 1) * OpB::LOADS / MMAS; ++i)
+                    load_b(tb, i);
+            if (g >= 2) {
+                const int at = (g - 2) * MMAS + q;
+#pragma unroll
+                for (int i = at * OpA::LOADS / (2 * MMAS); i < (at + 1) * OpA::LOADS / (2 * MMAS); ++i)
+                    load_a(ta, i);
             }
             if constexpr (BIG)
                 Mma<T>::in_place(fb[g][q % TN], fa[g][q / TN], acc[q / TN][q % TN]);
@@ -479,29 +489,45 @@ __global__ __launch_bounds__(256, (BM + BN > 256 ? 1 : 2)) void k_gemm(const Gem
         }
     };
     if (s0 < s1) {
+        auto all_a = [&](uint32_t to) {
 #pragma unroll
-        for (int i = 0; i < LOADS; ++i) load(base, i);
+            for (int i = 0; i < OpA::LOADS; ++i) load_a(to, i);
+        };
+        auto all_b = [&](uint32_t to) {
 #pragma unroll
-        for (int i = 0; i < LOADS; ++i) load(base + BUF, i);
-        asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" : : "n"(LOADS) : "memory");
+            for (int i = 0; i < OpB::LOADS; ++i) load_b(to, i);
+        };
+        all_a(base);
+        all_b(base_b);
+        all_a(base + OpA::BYTES);
+        all_b(base_b + OpB::BYTES);
+        all_a(base + 2 * OpA::BYTES);
+        asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier"
+                     :
+                     : "n"(2 * OpA::LOADS + OpB::LOADS)
+                     : "memory");
 #pragma unroll
         for (int g = 0; g < 3; ++g)
 #pragma unroll
-            for (int q = 0; q < TM + TN; ++q) read(base, g, q);
-        uint32_t cur = base, other = base + BUF;
+            for (int q = 0; q < TM + TN; ++q) read(base, base_b, g, q);
+        uint32_t a0 = base, a1 = base + OpA::BYTES, a2 = base + 2 * OpA::BYTES;
+        uint32_t b0 = base_b, b1 = base_b + OpB::BYTES;
         // A step past the end of k reads zeros.
         for (int s = s0; s < s1; ++s) {
-            group(0, cur, 0);
-            // this step's buffer is read out by this wavefront and the next step's
-            // loads have landed; with the barrier, by and for everyone
-            asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+            group(0, a0, b0, 0, 0);
+            // this step's buffers are read out by this wavefront, and all loads but
+            // those of A two steps on have landed; with the barrier, by and for everyone
+            asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" : : "n"(OpA::LOADS) : "memory");
             __builtin_amdgcn_sched_barrier(0);
-            group(1, other, cur);
-            group(2, other, cur);
-            group(3, other, cur);
-            const uint32_t c = cur;
-            cur = other;
-            other = c;
+            group(1, a1, b1, a0, b0);
+            group(2, a1, b1, a0, b0);
+            group(3, a1, b1, a0, b0);
+            const uint32_t x = a0, y = b0;
+            a0 = a1;
+            a1 = a2;
+            a2 = x;
+            b0 = b1;
+            b1 = y;
         }
         // nothing in flight into LDS, and every wavefront done with it; the last
         // matrix results readable
@@ -537,7 +563,7 @@ __global__ __launch_bounds__(256, (BM + BN > 256 ? 1 : 2)) void k_gemm(const Gem
     // Each wavefront's own part of LDS holds 32 of its rows; rows are padded by
     // 4 floats, which spreads the rows of a store over the banks.
     constexpr int COLS = TN * 32, PITCH = COLS + 4, RG = 1, LPR = COLS / 8;
-    static_assert(RG * 32 * PITCH * 4 * 4 <= (int)(2 * BUF) && TM % RG == 0, "fits");
+    static_assert(RG * 32 * PITCH * 4 * 4 <= (int)LDS_BYTES && TM % RG == 0, "fits");
     float *mine = reinterpret_cast<float *>(lds) + wave * (RG * 32 * PITCH);
 #pragma unroll
     for (int h = 0; h < TM; h += RG) {
@@ -553,7 +579,7 @@ __global__ __launch_bounds__(256, (BM + BN > 256 ? 1 : 2)) void k_gemm(const Gem
                         float4_t{c[4 * q], c[4 * q + 1], c[4 * q + 2], c[4 * q + 3]};
                 }
         // (LDS operations of one wavefront stay in order)
-#pragma unroll 1
+#pragma unroll 2
         for (int r = lane / LPR; r < RG * 32; r += 64 / LPR) {
             const int m = row0 + h * 32 + r, n = col0 + (lane % LPR) * 8;
             if (m >= p.M || n >= p.N) continue;
@@ -612,42 +638,68 @@ __global__ __launch_bounds__(256) void k_pad_rows(const U *__restrict__ src, int
     }
 }
 
-// Column sums of dz [T][n] over the rows [b * per, (b + 1) * per), b =
-// blockIdx.y, into part [gridDim.y][n] (or, with one block of rows, straight
-// into db). A workgroup covers 64 columns; its 4 wavefronts take every fourth
-// row and are added in order through LDS.
-template <typename T>
+// Column sums of dz [rows][n]: a workgroup adds `per` rows from blockIdx.y * per
+// on, over 256 columns: 32 threads of 8 columns, 8 of every 8th row, joined in
+// order through LDS. Its sums go to part [gridDim.y][n], or with one block of
+// rows straight into db. VEC: rows are whole 16-byte chunks.
+constexpr int kSumCols = 256;
+template <typename T, bool VEC>
 __global__ __launch_bounds__(256) void k_colsum(const T *__restrict__ dz, int64_t ld, int rows,
                                                 int n, int per, float *__restrict__ part,
                                                 void *__restrict__ db, int db_f32)
 {
-    __shared__ float s[4][64];
-    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-    const int c = blockIdx.x * 64 + lane;
-    const int r0 = blockIdx.y * per, r1 = min(rows, r0 + per);
-    float v = 0.f;
+    __shared__ float s[8][kSumCols];
+    const int cg = threadIdx.x & 31, rg = threadIdx.x >> 5;
+    const int c = blockIdx.x * kSumCols + cg * 8;
+    const int64_t r0 = (int64_t)blockIdx.y * per, r1 = r0 + per < rows ? r0 + per : rows;
+    float v[8] = {};
     if (c < n)
-        for (int r = r0 + w; r < r1; r += 4) v += to_f32(dz[(int64_t)r * ld + c]);
-    s[w][lane] = v;
+#pragma unroll 4
+        for (int64_t r = r0 + rg; r < r1; r += 8) {
+            const T *p = dz + r * ld + c;
+            float q[8];
+            if (VEC) {
+                load8<T>(p, q);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) q[i] = c + i < n ? to_f32(p[i]) : 0.f;
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] += q[i];
+        }
+    store8<float>(&s[rg][cg * 8], v);
     __syncthreads();
-    if (w || c >= n) return;
-    v = ((s[0][lane] + s[1][lane]) + s[2][lane]) + s[3][lane];
+    const int m = blockIdx.x * kSumCols + threadIdx.x;
+    if (m >= n) return;
+    float t = 0.f;
+#pragma unroll
+    for (int q = 0; q < 8; ++q) t += s[q][threadIdx.x];
     if (gridDim.y > 1)
-        part[(int64_t)blockIdx.y * n + c] = v;
+        part[(int64_t)blockIdx.y * n + m] = t;
     else if (db_f32)
-        static_cast<float *>(db)[c] = v;
+        static_cast<float *>(db)[m] = t;
     else
-        static_cast<T *>(db)[c] = from_f32<T>(v);
+        static_cast<T *>(db)[m] = from_f32<T>(t);
 }
 
+// the blocks' sums added: 32 columns a workgroup, 8 threads each
 template <typename T>
 __global__ __launch_bounds__(256) void k_colsum_join(const float *__restrict__ part, int blocks,
                                                      int n, void *__restrict__ db, int db_f32)
 {
-    const int c = blockIdx.x * 256 + threadIdx.x;
-    if (c >= n) return;
+    __shared__ float s[8][32];
+    const int cg = threadIdx.x & 31, bg = threadIdx.x >> 5;
+    const int c = blockIdx.x * 32 + cg;
     float v = 0.f;
-    for (int b = 0; b < blocks; ++b) v += part[(int64_t)b * n + c];
+    if (c < n)
+#pragma unroll 8
+        for (int b = bg; b < blocks; b += 8) v += part[(int64_t)b * n + c];
+    s[bg][cg] = v;
+    __syncthreads();
+    if (bg || c >= n) return;
+    v = 0.f;
+#pragma unroll
+    for (int q = 0; q < 8; ++q) v += s[q][cg];
     if (db_f32)
         static_cast<float *>(db)[c] = v;
     else
@@ -670,11 +722,23 @@ struct Product {
     int64_t part_bytes;
 };
 
+// 256 x 256 tiles where, cut along k into splits of at least 16 steps, they
+// occupy three quarters of the 256 CUs (one workgroup each): 2,048 x 4,096
+// outputs over 32,768 values of k take 427 us in 128 tiles cut in two against
+// 563 us in 512 tiles of 128 x 128; over 8,192, both take 124 us
+bool tiles256_fill(int64_t M, int64_t N, int64_t steps)
+{
+    const int64_t t = div_up(M, 256) * div_up(N, 256);
+    const int64_t s = t < 256 ? 256 / t : 1;
+    const int64_t most = steps / 16 > 1 ? steps / 16 : 1;
+    return t * (s < most ? s : most) >= 192;
+}
+
 Product product_of(int64_t M, int64_t N, int64_t K, int dtype)
 {
     Product z;
     const int64_t steps = div_up(K, kStepBytes / elem_size(dtype));
-    z.tile = dtype != 0 && div_up(M, 256) * div_up(N, 256) >= 192 ? 256 : 128;
+    z.tile = dtype != 0 && tiles256_fill(M, N, steps) ? 256 : 128;
     z.mt = div_up(M, z.tile);
     z.nt = div_up(N, z.tile);
     int64_t s = (z.tile == 256 ? kSlots / 2 : kSlots) / (z.mt * z.nt);
@@ -838,11 +902,13 @@ hipError_t linear_backward_t(const LinearBackwardCall &c, char *ws, hipStream_t 
     }
     if (c.db) {
         const int blocks = z.db_blocks, per = (int)div_up(c.T, blocks);
-        hipLaunchKernelGGL(k_colsum<T>, dim3((c.n + 63) / 64, blocks), dim3(256), 0, s,
-                           static_cast<const T *>(c.dz), c.lddz, c.T, c.n, per, part, c.db,
-                           c.grad_dtype == 0 ? 1 : 0);
+        const bool vec = !padded(c.T, c.n, c.lddz, c.dtype).copy;
+        const dim3 grid((c.n + kSumCols - 1) / kSumCols, blocks);
+        auto sum = vec ? k_colsum<T, true> : k_colsum<T, false>;
+        hipLaunchKernelGGL(sum, grid, dim3(256), 0, s, static_cast<const T *>(c.dz), c.lddz, c.T,
+                           c.n, per, part, c.db, c.grad_dtype == 0 ? 1 : 0);
         if (blocks > 1)
-            hipLaunchKernelGGL(k_colsum_join<T>, dim3((c.n + 255) / 256), dim3(256), 0, s, part,
+            hipLaunchKernelGGL(k_colsum_join<T>, dim3((c.n + 31) / 32), dim3(256), 0, s, part,
                                blocks, c.n, c.db, c.grad_dtype == 0 ? 1 : 0);
     }
     return hipGetLastError();
@@ -872,9 +938,8 @@ LinearBackwardSpace linear_backward_space(int T, int d, int n, int64_t ldx, int6
     auto need = [&](int64_t b) { most = b > most ? b : most; };
     if (dx) need(product_of(T, d, n, dtype).part_bytes);
     if (dw) need(product_of(d, n, T, dtype).part_bytes);
-    // rows of dz per workgroup of the column sums: at least 64
-    const int64_t want = 1024 / div_up(n, 64);
-    const int64_t most_blocks = div_up(T, 64);
+    // the column sums: about 512 workgroups, of at least 64 rows
+    const int64_t want = 512 / div_up(n, kSumCols), most_blocks = div_up(T, 64);
     z.db_blocks = (int)(want < 1 ? 1 : want < most_blocks ? want : most_blocks);
     if (db && z.db_blocks > 1) need(up((int64_t)z.db_blocks * n * 4, 256));
     z.total = z.part + most;
