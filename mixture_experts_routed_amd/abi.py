@@ -12,6 +12,7 @@ the call raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -138,32 +139,37 @@ def _dev(t, name):
     return t.data_ptr()
 
 
-def _mat(t, name, shape=None, dtype=None):
-    """(device address, row stride) of a row-major GPU matrix [R, C]; (None, 0) for None"""
+def _mat(t, name, dev, rows, cols, dtype, other=None):
+    """(device address, row stride) of a row-major matrix [rows, cols] of dtype (or
+    `other`) on GPU `dev`; (None, 0) for None"""
     if t is None:
         return None, 0
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name}: expected a GPU tensor")
-    if t.dim() != 2 or (shape is not None and tuple(t.shape) != tuple(shape)):
-        raise ValueError(f"{name}: expected a matrix{'' if shape is None else ' ' + str(tuple(shape))}, "
-                         f"got {tuple(t.shape)}")
-    if dtype is not None and t.dtype not in (dtype if isinstance(dtype, tuple) else (dtype,)):
-        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
-    rows, cols = t.shape
-    if cols > 1 and t.stride(1) != 1:
+    if t.get_device() != dev:
+        raise ValueError(f"{name}: on {t.device}, expected GPU {dev}")
+    if t.dtype is not dtype and (other is None or t.dtype is not other):
+        raise TypeError(f"{name}: expected {dtype}{f' or {other}' if other else ''}, got {t.dtype}")
+    if t.shape != (rows, cols):
+        raise ValueError(f"{name}: expected {(rows, cols)}, got {tuple(t.shape)}")
+    s0, s1 = t.stride()
+    if s1 != 1 and cols > 1:
         raise ValueError(f"{name}: expected contiguous rows")
-    ld = t.stride(0) if rows > 1 else max(cols, 1)
-    if ld < cols:
+    if rows <= 1:
+        s0 = cols
+    elif s0 < cols:
         raise ValueError(f"{name}: overlapping rows")
-    return t.data_ptr(), ld
+    return t.data_ptr(), s0
 
 
-def _vec(t, name, n, dtype):
-    """device address of a contiguous GPU array of n elements (or None)"""
+def _vec(t, name, dev, n, dtype):
+    """device address of a contiguous array of n elements of dtype on GPU `dev` (or None)"""
     if t is None:
         return None
     p = _dev(t, name)
-    if t.numel() != n or t.dtype != dtype:
+    if t.get_device() != dev:
+        raise ValueError(f"{name}: on {t.device}, expected GPU {dev}")
+    if t.numel() != n or t.dtype is not dtype:
         raise ValueError(f"{name}: expected {n} elements of {dtype}, got {tuple(t.shape)} {t.dtype}")
     return p
 
@@ -471,6 +477,7 @@ def forward_host(x, ids, w, hw_gate, hw_up, hw_down, tm: int = 16, packed: bool 
 
 # ---------------------------------------------- dense operators (C entry points) --
 
+@functools.lru_cache(maxsize=1024)
 def moe_linear_workspace(T: int, d: int, n: int, ldx: int, ldw: int, dtype: int) -> int:
     v = ctypes.c_size_t()
     _check("moe_linear_workspace",
@@ -478,6 +485,7 @@ def moe_linear_workspace(T: int, d: int, n: int, ldx: int, ldw: int, dtype: int)
     return v.value
 
 
+@functools.lru_cache(maxsize=1024)
 def moe_linear_backward_workspace(T, d, n, ldx, ldw, lddz, dtype: int, grads: int) -> int:
     v = ctypes.c_size_t()
     _check("moe_linear_backward_workspace",
@@ -486,6 +494,7 @@ def moe_linear_backward_workspace(T, d, n, ldx, ldw, lddz, dtype: int, grads: in
     return v.value
 
 
+@functools.lru_cache(maxsize=1024)
 def moe_balance_workspace(T: int, E: int, K: int) -> int:
     v = ctypes.c_size_t()
     _check("moe_balance_workspace", lib().moe_balance_workspace(T, E, K, ctypes.byref(v)))
@@ -497,72 +506,77 @@ def moe_balance_workspace(T: int, E: int, K: int) -> int:
 # kernels run on, and launch on the tensors' device. `workspace` may be kept
 # from call to call; it is replaced when it is too small.
 
-class _Launch:
-    """Stream, device and workspace of one call whose tensors lie on t's device."""
+class _On:
+    """Device and stream of one call: the tensors' device made current, `handle` the
+    stream to launch on. empty() allocates on that stream."""
+    __slots__ = ("index", "handle", "stream", "before")
 
-    def __init__(self, t, stream):
+    def __init__(self, t, name, stream):
         if not isinstance(t, torch.Tensor) or not t.is_cuda:
-            raise TypeError("expected a GPU tensor")
-        self.device, self.stream, self.on = t.device, stream, None
-        if t.device.index != torch.cuda.current_device():
-            self.on = torch.cuda.device(t.device)
+            raise TypeError(f"{name}: expected a GPU tensor")
+        self.index, self.stream, self.before = t.get_device(), stream, -1
 
     def __enter__(self):
-        if self.on is not None:
-            self.on.__enter__()
-        if self.stream is None:
-            self.torch_stream = None
-            self.handle = torch.cuda.current_stream().cuda_stream
-        else:
-            self.handle = _stream(self.stream)
-            self.torch_stream = (self.stream if hasattr(self.stream, "cuda_stream")
-                                 else torch.cuda.ExternalStream(self.handle))
+        if self.index != torch._C._cuda_getDevice():
+            self.before = torch._C._cuda_getDevice()
+            torch.cuda.set_device(self.index)
+        self.handle = (torch._C._cuda_getCurrentRawStream(self.index) if self.stream is None
+                       else _stream(self.stream))
         return self
 
     def __exit__(self, *exc):
-        if self.on is not None:
-            self.on.__exit__(*exc)
-
-    def same(self, **tensors):
-        """the tensors that are given lie on this call's device"""
-        for name, t in tensors.items():
-            if t is not None and t.device != self.device:
-                raise ValueError(f"{name}: on {t.device}, expected {self.device}")
+        if self.before >= 0:
+            torch.cuda.set_device(self.before)
 
     def empty(self, shape, dtype):
-        if self.torch_stream is None:
-            return torch.empty(shape, dtype=dtype, device=self.device)
-        with torch.cuda.stream(self.torch_stream):
-            return torch.empty(shape, dtype=dtype, device=self.device)
+        if self.stream is None:
+            return torch.empty(shape, dtype=dtype, device=torch.device("cuda", self.index))
+        s = (self.stream if hasattr(self.stream, "cuda_stream")
+             else torch.cuda.ExternalStream(self.handle))
+        with torch.cuda.stream(s):
+            return torch.empty(shape, dtype=dtype, device=torch.device("cuda", self.index))
 
     def workspace(self, given, need):
-        if given is not None and given.numel() * given.element_size() >= need:
-            return given
-        return self.empty((need,), torch.uint8)
+        """(the tensor, its address, its bytes)"""
+        if given is not None:
+            p, have = _dev(given, "workspace"), given.numel() * given.element_size()
+            if given.get_device() != self.index:
+                raise ValueError(f"workspace: on {given.device}, expected GPU {self.index}")
+            if have >= need:
+                return given, p, have
+        given = self.empty((need,), torch.uint8)
+        return given, given.data_ptr(), need
+
+
+def _matrix_shape(t, name):
+    if t.dim() != 2:
+        raise ValueError(f"{name}: expected a matrix, got {tuple(t.shape)}")
+    return t.shape
 
 
 def linear(x, w, bias=None, residual=None, act: str = "none", out_dtype=None, workspace=None,
            out=None, stream=None):
     """out = act(x w + bias) + residual for x [T, d], w [d, n] of one type, in out_dtype
     (x's type, or torch.float32); returns (out, workspace). residual may be out itself."""
-    dtype = DTYPE_OF[x.dtype]
-    (T, d), n = x.shape, w.shape[1]
-    with _Launch(x, stream) as at:
-        at.same(w=w, bias=bias, residual=residual, out=out, workspace=workspace)
-        px, ldx = _mat(x, "x")
-        pw, ldw = _mat(w, "w", (d, n), x.dtype)
-        pr, ldr = _mat(residual, "residual", (T, n), (x.dtype, torch.float32))
+    with _On(x, "x", stream) as at:
+        dev, D = at.index, x.dtype
+        T, d = _matrix_shape(x, "x")
+        n = _matrix_shape(w, "w")[1]
         if out is None:
-            out = at.empty((T, n), out_dtype or x.dtype)
-        elif out_dtype is not None and out.dtype != out_dtype:
+            out = at.empty((T, n), out_dtype or D)
+        elif out_dtype is not None and out.dtype is not out_dtype:
             raise TypeError(f"out: expected {out_dtype}, got {out.dtype}")
-        po, ldo = _mat(out, "out", (T, n), (x.dtype, torch.float32))
-        workspace = at.workspace(workspace, moe_linear_workspace(T, d, n, ldx, ldw, dtype))
-        _check("moe_linear", lib().moe_linear(
-            px, ldx, pw, ldw, _vec(bias, "bias", n, x.dtype), pr, ldr,
-            dtype if residual is None else DTYPE_OF[residual.dtype], dtype, ACTS[act], T, d, n,
-            workspace.data_ptr(), workspace.numel() * workspace.element_size(), po, ldo,
-            DTYPE_OF[out.dtype], at.handle))
+        px, ldx = _mat(x, "x", dev, T, d, D)
+        pw, ldw = _mat(w, "w", dev, d, n, D)
+        pr, ldr = _mat(residual, "residual", dev, T, n, D, torch.float32)
+        po, ldo = _mat(out, "out", dev, T, n, D, torch.float32)
+        dtype = DTYPE_OF[D]
+        workspace, ws, have = at.workspace(workspace,
+                                           moe_linear_workspace(T, d, n, ldx, ldw, dtype))
+        rc = lib().moe_linear(px, ldx, pw, ldw, _vec(bias, "bias", dev, n, D), pr, ldr,
+                              dtype if pr is None else DTYPE_OF[residual.dtype], dtype, ACTS[act],
+                              T, d, n, ws, have, po, ldo, DTYPE_OF[out.dtype], at.handle)
+    _check("moe_linear", rc)
     return out, workspace
 
 
@@ -572,37 +586,39 @@ def linear_backward(x, w, dz, grads=("dx", "dw", "db"), grad_dtype=None, workspa
     [n] in grad_dtype (dz's type, or torch.float32). `grads` names what is computed; a
     given dx, dw or db is filled. x may be None without dw, w without dx (not both).
     Returns (dict of the gradients, workspace)."""
-    dtype = DTYPE_OF[dz.dtype]
-    T, n = dz.shape
-    if x is None and w is None:
-        raise ValueError("x and w are both None")
-    d = x.shape[1] if x is not None else w.shape[0]
-    want = {"dx": dx, "dw": dw, "db": db}
-    if not grads or set(grads) - set(want):
+    if not grads or set(grads) - {"dx", "dw", "db"}:
         raise ValueError(f"grads: expected some of dx, dw, db, got {grads}")
-    with _Launch(dz, stream) as at:
-        at.same(x=x, w=w, dx=dx, dw=dw, db=db, workspace=workspace)
-        px, ldx = _mat(x, "x", (T, d), dz.dtype)
-        pw, ldw = _mat(w, "w", (d, n), dz.dtype)
-        pz, lddz = _mat(dz, "dz")
-        if ("dw" in grads and x is None) or ("dx" in grads and w is None):
-            raise ValueError("dw needs x, dx needs w")
-        if grad_dtype is None:
-            grad_dtype = next((g.dtype for g in (dw, db) if g is not None), dz.dtype)
-        shapes = {"dx": ((T, d), dz.dtype), "dw": ((d, n), grad_dtype), "db": ((n,), grad_dtype)}
-        got = {k: want[k] if want[k] is not None else at.empty(*shapes[k])
-               for k in ("dx", "dw", "db") if k in grads}
-        pdx, lddx = _mat(got.get("dx"), "dx", (T, d), dz.dtype)
-        pdw, lddw = _mat(got.get("dw"), "dw", (d, n), grad_dtype)
-        pdb = _vec(got.get("db"), "db", n, grad_dtype)
-        mask = ((MOE_GRAD_X if pdx else 0) | (MOE_GRAD_W if pdw else 0) |
-                (MOE_GRAD_BIAS if pdb else 0))
-        need = moe_linear_backward_workspace(T, d, n, ldx, ldw, lddz, dtype, mask)
-        workspace = at.workspace(workspace, need)
-        _check("moe_linear_backward", lib().moe_linear_backward(
-            px, ldx, pw, ldw, pz, lddz, dtype, T, d, n, workspace.data_ptr(),
-            workspace.numel() * workspace.element_size(), pdx, lddx, pdw, lddw, pdb,
-            DTYPE_OF[grad_dtype], at.handle))
+    if ("dw" in grads and x is None) or ("dx" in grads and w is None) or (x is None and w is None):
+        raise ValueError("dw needs x, dx needs w, and one of them gives d")
+    with _On(dz, "dz", stream) as at:
+        dev, D = at.index, dz.dtype
+        T, n = _matrix_shape(dz, "dz")
+        d = _matrix_shape(x, "x")[1] if x is not None else _matrix_shape(w, "w")[0]
+        px, ldx = _mat(x, "x", dev, T, d, D)
+        pw, ldw = _mat(w, "w", dev, d, n, D)
+        pz, lddz = _mat(dz, "dz", dev, T, n, D)
+        G = grad_dtype or (dw.dtype if dw is not None else db.dtype if db is not None else D)
+        if G is not D and G is not torch.float32:
+            raise TypeError(f"grad_dtype: expected {D} or torch.float32, got {G}")
+        got, mask = {}, 0
+        if "dx" in grads:
+            got["dx"] = at.empty((T, d), D) if dx is None else dx
+            mask = MOE_GRAD_X
+        if "dw" in grads:
+            got["dw"] = at.empty((d, n), G) if dw is None else dw
+            mask |= MOE_GRAD_W
+        if "db" in grads:
+            got["db"] = at.empty((n,), G) if db is None else db
+            mask |= MOE_GRAD_BIAS
+        pdx, lddx = _mat(got.get("dx"), "dx", dev, T, d, D)
+        pdw, lddw = _mat(got.get("dw"), "dw", dev, d, n, G)
+        pdb = _vec(got.get("db"), "db", dev, n, G)
+        dtype = DTYPE_OF[D]
+        workspace, ws, have = at.workspace(
+            workspace, moe_linear_backward_workspace(T, d, n, ldx, ldw, lddz, dtype, mask))
+        rc = lib().moe_linear_backward(px, ldx, pw, ldw, pz, lddz, dtype, T, d, n, ws, have, pdx,
+                                       lddx, pdw, lddw, pdb, DTYPE_OF[G], at.handle)
+    _check("moe_linear_backward", rc)
     return got, workspace
 
 
@@ -610,19 +626,20 @@ def balance_loss(logits, ids, workspace=None, cnt=None, prob=None, loss=None, st
     """Router losses of logits [T, E] fp32 and ids [T, K] int32. Returns (dict, workspace):
     loss [2] (balance, z), cnt [E + 2] int32 (entries per expert, valid tokens, valid
     entries), prob [E] (mean probability over the valid tokens)."""
-    T, E = logits.shape
-    K = ids.shape[1]
-    with _Launch(logits, stream) as at:
-        at.same(ids=ids, cnt=cnt, prob=prob, loss=loss, workspace=workspace)
+    with _On(logits, "logits", stream) as at:
+        dev = at.index
+        T, E = _matrix_shape(logits, "logits")
+        K = _matrix_shape(ids, "ids")[1]
         cnt = at.empty((E + 2,), torch.int32) if cnt is None else cnt
         prob = at.empty((E,), torch.float32) if prob is None else prob
         loss = at.empty((2,), torch.float32) if loss is None else loss
-        workspace = at.workspace(workspace, moe_balance_workspace(T, E, K))
-        _check("moe_balance_loss", lib().moe_balance_loss(
-            _vec(logits, "logits", T * E, torch.float32), _vec(ids, "ids", T * K, torch.int32), T,
-            E, K, workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-            _vec(cnt, "cnt", E + 2, torch.int32), _vec(prob, "prob", E, torch.float32),
-            _vec(loss, "loss", 2, torch.float32), at.handle))
+        workspace, ws, have = at.workspace(workspace, moe_balance_workspace(T, E, K))
+        rc = lib().moe_balance_loss(
+            _vec(logits, "logits", dev, T * E, torch.float32),
+            _vec(ids, "ids", dev, T * K, torch.int32), T, E, K, ws, have,
+            _vec(cnt, "cnt", dev, E + 2, torch.int32), _vec(prob, "prob", dev, E, torch.float32),
+            _vec(loss, "loss", dev, 2, torch.float32), at.handle)
+    _check("moe_balance_loss", rc)
     return {"loss": loss, "cnt": cnt, "prob": prob}, workspace
 
 
@@ -631,19 +648,21 @@ def route_backward(logits, ids, w, dw, cnt, dloss, out_dtype=None, out=None, str
     w (None: no such term), and dloss [2], the gradient by balance_loss()'s two losses
     (None: no such term); cnt as balance_loss() gave it. out_dtype: fp32, or the type of
     the router's product."""
-    T, E = logits.shape
-    K = ids.shape[1]
-    with _Launch(logits, stream) as at:
-        at.same(ids=ids, w=w, dw=dw, cnt=cnt, dloss=dloss, out=out)
+    with _On(logits, "logits", stream) as at:
+        dev = at.index
+        T, E = _matrix_shape(logits, "logits")
+        K = _matrix_shape(ids, "ids")[1]
         if out is None:
             out = at.empty((T, E), out_dtype or torch.float32)
-        elif out_dtype is not None and out.dtype != out_dtype:
+        elif out_dtype is not None and out.dtype is not out_dtype:
             raise TypeError(f"out: expected {out_dtype}, got {out.dtype}")
-        _check("moe_route_backward", lib().moe_route_backward(
-            _vec(logits, "logits", T * E, torch.float32), _vec(ids, "ids", T * K, torch.int32),
-            _vec(w, "w", T * K, torch.float32), _vec(dw, "dw", T * K, torch.float32),
-            _vec(cnt, "cnt", E + 2, torch.int32), _vec(dloss, "dloss", 2, torch.float32), T, E, K,
-            _vec(out, "out", T * E, out.dtype), DTYPE_OF[out.dtype], at.handle))
+        rc = lib().moe_route_backward(
+            _vec(logits, "logits", dev, T * E, torch.float32),
+            _vec(ids, "ids", dev, T * K, torch.int32), _vec(w, "w", dev, T * K, torch.float32),
+            _vec(dw, "dw", dev, T * K, torch.float32), _vec(cnt, "cnt", dev, E + 2, torch.int32),
+            _vec(dloss, "dloss", dev, 2, torch.float32), T, E, K,
+            _vec(out, "out", dev, T * E, out.dtype), DTYPE_OF[out.dtype], at.handle)
+    _check("moe_route_backward", rc)
     return out
 
 
@@ -652,23 +671,22 @@ def act_forward(g, u=None, act: str = "silu", ckpt=None, h=None, stream=None):
     new 8-bit checkpoint) or an earlier call's, which is overwritten. Returns (h, ckpt);
     a checkpoint is a dict of e4m3 codes g8, u8 [T, f] and scale bytes gs, us [T,
     ceil(f / 32)], code * 2^(scale - 127) the values they stand for."""
-    T, f = g.shape
-    with _Launch(g, stream) as at:
-        at.same(u=u, h=h)
-        pg, ldg = _mat(g, "g")
-        pu, ldu = _mat(u, "u", (T, f), g.dtype)
-        h = at.empty((T, f), g.dtype) if h is None else h
-        ph, ldh = _mat(h, "h", (T, f), g.dtype)
+    with _On(g, "g", stream) as at:
+        dev, D = at.index, g.dtype
+        T, f = _matrix_shape(g, "g")
         if ckpt is True:
-            nb = -(-f // ACT8_BLOCK)
             ckpt = {}
             for k in ("g", "u")[:1 if u is None else 2]:
                 ckpt[k + "8"] = at.empty((T, f), torch.float8_e4m3fn)
-                ckpt[k + "s"] = at.empty((T, nb), torch.uint8)
-        g8, gs, u8, us = _ckpt(at, ckpt, T, f, u is not None)
-        _check("moe_act_forward", lib().moe_act_forward(
-            pg, ldg, pu, ldu, DTYPE_OF[g.dtype], ACTS[act], T, f, ph, ldh, g8, gs, u8, us,
-            at.handle))
+                ckpt[k + "s"] = at.empty((T, -(-f // ACT8_BLOCK)), torch.uint8)
+        h = at.empty((T, f), D) if h is None else h
+        pg, ldg = _mat(g, "g", dev, T, f, D)
+        pu, ldu = _mat(u, "u", dev, T, f, D)
+        ph, ldh = _mat(h, "h", dev, T, f, D)
+        g8, gs, u8, us = _ckpt(dev, ckpt, T, f, u is not None)
+        rc = lib().moe_act_forward(pg, ldg, pu, ldu, DTYPE_OF[D], ACTS[act], T, f, ph, ldh, g8, gs,
+                                   u8, us, at.handle)
+    _check("moe_act_forward", rc)
     return h, ckpt
 
 
@@ -676,37 +694,36 @@ def act_backward(ckpt, dh, act: str = "silu", dg=None, du=None, h=None, need_h: 
                  stream=None):
     """From act_forward()'s checkpoint and dh [T, f]: a dict of dg, du (if there was a u) and
     h, the forward's output as the checkpoint gives it (not with need_h=False)."""
-    T, f = dh.shape
-    gated = "u8" in ckpt
-    with _Launch(dh, stream) as at:
-        at.same(dg=dg, du=du, h=h)
+    with _On(dh, "dh", stream) as at:
+        dev, D = at.index, dh.dtype
+        T, f = _matrix_shape(dh, "dh")
+        gated = "u8" in ckpt
         if du is not None and not gated:
             raise ValueError("du: the checkpoint has no u")
-        pz, lddh = _mat(dh, "dh")
-        new = lambda t: at.empty((T, f), dh.dtype) if t is None else t  # noqa: E731
-        got = {"dg": new(dg)}
+        got = {"dg": at.empty((T, f), D) if dg is None else dg}
         if gated:
-            got["du"] = new(du)
+            got["du"] = at.empty((T, f), D) if du is None else du
         if need_h or h is not None:
-            got["h"] = new(h)
-        pdg, lddg = _mat(got["dg"], "dg", (T, f), dh.dtype)
-        pdu, lddu = _mat(got.get("du"), "du", (T, f), dh.dtype)
-        ph, ldh = _mat(got.get("h"), "h", (T, f), dh.dtype)
-        g8, gs, u8, us = _ckpt(at, ckpt, T, f, gated)
-        _check("moe_act_backward", lib().moe_act_backward(
-            g8, gs, u8, us, pz, lddh, DTYPE_OF[dh.dtype], ACTS[act], T, f, pdg, lddg, pdu, lddu,
-            ph, ldh, at.handle))
+            got["h"] = at.empty((T, f), D) if h is None else h
+        pz, lddh = _mat(dh, "dh", dev, T, f, D)
+        pdg, lddg = _mat(got["dg"], "dg", dev, T, f, D)
+        pdu, lddu = _mat(got.get("du"), "du", dev, T, f, D)
+        ph, ldh = _mat(got.get("h"), "h", dev, T, f, D)
+        g8, gs, u8, us = _ckpt(dev, ckpt, T, f, gated)
+        rc = lib().moe_act_backward(g8, gs, u8, us, pz, lddh, DTYPE_OF[D], ACTS[act], T, f, pdg,
+                                    lddg, pdu, lddu, ph, ldh, at.handle)
+    _check("moe_act_backward", rc)
     return got
 
 
-def _ckpt(at, ckpt, T, f, gated):
+def _ckpt(dev, ckpt, T, f, gated):
     """device addresses g8, gs, u8, us of a checkpoint (None where there is none)"""
     if ckpt is None:
         return None, None, None, None
     if ("u8" in ckpt) != gated:
         raise ValueError("ckpt: made for another kind of activation (with or without u)")
-    at.same(**ckpt)
-    nb = -(-f // ACT8_BLOCK)
-    one = lambda k: (_vec(ckpt[k + "8"], k + "8", T * f, torch.float8_e4m3fn),  # noqa: E731
-                     _vec(ckpt[k + "s"], k + "s", T * nb, torch.uint8))
-    return one("g") + (one("u") if gated else (None, None))
+    nb = T * -(-f // ACT8_BLOCK)
+    g = (_vec(ckpt["g8"], "g8", dev, T * f, torch.float8_e4m3fn),
+         _vec(ckpt["gs"], "gs", dev, nb, torch.uint8))
+    return g + ((_vec(ckpt["u8"], "u8", dev, T * f, torch.float8_e4m3fn),
+                 _vec(ckpt["us"], "us", dev, nb, torch.uint8)) if gated else (None, None))
