@@ -511,10 +511,15 @@ enum moe_act { MOE_ACT_NONE = 0, MOE_ACT_RELU = 1, MOE_ACT_SILU = 2, MOE_ACT_GEL
  * workspace: moe_linear_workspace() bytes (padded copies of operands whose
  *      stride or row length is not a multiple of 16 bytes; fp32 partial sums
  *      when few tiles are cut along d).
+ * moe_linear_shape -- host only: the tile (64, 128 or 256 rows and columns of a
+ *      workgroup) and the ranges of K that a product of M x N outputs over K is
+ *      computed in: the forward product is T x n over d, dx is T x d over n, dw
+ *      d x n over T. Errors: MOE_EINVAL for a size < 1, a bad dtype, NULL.
  * Errors: MOE_EINVAL for T, d or n < 1, a stride below the row length or above
  *      2^20, a bad dtype or act, NULL or misaligned pointers, a small
- *      workspace, more than 2^31 tiles of 128 x 128; MOE_EHIP on a failed launch.
+ *      workspace, more than 2^31 tiles of 64 x 64; MOE_EHIP on a failed launch.
  */
+int moe_linear_shape(int M, int N, int K, int dtype, int *tile, int *split);
 int moe_linear_workspace(int T, int d, int n, int64_t ldx, int64_t ldw, int dtype, size_t *bytes);
 int moe_linear(const void *x, int64_t ldx, const void *w, int64_t ldw, const void *bias,
                const void *residual, int64_t ldr, int residual_dtype, int dtype, int act, int T,

@@ -89,6 +89,8 @@ _SIGS = {
     "moe_forward_packed_timed": [P, P, P, P, P, P, I32, I32, I32, I32, I32, I32, I32, P, SZ, P, P,
                                  P],
     "moe_linear_workspace": [I32, I32, I32, I64, I64, I32, ctypes.POINTER(ctypes.c_size_t)],
+    "moe_linear_shape": [I32, I32, I32, I32, ctypes.POINTER(ctypes.c_int),
+                         ctypes.POINTER(ctypes.c_int)],
     "moe_linear": [P, I64, P, I64, P, P, I64, I32, I32, I32, I32, I32, I32, P, SZ, P, I64, I32, P],
     "moe_linear_backward_workspace": [I32, I32, I32, I64, I64, I64, I32, I32,
                                       ctypes.POINTER(ctypes.c_size_t)],
@@ -476,6 +478,14 @@ def forward_host(x, ids, w, hw_gate, hw_up, hw_down, tm: int = 16, packed: bool 
 
 
 # ---------------------------------------------- dense operators (C entry points) --
+
+def moe_linear_shape(M: int, N: int, K: int, dtype: int):
+    """(tile, splits along K) of a product of M x N outputs over K."""
+    a, b = ctypes.c_int(), ctypes.c_int()
+    _check("moe_linear_shape",
+           lib().moe_linear_shape(M, N, K, dtype, ctypes.byref(a), ctypes.byref(b)))
+    return a.value, b.value
+
 
 @functools.lru_cache(maxsize=1024)
 def moe_linear_workspace(T: int, d: int, n: int, ldx: int, ldw: int, dtype: int) -> int:

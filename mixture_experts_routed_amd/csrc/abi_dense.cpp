@@ -22,8 +22,8 @@ int linear_sizes(int T, int d, int n, int64_t ldx, int64_t ldw, int dtype)
 {
     if (T < 1 || d < 1 || n < 1 || T > kI32Max - 1024 || !dtype_ok(dtype)) return MOE_EINVAL;
     if (!rows_ok(d, ldx) || !rows_ok(n, ldw)) return MOE_EINVAL;
-    // workgroups of the largest product (128 x 128 tiles)
-    const int64_t t = ((int64_t)T + 127) / 128, a = (d + 127) / 128, b = (n + 127) / 128;
+    // workgroups of the largest product (64 x 64 tiles)
+    const int64_t t = ((int64_t)T + 63) / 64, a = (d + 63) / 64, b = (n + 63) / 64;
     if (t * (a > b ? a : b) > kI32Max - 1024) return MOE_EINVAL;
     return MOE_OK;
 }
@@ -51,6 +51,15 @@ int moe_linear_workspace(int T, int d, int n, int64_t ldx, int64_t ldw, int dtyp
     const int rc = linear_sizes(T, d, n, ldx, ldw, dtype);
     if (rc == MOE_OK) *bytes = (size_t)moe::linear_space(T, d, n, ldx, ldw, dtype).total;
     return rc;
+}
+
+int moe_linear_shape(int M, int N, int K, int dtype, int *tile, int *split)
+{
+    if (!tile || !split || M < 1 || N < 1 || K < 1 || M > kI32Max - 1024 || N > kI32Max - 1024 ||
+        K > kI32Max - 1024 || !dtype_ok(dtype))
+        return MOE_EINVAL;
+    moe::linear_shape(M, N, K, dtype, tile, split);
+    return MOE_OK;
 }
 
 int moe_linear(const void *x, int64_t ldx, const void *w, int64_t ldw, const void *bias,

@@ -152,6 +152,8 @@ struct LinearBackwardSpace {
     int64_t x, w, dz, part, total;
     int db_blocks;  // blocks of rows of the column sums
 };
+// tile (rows and columns of a workgroup) and splits along K of an M x N product over K
+void linear_shape(int M, int N, int K, int dtype, int *tile, int *split);
 LinearSpace linear_space(int T, int d, int n, int64_t ldx, int64_t ldw, int dtype);
 LinearBackwardSpace linear_backward_space(int T, int d, int n, int64_t ldx, int64_t ldw,
                                           int64_t lddz, int dtype, bool dx, bool dw, bool db);

@@ -267,23 +267,25 @@ __device__ __forceinline__ void load_to_lds(uint32_t to, uint32_t off, int4v rsr
 
 // One operand's part of a workgroup's tile: ROWS output rows (or columns) of
 // it, NTH threads; COL: the operand is in columns form; NF: 32-row fragments
-// of a wavefront. Loads of successive K-steps are issued in order: advance()
-// makes the next step current.
-template <typename T, bool COL, int ROWS, int NTH, int NF>
+// of a wavefront. Loads of every STRIDE-th K-step are issued in order: advance()
+// makes the next one current.
+template <typename T, bool COL, int ROWS, int NTH, int NF, int STRIDE = 1>
 struct Operand {
     static constexpr int ES = sizeof(T), EPC = 16 / ES, BK = kStepBytes / ES;
+    static constexpr int AHEAD = BK * STRIDE;           // values of k per advance()
     static constexpr int BYTES = ROWS * kStepBytes;     // of a step
     static constexpr int CHUNKS = BYTES / 16;
     static constexpr int LOADS = CHUNKS / NTH;          // per thread and step
     static constexpr int CPR = COL ? ROWS / EPC : kStepBytes / 16;  // chunks per LDS row
     static constexpr int SEG = ES == 2 ? 2 : 8;         // columns form: chunks per segment
     static_assert(CHUNKS % NTH == 0, "whole loads");
-    static_assert(!COL || ROWS >= 128, "the permutation needs 8 (fp32: 2) segments");
+    static_assert(ROWS >= 64, "the permutation needs 4 (fp32: 2) segments");
 
-    // the permutation of row k's segments (columns form)
+    // the permutation of row k's segments (columns form); rows of 64 columns of
+    // the 16-bit types are half the banks long: two rows already lie apart
     static __device__ __forceinline__ int seg_xor(int k)
     {
-        return ES == 2 ? (k & 3) << 1 : (k >> 2) & 1;
+        return ES == 4 ? (k >> 2) & 1 : ROWS == 64 ? k & 2 : (k & 3) << 1;
     }
 
     const char *base;    // rows form: the tile's first row; columns: the current step's first row
@@ -301,11 +303,11 @@ struct Operand {
                                          int k0, int tid, int frag0)
     {
         ld = ld_;
-        left = K - k0 + BK;  // (advance() comes before the first step)
+        left = K - k0 + AHEAD;  // (advance() comes before the first step)
         const int have = min(ROWS, total - first);
         kc = 0;
         if (COL) {
-            base = p + (int64_t)first * ES + ((int64_t)k0 - BK) * ld;
+            base = p + (int64_t)first * ES + ((int64_t)k0 - AHEAD) * ld;
             tail = (uint32_t)(have * ES);
             full = (uint32_t)((BK - 1) * ld) + tail;
         } else {
@@ -323,7 +325,7 @@ struct Operand {
                 const int lc = c ^ ((r >> 1) & 7);  // the same for every i
                 kc = lc * EPC;
                 off[i] = r < have ? (uint32_t)r * (uint32_t)ld + (uint32_t)lc * 16u +
-                                        (uint32_t)((k0 - BK) * ES)
+                                        (uint32_t)((k0 - AHEAD) * ES)
                                   : kOutside;
             }
         }
@@ -350,14 +352,14 @@ struct Operand {
 
     __device__ __forceinline__ void advance()
     {
-        left -= BK;
+        left -= AHEAD;
         if (COL) {
-            base += (int64_t)BK * ld;
+            base += (int64_t)AHEAD * ld;
             bytes = left >= BK ? full : left > 0 ? (uint32_t)((left - 1) * ld) + tail : 0u;
         } else {
             // (a row past the operand's end stays outside: the range ends below 2^31)
 #pragma unroll
-            for (int i = 0; i < LOADS; ++i) off[i] += kStepBytes;
+            for (int i = 0; i < LOADS; ++i) off[i] += kStepBytes * STRIDE;
         }
     }
 
@@ -590,6 +592,138 @@ __global__ __launch_bounds__(256, (BM + BN > 256 ? 1 : 2)) void k_gemm(const Gem
     }
 }
 
+// 64 x 64 tiles for products that are too small to fill the GPU with larger
+// ones: every wavefront computes the whole tile over one k-group of each step
+// (wavefront w group w), and the partial tiles are added, in order, through LDS
+// at the end. Four buffers hold four steps; the loads of step s + 3 go out when
+// step s is read. Such a product waits for memory and for its barriers, not for
+// the matrix cores: two of these workgroups run on a CU, or, where there is no
+// more than one for every CU, one of TEAMS = 2 times 4 wavefronts, each with
+// buffers of its own and every other step (2,048 x 512 outputs over 2,560
+// values of k: 17 us with 256 workgroups of one team).
+constexpr int kSmall = 64, kSmallBuffers = 4;
+template <typename T, bool AC, bool BC, int TEAMS>
+__global__ __launch_bounds__(256 * TEAMS, 2) void k_gemm_small(const GemmArg p)
+{
+    constexpr int NTH = 256, BK = kStepBytes / (int)sizeof(T), NB = kSmallBuffers;
+    typedef Operand<T, AC, kSmall, NTH, 2, TEAMS> OpA;
+    typedef Operand<T, BC, kSmall, NTH, 2, TEAMS> OpB;
+    constexpr uint32_t BUF = OpA::BYTES + OpB::BYTES;
+    constexpr int LOADS = OpA::LOADS + OpB::LOADS;
+    __shared__ uint4 lds[TEAMS * NB * BUF / 16];
+    const int lb = xcd_logical_block(p.mt * p.nt * p.split);
+    if (lb < 0) return;  // whole workgroup: no barrier reached
+    const int tile = lb / p.split, split = lb - tile * p.split;
+    const int tm = tile / p.nt, tn = tile - tm * p.nt;
+    const int lane = threadIdx.x & 63;
+    const int team = __builtin_amdgcn_readfirstlane(threadIdx.x >> 8);
+    const int tid = threadIdx.x & 255;  // in the team
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    // (whole rounds of the teams: a step past the end of k reads zeros)
+    const int s0 = split * p.steps;
+    const int s1 = min(s0 + p.steps, (p.K + BK - 1) / BK);
+    const int rounds = (s1 - s0 + TEAMS - 1) / TEAMS;
+    const int k0 = (s0 + team) * BK;
+    OpA a;
+    OpB b;
+    a.init(p.A, p.lda, tm * kSmall, AC ? p.a_cols : p.M, AC ? p.K : p.a_cols, k0, tid, 0);
+    b.init(p.B, p.ldb, tn * kSmall, BC ? p.b_cols : p.N, BC ? p.K : p.b_cols, k0, tid, 0);
+    float16_t acc[2][2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
+    const uint32_t base = lds_at(lds) + (uint32_t)team * NB * BUF;
+    auto next = [&](uint32_t q) { return q + BUF == base + NB * BUF ? base : q + BUF; };
+    auto load = [&](uint32_t to) {
+        a.advance();
+        b.advance();
+        asm volatile("s_nop 4" ::: "memory");
+#pragma unroll
+        for (int i = 0; i < OpA::LOADS; ++i) a.issue(to, i, wave);
+#pragma unroll
+        for (int i = 0; i < OpB::LOADS; ++i) b.issue(to + OpA::BYTES, i, wave);
+    };
+    if (rounds > 0) {
+        uint32_t rd = base, wr = base;
+#pragma unroll
+        for (int q = 0; q < NB - 1; ++q) {
+            load(wr);
+            wr = next(wr);
+        }
+        for (int s = 0; s < rounds; ++s) {
+            // this step has landed and the one before is read out; for everyone
+            asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier"
+                         :
+                         : "n"((NB - 2) * LOADS)
+                         : "memory");
+            load(wr);
+            wr = next(wr);
+            uint4 fa[2], fb[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                // (the group is the wavefront's: uniform, so a scalar branch)
+#pragma unroll
+                for (int g = 0; g < kGroups; ++g)
+                    if (g == wave) {
+                        fa[i] = a.frag(rd, i, g);
+                        fb[i] = b.frag(rd + OpA::BYTES, i, g);
+                    }
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) Mma<T>::run(fb[j], fa[i], acc[i][j]);
+            rd = next(rd);
+        }
+        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    }
+    // 32 rows at a time: the wavefronts' parts side by side, then one thread per
+    // 8 columns of a row
+    constexpr int PITCH = kSmall + 4, PART = 32 * PITCH, PARTS = 4 * TEAMS;
+    static_assert(PARTS * PART * 4 <= (int)(TEAMS * NB * BUF), "fits");
+    float *f = reinterpret_cast<float *>(lds);
+    float *plane = p.part + (int64_t)split * p.M * p.N;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        if (i) __syncthreads();
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const float16_t &c = acc[i][j];
+                *reinterpret_cast<float4_t *>(f + (team * 4 + wave) * PART + (lane & 31) * PITCH +
+                                              j * 32 + 8 * q + 4 * (lane >> 5)) =
+                    float4_t{c[4 * q], c[4 * q + 1], c[4 * q + 2], c[4 * q + 3]};
+            }
+        __syncthreads();
+        const int r = tid >> 3, m = tm * kSmall + i * 32 + r, n = tn * kSmall + (tid & 7) * 8;
+        if (team == 0 && m < p.M && n < p.N) {
+            float v[8] = {};
+#pragma unroll
+            for (int w = 0; w < PARTS; ++w) {
+                float q[8];
+                load8<float>(f + w * PART + r * PITCH + (tid & 7) * 8, q);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) v[k] += q[k];
+            }
+            if (p.split > 1) {
+                float *o = plane + (int64_t)m * p.N + n;
+                if (n + 8 <= p.N && (p.N & 3) == 0)
+                    store8<float>(o, v);
+                else
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        if (n + k < p.N) o[k] = v[k];
+            } else {
+                finish8<T>(p.e, m, n, p.N, v);
+            }
+        }
+    }
+}
+
 // The split products' partial planes added in split order, then the epilogue:
 // one thread per 8 columns of a row.
 template <typename T>
@@ -618,8 +752,10 @@ __global__ __launch_bounds__(256) void k_gemm_reduce(const float *__restrict__ p
     }
 }
 
-// dst [R][ldd] = src [R][C] (rows of lds elements), columns C .. ldd zero; U is
-// the raw element, one 16-byte chunk of dst per thread
+// dst [R][ldd] = src [R][C] (rows of lds units), columns C .. ldd zero. U is the
+// unit that is copied: the element, or 2 or 4 of the 16-bit types (2 of fp32)
+// together where a row is whole units and starts at one. One 16-byte chunk of
+// dst per thread.
 template <typename U>
 __global__ __launch_bounds__(256) void k_pad_rows(const U *__restrict__ src, int64_t lds, int64_t R,
                                                   int C, U *__restrict__ dst, int ldd)
@@ -708,43 +844,71 @@ __global__ __launch_bounds__(256) void k_colsum_join(const float *__restrict__ p
 
 // ---- host side ---------------------------------------------------------------
 
-constexpr int kSlots = 512;       // workgroups of a 128 x 128 tile that the GPU holds at once
-constexpr int kMinSplitSteps = 4;
-
 int elem_size(int dtype) { return dtype == 0 ? 4 : 2; }
 int64_t up(int64_t v, int64_t a) { return (v + a - 1) / a * a; }
 int64_t div_up(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 struct Product {
     int64_t mt, nt;
-    int tile;  // 128 or 256 rows and columns
+    int tile;  // 64, 128 or 256 rows and columns
     int split, steps;
     int64_t part_bytes;
 };
 
-// 256 x 256 tiles where, cut along k into splits of at least 16 steps, they
-// occupy three quarters of the 256 CUs (one workgroup each): 2,048 x 4,096
-// outputs over 32,768 values of k take 427 us in 128 tiles cut in two against
-// 563 us in 512 tiles of 128 x 128; over 8,192, both take 124 us
-bool tiles256_fill(int64_t M, int64_t N, int64_t steps)
+// Estimated microseconds of M x N outputs over `steps` K-steps in tiles of
+// `tile`, cut into `split` along k. A workgroup alone on its CU takes c per
+// step, two of them together c2 each; `fixed` is the launch with the first
+// loads and the last stores. The constants are fits to measurements on the
+// shapes named (tile 64 / 128 / 256, best split, 16-bit types):
+//   4 x 2,816 over 704             6.5 /  7.8 / 12
+//   64 x 512 over 2,560            9.7 / 10.5 / 16
+//   1,024 x 1,024 over 1,024       8.6 / 11.7 / 27
+//   2,048 x 512 over 2,560        14.9 / 18.5 / 28
+//   512 x 2,048 over 4,096          26 /   22 / 32
+//   2,048 x 2,048 over 2,048        38 /   26 / 42
+//   2,560 x 512 over 32,768        159 /  112 / 95
+//   32,768 x 2,048 over 4,096        - /  555 / 485
+// and, in fp32 (bound by the matrix cores), 512 x 512 over 1,024: 14.8 / 21,
+// 2,048 x 2,048 over 2,048: 164 / 134.
+double product_us(int64_t M, int64_t N, int64_t steps, int dtype, int tile, int64_t split)
 {
-    const int64_t t = div_up(M, 256) * div_up(N, 256);
-    const int64_t s = t < 256 ? 256 / t : 1;
-    const int64_t most = steps / 16 > 1 ? steps / 16 : 1;
-    return t * (s < most ? s : most) >= 192;
+    const double wgs = (double)(div_up(M, tile) * div_up(N, tile) * split);
+    const double n = (double)div_up(steps, split);
+    const double full = wgs < 256 ? wgs / 256 : 1;  // share of the CUs (their power and L2)
+    double t;
+    if (tile == 256) {
+        t = 5 + (double)div_up((int64_t)wgs, 256) * (4 + n * (0.9 + 0.8 * full * full));
+    } else {
+        const double c = dtype == 0 ? (tile == 64 ? 0.6 : 1.9)
+                         : tile == 64 ? 0.2 + 0.1 * full : 0.42 + 0.12 * full;
+        const double c2 = dtype == 0 ? 2 * c : tile == 64 ? 0.5 : 1.1;
+        t = (tile == 64 ? 4.5 : 6) +
+            (wgs <= 256 ? n * c : (double)div_up((int64_t)wgs, 512) * (1 + n * c2));
+    }
+    if (split > 1) t += 2 + (double)split * (double)M * (double)N * 8 / 5e6;
+    return t;
 }
 
 Product product_of(int64_t M, int64_t N, int64_t K, int dtype)
 {
-    Product z;
     const int64_t steps = div_up(K, kStepBytes / elem_size(dtype));
-    z.tile = dtype != 0 && tiles256_fill(M, N, steps) ? 256 : 128;
-    z.mt = div_up(M, z.tile);
-    z.nt = div_up(N, z.tile);
-    int64_t s = (z.tile == 256 ? kSlots / 2 : kSlots) / (z.mt * z.nt);
-    s = s < steps / kMinSplitSteps ? s : steps / kMinSplitSteps;
-    s = s < 1 ? 1 : s;
-    z.steps = (int)div_up(steps, s);
+    Product z{};
+    double best = 0;
+    for (int tile = 64; tile <= (dtype == 0 ? 128 : 256); tile *= 2) {
+        const int64_t mt = div_up(M, tile), nt = div_up(N, tile);
+        for (int64_t s = 1; s <= 16; ++s) {
+            // splits of at least two steps, of a product that does not fill the GPU
+            if (s > 1 && (2 * s > steps || mt * nt * s > (tile == 256 ? 256 : 512))) break;
+            const double t = product_us(M, N, steps, dtype, tile, s);
+            if (z.tile && t >= best) continue;
+            best = t;
+            z.mt = mt;
+            z.nt = nt;
+            z.tile = tile;
+            z.split = (int)s;
+        }
+    }
+    z.steps = (int)up(div_up(steps, z.split), 2);  // (whole rounds of two teams)
     z.split = (int)div_up(steps, z.steps);
     z.part_bytes = z.split > 1 ? up((int64_t)z.split * M * N * 4, 256) : 0;
     return z;
@@ -785,15 +949,19 @@ hipError_t place(const void *src, int64_t R, int64_t C, int64_t ld, int dtype, c
     m->p = dst;
     m->ld = z.cols * es;
     const int64_t chunks = R * (z.cols * es / 16);
-    const dim3 grid((unsigned)(chunks / 256 + 1 < 4096 ? chunks / 256 + 1 : 4096)), block(256);
-    if (es == 2)
-        hipLaunchKernelGGL(k_pad_rows<uint16_t>, grid, block, 0, s,
-                           static_cast<const uint16_t *>(src), ld, R, (int)C,
-                           reinterpret_cast<uint16_t *>(dst), (int)z.cols);
+    const dim3 grid((unsigned)(chunks / 256 + 1 < 8192 ? chunks / 256 + 1 : 8192)), block(256);
+    auto copy = [&](auto unit) {
+        typedef decltype(unit) U;
+        const int64_t per = sizeof(U) / es;
+        hipLaunchKernelGGL(k_pad_rows<U>, grid, block, 0, s, static_cast<const U *>(src), ld / per,
+                           R, (int)(C / per), reinterpret_cast<U *>(dst), (int)(z.cols / per));
+    };
+    if (C * es % 8 == 0 && ld * es % 8 == 0)
+        copy(uint64_t());
+    else if (C * es % 4 == 0 && ld * es % 4 == 0)
+        copy(uint32_t());
     else
-        hipLaunchKernelGGL(k_pad_rows<uint32_t>, grid, block, 0, s,
-                           static_cast<const uint32_t *>(src), ld, R, (int)C,
-                           reinterpret_cast<uint32_t *>(dst), (int)z.cols);
+        copy(uint16_t());
     return hipGetLastError();
 }
 
@@ -818,7 +986,12 @@ hipError_t launch_product(const Matrix &A, const Matrix &B, int M, int N, int K,
     g.part = part;
     g.e = e;
     const dim3 grid((unsigned)up(z.mt * z.nt * z.split, 8)), block(256);
-    if constexpr (sizeof(T) == 2) {
+    if (z.tile == kSmall) {
+        if (z.mt * z.nt * z.split <= 256)
+            hipLaunchKernelGGL((k_gemm_small<T, AC, BC, 2>), grid, dim3(512), 0, s, g);
+        else
+            hipLaunchKernelGGL((k_gemm_small<T, AC, BC, 1>), grid, block, 0, s, g);
+    } else if constexpr (sizeof(T) == 2) {
         if (z.tile == 256)
             hipLaunchKernelGGL((k_gemm<T, AC, BC, 256, 256, 2, 2>), grid, block, 0, s, g);
         else
@@ -902,11 +1075,13 @@ hipError_t linear_backward_t(const LinearBackwardCall &c, char *ws, hipStream_t 
     }
     if (c.db) {
         const int blocks = z.db_blocks, per = (int)div_up(c.T, blocks);
-        const bool vec = !padded(c.T, c.n, c.lddz, c.dtype).copy;
+        // (the padded copy, where there is one)
+        const bool vec = D.p || !padded(c.T, c.n, c.lddz, c.dtype).copy;
+        const T *dz = D.p ? reinterpret_cast<const T *>(D.p) : static_cast<const T *>(c.dz);
+        const int64_t ld = D.p ? D.ld / es : c.lddz;
         const dim3 grid((c.n + kSumCols - 1) / kSumCols, blocks);
         auto sum = vec ? k_colsum<T, true> : k_colsum<T, false>;
-        hipLaunchKernelGGL(sum, grid, dim3(256), 0, s, static_cast<const T *>(c.dz), c.lddz, c.T,
-                           c.n, per, part, c.db, c.grad_dtype == 0 ? 1 : 0);
+        hipLaunchKernelGGL(sum, grid, dim3(256), 0, s, dz, ld, c.T, c.n, per, part, c.db, c.grad_dtype == 0 ? 1 : 0);
         if (blocks > 1)
             hipLaunchKernelGGL(k_colsum_join<T>, dim3((c.n + 31) / 32), dim3(256), 0, s, part,
                                blocks, c.n, c.db, c.grad_dtype == 0 ? 1 : 0);
@@ -915,6 +1090,13 @@ hipError_t linear_backward_t(const LinearBackwardCall &c, char *ws, hipStream_t 
 }
 
 }  // namespace
+
+void linear_shape(int M, int N, int K, int dtype, int *tile, int *split)
+{
+    const Product z = product_of(M, N, K, dtype);
+    *tile = z.tile;
+    *split = z.split;
+}
 
 LinearSpace linear_space(int T, int d, int n, int64_t ldx, int64_t ldw, int dtype)
 {

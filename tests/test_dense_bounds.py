@@ -11,8 +11,8 @@ import pytest
 STEP = 128  # bytes of k per step of a row operand
 
 
-def seg_xor(k, es):
-    return (k & 3) << 1 if es == 2 else (k >> 2) & 1
+def seg_xor(k, es, rows):
+    return (k >> 2) & 1 if es == 4 else k & 2 if rows == 64 else (k & 3) << 1
 
 
 def stage(col, es, rows, nth, have, ld, K, k0):
@@ -30,7 +30,7 @@ def stage(col, es, rows, nth, have, ld, K, k0):
         r, c = q // cpr, q % cpr
         if col:
             seg = 2 if es == 2 else 8
-            lc = ((c // seg) ^ seg_xor(r, es)) * seg + c % seg
+            lc = ((c // seg) ^ seg_xor(r, es, rows)) * seg + c % seg
             off = r * ld + lc * 16 if lc * epc < have else None
         else:
             lc = c ^ ((r >> 1) & 7)
@@ -60,20 +60,20 @@ def frag(col, es, rows, i, g, lane):
                 # of its 16 lanes points at, element l & 3
                 src = (lane & ~15) | (4 * j + ((lane & 15) >> 2))
                 k = 8 * (src >> 5) + ((src >> 2) & 3)
-                seg = (2 * i + ((src >> 4) & 1)) ^ seg_xor(k, es)
+                seg = (2 * i + ((src >> 4) & 1)) ^ seg_xor(k, es, rows)
                 at = (k + 4 * half + 16 * g) * rows + seg * 16 + (src & 3) * 4 + (lane & 3)
                 got.append((at // 8, at % 8))
     else:
         for j in range(4):
             k = 4 * (lane >> 5)
-            at = (k + j + 8 * g) * rows + (i ^ seg_xor(k, es)) * 32 + (lane & 31)
+            at = (k + j + 8 * g) * rows + (i ^ seg_xor(k, es, rows)) * 32 + (lane & 31)
             got.append((at // 4, at % 4))
     return got
 
 
 @pytest.mark.parametrize("col", [False, True])
 @pytest.mark.parametrize("es", [2, 4])
-@pytest.mark.parametrize("rows,nth", [(128, 256), (256, 256)])
+@pytest.mark.parametrize("rows,nth", [(64, 256), (128, 256), (256, 256)])
 @pytest.mark.parametrize("have,K,k0", [(10 ** 6, 10 ** 6, 0), (24, 40, 0), (8, 200, 128),
                                        (10 ** 6, 64, 64), (17, 65, 0), (129, 65, 64), (9, 1, 0)])
 def test_fragments_are_the_elements_they_stand_for(col, es, rows, nth, have, K, k0):
@@ -103,7 +103,7 @@ def test_fragments_are_the_elements_they_stand_for(col, es, rows, nth, have, K, 
 
 @pytest.mark.parametrize("es", [2, 4])
 @pytest.mark.parametrize("col", [False, True])
-@pytest.mark.parametrize("rows", [128, 256])
+@pytest.mark.parametrize("rows", [64, 128, 256])
 def test_reads_spread_over_the_banks(col, es, rows):
     """the lanes that the LDS serves together touch 32-bit banks evenly: 8 lanes of
     16 bytes (rows), 32 lanes of 8 bytes (columns, 16-bit types), 64 lanes of 4
@@ -116,12 +116,12 @@ def test_reads_spread_over_the_banks(col, es, rows):
                            for w in range(4)] for p in range(8)]
             elif es == 2:
                 groups = [[((8 * (l >> 5) + ((l >> 2) & 3) + 16 * g) * rows
-                            + ((2 * i + ((l >> 4) & 1)) ^ seg_xor((l >> 2) & 3, 2)) * 16) * 2
+                            + ((2 * i + ((l >> 4) & 1)) ^ seg_xor((l >> 2) & 3, 2, rows)) * 16) * 2
                            + (l & 3) * 8 + 4 * w
                            for l in range(32 * p, 32 * p + 32) for w in range(2)] for p in range(2)]
             else:
                 groups = [[((4 * (l >> 5) + 8 * g) * rows
-                            + (i ^ seg_xor(4 * (l >> 5), 4)) * 32 + (l & 31)) * 4
+                            + (i ^ seg_xor(4 * (l >> 5), 4, rows)) * 32 + (l & 31)) * 4
                            for l in range(64)]]
             for at in groups:
                 banks = [(b // 4) % 64 for b in at]

@@ -51,6 +51,23 @@ def test_linear_null_size_pointer():
         assert L().moe_linear_backward_workspace(8, 8, 8, 8, 8, 8, 0, grads, ctypes.byref(v)) == 1
 
 
+def test_linear_shape():
+    a, b = ctypes.c_int(), ctypes.c_int()
+    A_, B_ = ctypes.byref(a), ctypes.byref(b)
+    for M, N, K, dt in [(0, 8, 8, 0), (8, 0, 8, 0), (8, 8, 0, 0), (8, 8, 8, 3), (8, 8, 2 ** 31 - 1, 0)]:
+        assert L().moe_linear_shape(M, N, K, dt, A_, B_) == 1
+    assert L().moe_linear_shape(8, 8, 8, 0, None, B_) == 1
+    assert L().moe_linear_shape(8, 8, 8, 0, A_, None) == 1
+    # few outputs over a long reduction are cut along it; many outputs are not
+    assert abi.moe_linear_shape(64, 512, 2560, 2)[1] > 1
+    assert abi.moe_linear_shape(32768, 2048, 4096, 2) == (256, 1)
+    for dt in (0, 1, 2):  # the workspace holds the partial sums of what the shape says
+        for T, d, n in [(1, 8, 8), (64, 2560, 512), (4, 4096, 4096), (512, 4096, 2048)]:
+            tile, split = abi.moe_linear_shape(T, n, d, dt)
+            want = split * T * n * 4 if split > 1 else 0
+            assert ws(T, d, n, d, n, dt) == (0, (want + 255) // 256 * 256)
+
+
 #          x  ldx w ldw bias res ldr rdt dt act T   d   n  ws bytes   out ldo odt stream
 # (97 columns: w's rows are copied into padded ones, so a workspace is needed)
 GOOD = [A, 64, A, 97, A, A, 97, 0, 2, 2, 64, 64, 97, A, 1 << 30, A, 97, 0, N]

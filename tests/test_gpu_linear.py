@@ -76,8 +76,30 @@ def test_linear_sizes(T, d, n, dtype):
     check_linear(T, d, n, dtype, "f32")
 
 
-# enough tiles for the large tile in the forward product, dx and dw (16-bit types)
-LARGE = [(3900, 40, 3100), (3841, 200, 3328), (3900, 3100, 40), (40, 3900, 3100), (333, 3841, 3333)]
+# the large tile (16-bit types) in the forward product, in dx and in dw, with ragged
+# edges; cut along k; and the middle tile, whole and cut
+LARGE = [(3900, 400, 3100), (3841, 328, 3329), (3900, 3100, 400), (400, 3900, 3100),
+         (333, 3841, 3333), (700, 2600, 700), (20000, 700, 700)]
+
+
+def test_large_sizes_take_the_tiles_they_stand_for():
+    for dt in (abi.MOE_F16, abi.MOE_BF16):
+        assert abi.moe_linear_shape(3900, 3100, 400, dt) == (256, 1)
+        assert abi.moe_linear_shape(3841, 3329, 328, dt) == (256, 1)
+        tile, split = abi.moe_linear_shape(700, 700, 20000, dt)
+        assert split > 1 and tile >= 128
+        assert abi.moe_linear_shape(333, 3333, 3841, dt)[0] == 128
+        assert abi.moe_linear_shape(40, 60, 100, dt) == (64, 1)
+        assert abi.moe_linear_shape(64, 512, 2560, dt)[0] == 64
+    shapes = {abi.moe_linear_shape(M, N, K, abi.MOE_F32)[0]
+              for M, N, K in [(300, 517, 1003), (1900, 1990, 300), (2000, 700, 3001)]}
+    assert shapes == {64, 128}
+
+
+@pytest.mark.parametrize("T,d,n", [(1900, 300, 1990), (2000, 3001, 700)])
+def test_linear_large_f32(T, d, n):
+    check_linear(T, d, n, "f32", "f32", "silu", residual="f32")
+    check_backward(T, d, n, "f32", "f32")
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
