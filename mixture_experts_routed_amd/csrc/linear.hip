@@ -165,19 +165,21 @@ template <typename T> __device__ __forceinline__ void load8(const T *p, float (&
         }
     }
 }
-template <typename T> __device__ __forceinline__ void store8(T *p, const float (&v)[8])
+template <typename T, bool NT = false>
+__device__ __forceinline__ void store8(T *p, const float (&v)[8])
 {
     if constexpr (sizeof(T) == 2) {
-        Vec<T, 8>::store(p, v);
+        Vec<T, 8>::template store<NT>(p, v);
     } else {
         const float a[4] = {v[0], v[1], v[2], v[3]}, b[4] = {v[4], v[5], v[6], v[7]};
-        Vec<T, 4>::store(p, a);
-        Vec<T, 4>::store(p + 4, b);
+        Vec<T, 4>::template store<NT>(p, a);
+        Vec<T, 4>::template store<NT>(p + 4, b);
     }
 }
 
-// columns c .. c + 7 of row r (those below N); c is a multiple of 8
-template <typename T>
+// columns c .. c + 7 of row r (those below N); c is a multiple of 8. NT: whole
+// chunks are stored non-temporally (outputs that are larger than the caches)
+template <typename T, bool NT = false>
 __device__ __forceinline__ void finish8(const Epilogue &e, int64_t r, int c, int N, float (&v)[8])
 {
     const int64_t ro = r * e.ldo + c, rr = r * e.ldr + c;
@@ -215,9 +217,9 @@ __device__ __forceinline__ void finish8(const Epilogue &e, int64_t r, int c, int
     }
     if (whole) {
         if (e.out_f32)
-            store8<float>(static_cast<float *>(e.out) + ro, v);
+            store8<float, NT>(static_cast<float *>(e.out) + ro, v);
         else
-            store8<T>(static_cast<T *>(e.out) + ro, v);
+            store8<T, NT>(static_cast<T *>(e.out) + ro, v);
         return;
     }
 #pragma unroll
@@ -432,12 +434,14 @@ __global__ __launch_bounds__(256, (BM + BN > 256 ? 1 : 2)) void k_gemm(const Gem
     b.init(p.B, p.ldb, tn * BN, BC ? p.b_cols : p.N, BC ? p.K : p.b_cols, s0 * BK, tid, wn * TN);
 
     float16_t acc[TM][TN];
+    auto clear = [&]() {
 #pragma unroll
-    for (int i = 0; i < TM; ++i)
+        for (int i = 0; i < TM; ++i)
 #pragma unroll
-        for (int j = 0; j < TN; ++j)
+            for (int j = 0; j < TN; ++j)
 #pragma unroll
-            for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
+                for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
+    };
 
     // LDS: three steps of A, then two of B
     const uint32_t base = lds_at(lds), base_b = base + 3 * OpA::BYTES;
@@ -504,6 +508,8 @@ __global__ __launch_bounds__(256, (BM + BN > 256 ? 1 : 2)) void k_gemm(const Gem
         all_a(base + OpA::BYTES);
         all_b(base_b + OpB::BYTES);
         all_a(base + 2 * OpA::BYTES);
+        clear();  // (while the loads are on their way)
+        __builtin_amdgcn_sched_barrier(0);
         asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier"
                      :
                      : "n"(2 * OpA::LOADS + OpB::LOADS)
@@ -535,6 +541,8 @@ __global__ __launch_bounds__(256, (BM + BN > 256 ? 1 : 2)) void k_gemm(const Gem
         // matrix results readable
         asm volatile("s_nop 15\n\ts_nop 15\n\ts_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
         __builtin_amdgcn_sched_barrier(0);
+    } else {
+        clear();
     }
 
     const int row0 = tm * BM + wm * TM * 32, col0 = tn * BN + wn * TN * 32;
@@ -587,7 +595,7 @@ __global__ __launch_bounds__(256, (BM + BN > 256 ? 1 : 2)) void k_gemm(const Gem
             if (m >= p.M || n >= p.N) continue;
             float v[8];
             load8<float>(mine + r * PITCH + (lane % LPR) * 8, v);
-            finish8<T>(p.e, m, n, p.N, v);
+            finish8<T, BIG>(p.e, m, n, p.N, v);
         }
     }
 }

@@ -36,12 +36,16 @@ template <typename T, int N> struct Vec {
 #pragma unroll
         for (int i = 0; i < N; ++i) v[i] = to_f32(x[i]);
     }
+    template <bool NT = false>  // NT: non-temporal
     static __device__ __forceinline__ void store(T *p, const float (&v)[N])
     {
         type x;
 #pragma unroll
         for (int i = 0; i < N; ++i) x[i] = from_f32<T>(v[i]);
-        *reinterpret_cast<type *>(p) = x;
+        if constexpr (NT)
+            __builtin_nontemporal_store(x, reinterpret_cast<type *>(p));
+        else
+            *reinterpret_cast<type *>(p) = x;
     }
 };
 
