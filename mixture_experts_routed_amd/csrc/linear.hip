@@ -115,6 +115,7 @@ struct Epilogue {
     int64_t ldr, ldo;
     int res_f32, out_f32, act;
     int vec;               // rows of out and residual start at 16-byte boundaries
+    int plain;             // vec, and no bias, activation or residual
 };
 
 struct GemmArg {
@@ -124,7 +125,8 @@ struct GemmArg {
     int a_cols, b_cols;  // length of an operand's rows as they lie (whole 16-byte chunks), elements
     int mt, nt;          // tiles
     int split, steps;    // K splits, K-steps per split
-    float *part;         // split > 1: partial planes [split][M][N]
+    float *part;         // split > 1: partial planes [split][M][pitch]
+    int pitch;           // N rounded up to whole chunks of 8
     Epilogue e;
 };
 
@@ -232,6 +234,16 @@ __device__ __forceinline__ void finish8(const Epilogue &e, int64_t r, int c, int
         }
 }
 
+// the same for whole chunks without bias, activation and residual
+template <typename T, bool NT>
+__device__ __forceinline__ void store_plain(const Epilogue &e, int64_t r, int c, const float (&v)[8])
+{
+    if (e.out_f32)
+        store8<float, NT>(static_cast<float *>(e.out) + r * e.ldo + c, v);
+    else
+        store8<T, NT>(static_cast<T *>(e.out) + r * e.ldo + c, v);
+}
+
 // LDS byte address of a shared object
 __device__ __forceinline__ uint32_t lds_at(const void *p)
 {
@@ -243,27 +255,34 @@ __device__ __forceinline__ uint32_t lds_at(const void *p)
 #endif
 }
 
-typedef int int4v __attribute__((ext_vector_type(4)));
-
-// Buffer resource words (as buffer_of). A range of 0 bytes makes every load zeros.
-__device__ __forceinline__ int4v rsrc_of(const char *base, uint32_t bytes)
+// A buffer resource (as buffer_of) in two halves: base address; range in bytes
+// and the raw-buffer word. A range of 0 bytes makes every load zeros.
+struct Rsrc {
+    uint64_t lo, hi;
+};
+__device__ __forceinline__ Rsrc rsrc_of(const char *base, uint32_t bytes)
 {
-    const uint64_t a = reinterpret_cast<uint64_t>(base);
-    return int4v{(int)(uint32_t)a, (int)((uint32_t)(a >> 32) & 0xffffu), (int)bytes, 0x00020000};
+    return Rsrc{reinterpret_cast<uint64_t>(base) & 0xffffffffffffull,
+                (uint64_t)bytes | (0x00020000ull << 32)};
 }
 
 // 64 lanes x 16 bytes from the buffer at each lane's `off` to LDS at `to` + 16 lane;
 // counted by vmcnt, which the compiler does not know of here. Sets m0, which
-// nothing else in these kernels uses (a clobber of it cannot be declared).
-__device__ __forceinline__ void load_to_lds(uint32_t to, uint32_t off, int4v rsrc)
+// nothing else in these kernels uses (a clobber of it cannot be declared). The
+// compiler does not see a buffer load here and keeps no wait states before it:
+// a resource word that a vector instruction has just written may be read by a
+// scalar move, not by a buffer load, so it goes through s[96:99]; the moves are
+// also the wait state that the load needs behind m0.
+__device__ __forceinline__ void load_to_lds(uint32_t to, uint32_t off, const Rsrc &r)
 {
 #ifdef __HIP_DEVICE_COMPILE__
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+    asm volatile("s_mov_b32 m0, %0\n\ts_mov_b64 s[96:97], %2\n\ts_mov_b64 s[98:99], %3\n\t"
+                 "buffer_load_dwordx4 %1, s[96:99], 0 offen lds"
                  :
-                 : "s"(to), "v"(off), "s"(rsrc)
-                 : "memory");
+                 : "s"(to), "v"(off), "s"(r.lo), "s"(r.hi)
+                 : "memory", "s96", "s97", "s98", "s99");
 #else
-    (void)to, (void)off, (void)rsrc;
+    (void)to, (void)off, (void)r;
 #endif
 }
 
@@ -445,19 +464,12 @@ __global__ __launch_bounds__(256, (BM + BN > 256 ? 1 : 2)) void k_gemm(const Gem
 
     // LDS: three steps of A, then two of B
     const uint32_t base = lds_at(lds), base_b = base + 3 * OpA::BYTES;
-    // (a resource word may come from a vector instruction: 5 wait states)
     auto load_a = [&](uint32_t to, int i) {
-        if (i == 0) {
-            a.advance();
-            asm volatile("s_nop 4" ::: "memory");
-        }
+        if (i == 0) a.advance();
         a.issue(to, i, wave);
     };
     auto load_b = [&](uint32_t to, int i) {
-        if (i == 0) {
-            b.advance();
-            asm volatile("s_nop 4" ::: "memory");
-        }
+        if (i == 0) b.advance();
         b.issue(to, i, wave);
     };
     // fragments of the four k-groups, read in the order in which they are needed
@@ -494,7 +506,7 @@ __global__ __launch_bounds__(256, (BM + BN > 256 ? 1 : 2)) void k_gemm(const Gem
             __builtin_amdgcn_sched_barrier(0);
         }
     };
-    if (s0 < s1) {
+    {  // (every range of k has a step)
         auto all_a = [&](uint32_t to) {
 #pragma unroll
             for (int i = 0; i < OpA::LOADS; ++i) load_a(to, i);
@@ -541,13 +553,11 @@ __global__ __launch_bounds__(256, (BM + BN > 256 ? 1 : 2)) void k_gemm(const Gem
         // matrix results readable
         asm volatile("s_nop 15\n\ts_nop 15\n\ts_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
         __builtin_amdgcn_sched_barrier(0);
-    } else {
-        clear();
     }
 
     const int row0 = tm * BM + wm * TM * 32, col0 = tn * BN + wn * TN * 32;
     if (p.split > 1) {
-        float *plane = p.part + (int64_t)split * p.M * p.N;
+        float *plane = p.part + (int64_t)split * p.M * p.pitch;
 #pragma unroll
         for (int i = 0; i < TM; ++i) {
             const int m = row0 + i * 32 + (lane & 31);
@@ -556,16 +566,10 @@ __global__ __launch_bounds__(256, (BM + BN > 256 ? 1 : 2)) void k_gemm(const Gem
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
                     const int n = col0 + j * 32 + 8 * q + 4 * (lane >> 5);
-                    if (m >= p.M || n >= p.N) continue;
-                    float *o = plane + (int64_t)m * p.N + n;
                     const float16_t &c = acc[i][j];
-                    const float4_t v = {c[4 * q], c[4 * q + 1], c[4 * q + 2], c[4 * q + 3]};
-                    if (n + 4 <= p.N && (p.N & 3) == 0)
-                        *reinterpret_cast<float4_t *>(o) = v;
-                    else
-#pragma unroll
-                        for (int r = 0; r < 4; ++r)
-                            if (n + r < p.N) o[r] = v[r];
+                    if (m < p.M && n < p.pitch)
+                        *reinterpret_cast<float4_t *>(plane + (int64_t)m * p.pitch + n) =
+                            float4_t{c[4 * q], c[4 * q + 1], c[4 * q + 2], c[4 * q + 3]};
                 }
         }
         return;
@@ -589,13 +593,23 @@ __global__ __launch_bounds__(256, (BM + BN > 256 ? 1 : 2)) void k_gemm(const Gem
                         float4_t{c[4 * q], c[4 * q + 1], c[4 * q + 2], c[4 * q + 3]};
                 }
         // (LDS operations of one wavefront stay in order)
-#pragma unroll 2
-        for (int r = lane / LPR; r < RG * 32; r += 64 / LPR) {
-            const int m = row0 + h * 32 + r, n = col0 + (lane % LPR) * 8;
-            if (m >= p.M || n >= p.N) continue;
+        const int n = col0 + (lane % LPR) * 8;
+        auto one = [&](int r, bool plain) __attribute__((always_inline)) {
+            const int m = row0 + h * 32 + r;
+            if (m >= p.M || n >= p.N) return;
             float v[8];
             load8<float>(mine + r * PITCH + (lane % LPR) * 8, v);
-            finish8<T, BIG>(p.e, m, n, p.N, v);
+            if (plain)
+                store_plain<T, BIG>(p.e, m, n, v);
+            else
+                finish8<T, BIG>(p.e, m, n, p.N, v);
+        };
+        if (p.e.plain && n + 8 <= p.N) {
+#pragma unroll 4
+            for (int r = lane / LPR; r < RG * 32; r += 64 / LPR) one(r, true);
+        } else {
+#pragma unroll 2
+            for (int r = lane / LPR; r < RG * 32; r += 64 / LPR) one(r, false);
         }
     }
 }
@@ -648,13 +662,12 @@ __global__ __launch_bounds__(256 * TEAMS, 2) void k_gemm_small(const GemmArg p)
     auto load = [&](uint32_t to) {
         a.advance();
         b.advance();
-        asm volatile("s_nop 4" ::: "memory");
 #pragma unroll
         for (int i = 0; i < OpA::LOADS; ++i) a.issue(to, i, wave);
 #pragma unroll
         for (int i = 0; i < OpB::LOADS; ++i) b.issue(to + OpA::BYTES, i, wave);
     };
-    if (rounds > 0) {
+    {  // (every range of k has a step)
         uint32_t rd = base, wr = base;
 #pragma unroll
         for (int q = 0; q < NB - 1; ++q) {
@@ -693,7 +706,7 @@ __global__ __launch_bounds__(256 * TEAMS, 2) void k_gemm_small(const GemmArg p)
     constexpr int PITCH = kSmall + 4, PART = 32 * PITCH, PARTS = 4 * TEAMS;
     static_assert(PARTS * PART * 4 <= (int)(TEAMS * NB * BUF), "fits");
     float *f = reinterpret_cast<float *>(lds);
-    float *plane = p.part + (int64_t)split * p.M * p.N;
+    float *plane = p.part + (int64_t)split * p.M * p.pitch;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         if (i) __syncthreads();
@@ -718,13 +731,7 @@ __global__ __launch_bounds__(256 * TEAMS, 2) void k_gemm_small(const GemmArg p)
                 for (int k = 0; k < 8; ++k) v[k] += q[k];
             }
             if (p.split > 1) {
-                float *o = plane + (int64_t)m * p.N + n;
-                if (n + 8 <= p.N && (p.N & 3) == 0)
-                    store8<float>(o, v);
-                else
-#pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        if (n + k < p.N) o[k] = v[k];
+                store8<float>(plane + (int64_t)m * p.pitch + n, v);
             } else {
                 finish8<T>(p.e, m, n, p.N, v);
             }
@@ -736,23 +743,20 @@ __global__ __launch_bounds__(256 * TEAMS, 2) void k_gemm_small(const GemmArg p)
 // one thread per 8 columns of a row.
 template <typename T>
 __global__ __launch_bounds__(256) void k_gemm_reduce(const float *__restrict__ part, int M, int N,
-                                                     int split, const Epilogue e)
+                                                     int pitch, int split, const Epilogue e)
 {
-    const int per = (N + 7) / 8;
-    const int64_t total = (int64_t)M * per;
+    const int per = pitch / 8;
+    const int64_t total = (int64_t)M * per, plane = (int64_t)M * pitch;
     for (int64_t q = (int64_t)blockIdx.x * 256 + threadIdx.x; q < total;
          q += (int64_t)gridDim.x * 256) {
         const int64_t r = q / per;
         const int c = (int)(q - r * per) * 8;
         float v[8] = {};
-        const float *s = part + r * N + c;
-        for (int i = 0; i < split; ++i, s += (int64_t)M * N) {
+        const float *s = part + r * pitch + c;
+#pragma unroll 4
+        for (int i = 0; i < split; ++i) {
             float z[8];
-            if (c + 8 <= N && (N & 3) == 0)
-                load8<float>(s, z);
-            else
-#pragma unroll
-                for (int j = 0; j < 8; ++j) z[j] = c + j < N ? s[j] : 0.f;
+            load8<float>(s + i * plane, z);
 #pragma unroll
             for (int j = 0; j < 8; ++j) v[j] += z[j];
         }
@@ -918,7 +922,7 @@ Product product_of(int64_t M, int64_t N, int64_t K, int dtype)
     }
     z.steps = (int)up(div_up(steps, z.split), 2);  // (whole rounds of two teams)
     z.split = (int)div_up(steps, z.steps);
-    z.part_bytes = z.split > 1 ? up((int64_t)z.split * M * N * 4, 256) : 0;
+    z.part_bytes = z.split > 1 ? up((int64_t)z.split * M * up(N, 8) * 4, 256) : 0;
     return z;
 }
 
@@ -992,7 +996,9 @@ hipError_t launch_product(const Matrix &A, const Matrix &B, int M, int N, int K,
     g.split = z.split;
     g.steps = z.steps;
     g.part = part;
+    g.pitch = (int)up(N, 8);
     g.e = e;
+    g.e.plain = e.vec && !e.bias && !e.residual && e.act == kActNone;
     const dim3 grid((unsigned)up(z.mt * z.nt * z.split, 8)), block(256);
     if (z.tile == kSmall) {
         if (z.mt * z.nt * z.split <= 256)
@@ -1008,9 +1014,9 @@ hipError_t launch_product(const Matrix &A, const Matrix &B, int M, int N, int K,
         hipLaunchKernelGGL((k_gemm<T, AC, BC, 128, 128, 2, 2>), grid, block, 0, s, g);
     }
     if (z.split > 1) {
-        const int64_t parts = (int64_t)M * ((N + 7) / 8);
+        const int64_t parts = (int64_t)M * (g.pitch / 8);
         const dim3 rgrid((unsigned)(parts / 256 + 1 < 8192 ? parts / 256 + 1 : 8192));
-        hipLaunchKernelGGL(k_gemm_reduce<T>, rgrid, dim3(256), 0, s, part, M, N, z.split, e);
+        hipLaunchKernelGGL(k_gemm_reduce<T>, rgrid, dim3(256), 0, s, part, M, N, g.pitch, z.split, e);
     }
     return hipGetLastError();
 }
