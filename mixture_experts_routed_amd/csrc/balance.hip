@@ -321,17 +321,19 @@ __global__ __launch_bounds__(256) void k_balance_join(int blocks, int E, const B
     if (!s_last) return;
     __threadfence();
     // (at most 64 workgroups here: E <= 1024)
+    float *terms = &s_p[0][0];
+    int *counts = &s_c[0][0];
     if (tid < (int)gridDim.x) {
-        s_p[0][tid] = __hip_atomic_load(w.term + tid, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        s_c[0][tid] = __hip_atomic_load(w.entries + tid, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        terms[tid] = __hip_atomic_load(w.term + tid, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        counts[tid] = __hip_atomic_load(w.entries + tid, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     }
     __syncthreads();
     if (tid) return;
     double term = 0.;
     int64_t entries = 0;
     for (unsigned b = 0; b < gridDim.x; ++b) {
-        term += (&s_p[0][0])[b];
-        entries += (&s_c[0][0])[b];
+        term += terms[b];
+        entries += counts[b];
     }
     write_losses(E, term, entries, s_z[0], nt, cnt, loss);
 }
