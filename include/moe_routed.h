@@ -517,7 +517,7 @@ enum moe_act { MOE_ACT_NONE = 0, MOE_ACT_RELU = 1, MOE_ACT_SILU = 2, MOE_ACT_GEL
  *      d x n over T. Errors: MOE_EINVAL for a size < 1, a bad dtype, NULL.
  * Errors: MOE_EINVAL for T, d or n < 1, a stride below the row length or above
  *      2^20, a bad dtype or act, NULL or misaligned pointers, a small
- *      workspace, more than 2^31 tiles of 64 x 64; MOE_EHIP on a failed launch.
+ *      workspace, a product of more than 2^23 tiles (moe_linear_shape); MOE_EHIP on a failed launch.
  */
 int moe_linear_shape(int M, int N, int K, int dtype, int *tile, int *split);
 int moe_linear_workspace(int T, int d, int n, int64_t ldx, int64_t ldw, int dtype, size_t *bytes);

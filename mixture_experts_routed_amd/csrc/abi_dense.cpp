@@ -22,9 +22,6 @@ int linear_sizes(int T, int d, int n, int64_t ldx, int64_t ldw, int dtype)
 {
     if (T < 1 || d < 1 || n < 1 || T > kI32Max - 1024 || !dtype_ok(dtype)) return MOE_EINVAL;
     if (!rows_ok(d, ldx) || !rows_ok(n, ldw)) return MOE_EINVAL;
-    // workgroups of the largest product (64 x 64 tiles)
-    const int64_t t = ((int64_t)T + 63) / 64, a = (d + 63) / 64, b = (n + 63) / 64;
-    if (t * (a > b ? a : b) > kI32Max - 1024) return MOE_EINVAL;
     return MOE_OK;
 }
 
@@ -49,6 +46,7 @@ int moe_linear_workspace(int T, int d, int n, int64_t ldx, int64_t ldw, int dtyp
 {
     if (!bytes) return MOE_EINVAL;
     const int rc = linear_sizes(T, d, n, ldx, ldw, dtype);
+    if (rc == MOE_OK && !moe::linear_fits(T, n, d, dtype)) return MOE_EINVAL;
     if (rc == MOE_OK) *bytes = (size_t)moe::linear_space(T, d, n, ldx, ldw, dtype).total;
     return rc;
 }
@@ -105,6 +103,9 @@ int moe_linear_backward_workspace(int T, int d, int n, int64_t ldx, int64_t ldw,
                                 dtype);
     if (rc != MOE_OK) return rc;
     if (!rows_ok(n, lddz)) return MOE_EINVAL;
+    if ((grads & MOE_GRAD_X && !moe::linear_fits(T, d, n, dtype)) ||
+        (grads & MOE_GRAD_W && !moe::linear_fits(d, n, T, dtype)))
+        return MOE_EINVAL;
     *bytes = (size_t)moe::linear_backward_space(T, d, n, ldx, ldw, lddz, dtype,
                                                 grads & MOE_GRAD_X, grads & MOE_GRAD_W,
                                                 grads & MOE_GRAD_BIAS)

@@ -154,6 +154,8 @@ struct LinearBackwardSpace {
 };
 // tile (rows and columns of a workgroup) and splits along K of an M x N product over K
 void linear_shape(int M, int N, int K, int dtype, int *tile, int *split);
+// whether it is one launch: at most 2^23 workgroups
+bool linear_fits(int M, int N, int K, int dtype);
 LinearSpace linear_space(int T, int d, int n, int64_t ldx, int64_t ldw, int dtype);
 LinearBackwardSpace linear_backward_space(int T, int d, int n, int64_t ldx, int64_t ldw,
                                           int64_t lddz, int dtype, bool dx, bool dw, bool db);

@@ -893,7 +893,7 @@ double product_us(int64_t M, int64_t N, int64_t steps, int dtype, int tile, int6
     } else {
         const double c = dtype == 0 ? (tile == 64 ? 0.6 : 1.9)
                          : tile == 64 ? 0.2 + 0.1 * full : 0.42 + 0.12 * full;
-        const double c2 = dtype == 0 ? 2 * c : tile == 64 ? 0.5 : 1.1;
+        const double c2 = dtype == 0 ? 2 * c : tile == 64 ? 0.5 : 1.05;
         t = (tile == 64 ? 4.5 : 6) +
             (wgs <= 256 ? n * c : (double)div_up((int64_t)wgs, 512) * (1 + n * c2));
     }
@@ -1055,7 +1055,7 @@ template <typename T>
 hipError_t linear_backward_t(const LinearBackwardCall &c, char *ws, hipStream_t s)
 {
     const LinearBackwardSpace z = linear_backward_space(
-        c.T, c.d, c.n, c.dx || c.dw ? c.ldx : c.d, c.ldw, c.lddz, c.dtype, c.dx, c.dw, c.db);
+        c.T, c.d, c.n, c.ldx, c.ldw, c.lddz, c.dtype, c.dx, c.dw, c.db);
     const int es = elem_size(c.dtype);
     Matrix X{}, W{}, D{};
     hipError_t rc = hipSuccess;
@@ -1104,6 +1104,13 @@ hipError_t linear_backward_t(const LinearBackwardCall &c, char *ws, hipStream_t 
 }
 
 }  // namespace
+
+// (a launch's threads, at most 512 a workgroup, are counted in 32 bits)
+bool linear_fits(int M, int N, int K, int dtype)
+{
+    const Product z = product_of(M, N, K, dtype);
+    return z.mt * z.nt * z.split <= ((int64_t)1 << 23) - 8;
+}
 
 void linear_shape(int M, int N, int K, int dtype, int *tile, int *split)
 {

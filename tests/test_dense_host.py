@@ -43,6 +43,19 @@ def test_linear_sizes_refused(T, d, n, ldx, ldw, dtype):
     assert L().moe_linear_backward_workspace(T, d, n, ldx, ldw, n, dtype, 7, ctypes.byref(v)) == 1
 
 
+def test_products_of_too_many_tiles_are_refused():
+    """2^23 workgroups are one launch: a tall product of one column is served up to there"""
+    T = 2 ** 31 - 2048
+    tile, split = abi.moe_linear_shape(T, 1, 8, 2)
+    rc = ws(T, 8, 1, 8, 1, 2)[0]
+    assert rc == (0 if -(-T // tile) * split <= 2 ** 23 - 8 else 1)
+    assert ws(T, 8, 4096, 8, 4096, 2)[0] == 1          # 2^23 x 16 tiles
+    v = ctypes.c_size_t()
+    back = L().moe_linear_backward_workspace
+    assert back(T, 4096, 8, 4096, 8, 8, 2, 1, ctypes.byref(v)) == 1   # dx
+    assert back(T, 4096, 8, 4096, 8, 8, 2, 2, ctypes.byref(v)) == 0   # dw: few tiles, a long sum
+
+
 def test_linear_null_size_pointer():
     assert L().moe_linear_workspace(8, 8, 8, 8, 8, 0, None) == 1
     assert L().moe_linear_backward_workspace(8, 8, 8, 8, 8, 8, 0, 7, None) == 1
