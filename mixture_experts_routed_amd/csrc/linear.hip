@@ -806,7 +806,8 @@ __global__ __launch_bounds__(256) void k_colsum(const T *__restrict__ dz, int64_
         for (int64_t r = r0 + rg; r < r1; r += 8) {
             const T *p = dz + r * ld + c;
             float q[8];
-            if (VEC) {
+            // (fp32 rows of whole chunks may end 4 columns into these 8)
+            if (VEC && (sizeof(T) == 2 || c + 8 <= n)) {
                 load8<T>(p, q);
             } else {
 #pragma unroll

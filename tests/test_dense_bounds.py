@@ -126,3 +126,20 @@ def test_reads_spread_over_the_banks(col, es, rows):
             for at in groups:
                 banks = [(b // 4) % 64 for b in at]
                 assert len(set(banks)) == len(banks)
+
+
+@pytest.mark.parametrize("es", [2, 4])
+def test_column_sums_read_only_their_rows(es):
+    """a thread of the column sums takes 8 columns of a row: in one piece where they are
+    all there (16-bit rows end with a whole chunk of 8, fp32 rows with one of 4)"""
+    epc = 16 // es
+    for n in list(range(epc, 40, epc)) + [256 - epc, 256, 256 + epc, 264]:
+        seen = set()
+        for c in range(0, -(-n // 256) * 256, 8):
+            if c >= n:
+                continue
+            whole = es == 2 or c + 8 <= n
+            cols = [c + i for i in range(8) if whole or c + i < n]
+            assert max(cols) < n
+            seen.update(cols)
+        assert seen == set(range(n))

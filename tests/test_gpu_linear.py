@@ -218,6 +218,13 @@ def test_linear_backward_in_part(grads):
     check_backward(50, 96, 61, "bf16", "f32", 0, grads)
 
 
+@pytest.mark.parametrize("T,n", [(1, 4), (7, 12), (900, 252), (130, 260)])
+def test_bias_gradient_of_rows_that_end_in_half_a_piece(T, n):
+    """fp32 rows of whole 16-byte chunks that are not whole pieces of 8 columns"""
+    check_backward(T, 8, n, "f32", "f32", 0, ("db",))
+    check_backward(T, 8, n, "f32", "f32", 4)
+
+
 def test_linear_backward_is_the_difference_quotient():
     """<dz, z(x + h v) - z(x - h v)> / 2h = <dx, v>, and so for w: z is linear, so
     what is left is 32-bit rounding of z (2^-24 |z| over h, with h = 1/4)"""
