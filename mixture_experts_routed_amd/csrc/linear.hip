@@ -592,7 +592,8 @@ __global__ __launch_bounds__(256, (BM + BN > 256 ? 1 : 2)) void k_gemm(const Gem
                                                   8 * q + 4 * (lane >> 5)) =
                         float4_t{c[4 * q], c[4 * q + 1], c[4 * q + 2], c[4 * q + 3]};
                 }
-        // (LDS operations of one wavefront stay in order)
+        // (LDS operations of one wavefront stay in order; the compiler keeps it)
+        asm volatile("" ::: "memory");
         const int n = col0 + (lane % LPR) * 8;
         auto one = [&](int r, bool plain) __attribute__((always_inline)) {
             const int m = row0 + h * 32 + r;
@@ -611,6 +612,7 @@ __global__ __launch_bounds__(256, (BM + BN > 256 ? 1 : 2)) void k_gemm(const Gem
 #pragma unroll 2
             for (int r = lane / LPR; r < RG * 32; r += 64 / LPR) one(r, false);
         }
+        asm volatile("" ::: "memory");
     }
 }
 
