@@ -491,6 +491,9 @@ int moe_forward_packed_noalloc(const void *x, const int32_t *ids, const float *w
  *  - a workspace is needed only where its size is not 0 (then 256-byte
  *    aligned); it starts with any contents, and calls that may overlap need
  *    one each;
+ *  - an output overlaps no other argument, but where a call names one that it
+ *    may be: then it is that array itself, from its first element and with its
+ *    stride (otherwise MOE_EINVAL where the addresses are equal);
  *  - results do not depend on timing: the same call gives the same bits.
  */
 
@@ -517,7 +520,8 @@ enum moe_act { MOE_ACT_NONE = 0, MOE_ACT_RELU = 1, MOE_ACT_SILU = 2, MOE_ACT_GEL
  *      d x n over T. Errors: MOE_EINVAL for a size < 1, a bad dtype, NULL.
  * Errors: MOE_EINVAL for T, d or n < 1, a stride below the row length or above
  *      2^20, a bad dtype or act, NULL or misaligned pointers, a small
- *      workspace, a product of more than 2^23 tiles (moe_linear_shape); MOE_EHIP on a failed launch.
+ *      workspace, a product of more than 2^23 tiles (moe_linear_shape);
+ *      MOE_EHIP on a failed launch.
  */
 int moe_linear_shape(int M, int N, int K, int dtype, int *tile, int *split);
 int moe_linear_workspace(int T, int d, int n, int64_t ldx, int64_t ldw, int dtype, size_t *bytes);
@@ -599,7 +603,7 @@ int moe_route_backward(const float *logits, const int32_t *ids, const float *w, 
  * relative error is at most 2^-4 for magnitudes of at least 2^(e-6), and below
  * that the absolute error is at most 2^(e-10).
  * In:  g, u [T][f] of dtype, strides ldg, ldu. act: not MOE_ACT_NONE.
- * Out: h [T][f] of dtype, stride ldh; g8 [T][f] codes and gs [T][ceil(f / 32)]
+ * Out: h [T][f] of dtype, stride ldh (may be g or u itself); g8 [T][f] codes and gs [T][ceil(f / 32)]
  *      scales, contiguous (g8 16-byte aligned); u8 and us likewise, given
  *      exactly when g8 and u are.
  * Errors: MOE_EINVAL for T or f < 1, a bad stride, dtype or act, NULL or
@@ -609,7 +613,8 @@ int moe_route_backward(const float *logits, const int32_t *ids, const float *w, 
  * and dh [T][f] of dtype:
  *   dg = dh * u * act'(g),  du = dh * act(g),  h = act(g) * u
  * (u8, us and du NULL: dg = dh * act'(g), h = act(g)). relu'(0) = 0.
- * h may be NULL; it is the operand x of the following product's dw. Errors: as above.
+ * h may be NULL; it is the operand x of the following product's dw. One of dg,
+ * du and h may be dh itself. Errors: as above.
  */
 #define MOE_ACT8_BLOCK 32
 int moe_act_forward(const void *g, int64_t ldg, const void *u, int64_t ldu, int dtype, int act,

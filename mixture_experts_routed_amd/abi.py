@@ -677,7 +677,7 @@ def route_backward(logits, ids, w, dw, cnt, dloss, out_dtype=None, out=None, str
 
 
 def act_forward(g, u=None, act: str = "silu", ckpt=None, h=None, stream=None):
-    """h = act(g) * u (or act(g)) for matrices [T, f]. ckpt: None (nothing kept), True (a
+    """h = act(g) * u (or act(g)) for matrices [T, f]; h may be g or u itself. ckpt: None (nothing kept), True (a
     new 8-bit checkpoint) or an earlier call's, which is overwritten. Returns (h, ckpt);
     a checkpoint is a dict of e4m3 codes g8, u8 [T, f] and scale bytes gs, us [T,
     ceil(f / 32)], code * 2^(scale - 127) the values they stand for."""
@@ -703,7 +703,8 @@ def act_forward(g, u=None, act: str = "silu", ckpt=None, h=None, stream=None):
 def act_backward(ckpt, dh, act: str = "silu", dg=None, du=None, h=None, need_h: bool = True,
                  stream=None):
     """From act_forward()'s checkpoint and dh [T, f]: a dict of dg, du (if there was a u) and
-    h, the forward's output as the checkpoint gives it (not with need_h=False)."""
+    h, the forward's output as the checkpoint gives it (not with need_h=False). One of
+    them may be dh itself."""
     with _On(dh, "dh", stream) as at:
         dev, D = at.index, dh.dtype
         T, f = _matrix_shape(dh, "dh")

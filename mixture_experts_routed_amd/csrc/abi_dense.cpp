@@ -18,6 +18,15 @@ bool result_ok(int dtype, int operand) { return dtype == MOE_F32 || dtype == ope
 
 bool act_ok(int act, int first) { return act >= first && act <= MOE_ACT_GELU; }
 
+// an output that may be one of the inputs: element by element, so with the same stride
+bool in_place_ok(const void *out, int64_t ldo, const void *in, int64_t ldi, int T)
+{
+    return !in || out != in || ldo == ldi || T == 1;
+}
+
+// outputs that are asked for lie apart
+bool apart(const void *a, const void *b) { return !a || a != b; }
+
 int linear_sizes(int T, int d, int n, int64_t ldx, int64_t ldw, int dtype)
 {
     if (T < 1 || d < 1 || n < 1 || T > kI32Max - 1024 || !dtype_ok(dtype)) return MOE_EINVAL;
@@ -74,6 +83,8 @@ int moe_linear(const void *x, int64_t ldx, const void *w, int64_t ldw, const voi
     if (!aligned(x, 16) || !aligned(w, 16) || !aligned(out, 16) || !aligned_or_null(bias, 16) ||
         !aligned_or_null(residual, 16) || !workspace_ok(workspace, ws_bytes, need))
         return MOE_EINVAL;
+    if (out == x || out == w || out == bias) return MOE_EINVAL;
+    if (out == residual && (residual_dtype != out_dtype || (ldr != ldo && T > 1))) return MOE_EINVAL;
     moe::LinearCall c;
     c.x = x;
     c.w = w;
@@ -127,6 +138,9 @@ int moe_linear_backward(const void *x, int64_t ldx, const void *w, int64_t ldw, 
     if (dw && (!aligned(dw, 16) || !aligned(x, 16) || !rows_ok(n, lddw))) return MOE_EINVAL;
     if (db && !aligned(db, 16)) return MOE_EINVAL;
     if ((dw || db) && !result_ok(grad_dtype, dtype)) return MOE_EINVAL;
+    for (const void *p : {(const void *)dx, (const void *)dw, (const void *)db})
+        if (p && (p == dz || (dw && p == x) || (dx && p == w))) return MOE_EINVAL;
+    if (!apart(dx, dw) || !apart(dx, db) || !apart(dw, db)) return MOE_EINVAL;
     moe::LinearBackwardCall c;
     c.x = x;
     c.w = w;
@@ -180,7 +194,7 @@ int moe_route_backward(const float *logits, const int32_t *ids, const float *w, 
     if (!dtype_ok(dtype) || (!dw && !dloss)) return MOE_EINVAL;
     if (!aligned(logits, 4) || !aligned(ids, 4) || !aligned(cnt, 4) ||
         !aligned(dlogits, (size_t)elem_bytes(dtype)) || !aligned_or_null(dw, 4) ||
-        !aligned_or_null(dloss, 4) || (dw && !aligned(w, 4)))
+        !aligned_or_null(dloss, 4) || (dw && !aligned(w, 4)) || dlogits == logits)
         return MOE_EINVAL;
     return moe::launch_route_backward(logits, ids, w, dw, cnt, dloss, T, E, K, dlogits, dtype,
                                       as_stream(stream)) == hipSuccess
@@ -200,6 +214,9 @@ int moe_act_forward(const void *g, int64_t ldg, const void *u, int64_t ldu, int 
     if ((gs != nullptr) != keep || (u8 != nullptr) != (keep && u) || (us != nullptr) != (keep && u))
         return MOE_EINVAL;
     if (!aligned_or_null(g8, 16) || !aligned_or_null(u8, 16)) return MOE_EINVAL;
+    if (!in_place_ok(h, ldh, g, ldg, T) || !in_place_ok(h, ldh, u, ldu, T) || !apart(g8, u8) ||
+        !apart(gs, us))
+        return MOE_EINVAL;
     return moe::launch_act_forward(g, ldg, u, ldu, dtype, act, T, f, h, ldh, g8, gs, u8, us,
                                    as_stream(stream)) == hipSuccess
                ? MOE_OK
@@ -218,6 +235,9 @@ int moe_act_backward(const uint8_t *g8, const uint8_t *gs, const uint8_t *u8, co
     // u's codes, scales and gradient go together
     if ((u8 != nullptr) != (us != nullptr) || (u8 != nullptr) != (du != nullptr)) return MOE_EINVAL;
     if (u8 && (!aligned(u8, 16) || !aligned(du, 16) || !rows_ok(f, lddu))) return MOE_EINVAL;
+    if (!in_place_ok(dg, lddg, dh, lddh, T) || !in_place_ok(dh, lddh, du, lddu, T) ||
+        !in_place_ok(dh, lddh, h, ldh, T) || !apart(dg, du) || !apart(dg, h) || !apart(du, h))
+        return MOE_EINVAL;
     return moe::launch_act_backward(g8, gs, u8, us, dh, lddh, dtype, act, T, f, dg, lddg, du, lddu,
                                     h, ldh, as_stream(stream)) == hipSuccess
                ? MOE_OK

@@ -83,7 +83,8 @@ def test_linear_shape():
 
 #          x  ldx w ldw bias res ldr rdt dt act T   d   n  ws bytes   out ldo odt stream
 # (97 columns: w's rows are copied into padded ones, so a workspace is needed)
-GOOD = [A, 64, A, 97, A, A, 97, 0, 2, 2, 64, 64, 97, A, 1 << 30, A, 97, 0, N]
+B, C, D, F, H = (A + (i << 20) for i in range(1, 6))  # (never read: refused, or no device)
+GOOD = [A, 64, A, 97, A, A, 97, 0, 2, 2, 64, 64, 97, A, 1 << 30, B, 97, 0, N]
 
 
 @pytest.mark.parametrize("at,value", [
@@ -101,7 +102,7 @@ def test_linear_refuses(at, value):
 
 
 #             x ldx w  ldw dz lddz dt T   d   n  ws bytes   dx lddx dw lddw db gdt stream
-GOOD_BACK = [A, 64, A, 97, A, 97, 2, 64, 64, 97, A, 1 << 30, A, 64, A, 97, A, 0, N]
+GOOD_BACK = [A, 64, A, 97, A, 97, 2, 64, 64, 97, A, 1 << 30, B, 64, C, 97, D, 0, N]
 
 
 @pytest.mark.parametrize("at,value", [
@@ -148,9 +149,9 @@ def test_balance_refuses():
 
 
 def test_route_backward_refuses():
-    good = [A, A, A, A, A, A, 64, 8, 2, A, 1, N]
+    good = [A, A, A, A, A, A, 64, 8, 2, B, 1, N]
     for at, value in [(0, N), (1, N), (2, N), (4, N), (9, N), (0, A + 2), (2, A + 2), (3, A + 1),
-                      (5, A + 2), (9, A + 1), (10, 3), (10, -1)]:
+                      (5, A + 2), (9, B + 1), (9, A), (10, 3), (10, -1)]:
         args = list(good)
         args[at] = value
         assert L().moe_route_backward(*args) == 1, (at, value)
@@ -161,7 +162,7 @@ def test_route_backward_refuses():
 
 def test_act_forward_refuses():
     #        g ldg u ldu dt act T f h ldh g8 gs u8 us stream
-    good = [A, 64, A, 64, 2, 2, 8, 64, A, 64, A, A, A, A, N]
+    good = [A, 64, A, 64, 2, 2, 8, 64, A, 64, B, C, D, F, N]
     for at, value in [(0, N), (0, A + 8), (2, A + 8), (8, N), (8, A + 2), (1, 63), (3, 63), (9, 63),
                       (1, (1 << 20) + 1), (4, 3), (5, 0), (5, 4), (6, 0), (7, 0), (10, N), (11, N),
                       (12, N), (13, N), (10, A + 8), (12, A + 8), (2, N)]:
@@ -172,13 +173,42 @@ def test_act_forward_refuses():
 
 def test_act_backward_refuses():
     #        g8 gs u8 us dh lddh dt act T f dg lddg du lddu h ldh stream
-    good = [A, A, A, A, A, 64, 2, 2, 8, 64, A, 64, A, 64, A, 64, N]
+    good = [A, A, A, A, A, 64, 2, 2, 8, 64, A, 64, B, 64, C, 64, N]
     for at, value in [(0, N), (0, A + 8), (1, N), (2, N), (3, N), (2, A + 8), (4, N), (4, A + 2),
                       (5, 63), (6, 3), (7, 0), (7, 4), (8, 0), (9, 0), (10, N), (10, A + 8),
                       (11, 63), (12, N), (12, A + 8), (13, 63), (14, A + 8), (15, 63)]:
         args = list(good)
         args[at] = value
         assert L().moe_act_backward(*args) == 1, (at, value)
+
+
+def test_outputs_on_other_arguments_are_refused():
+    """an output may be an input only where the call names it, element on element"""
+    def rc(call, good, *changes):
+        args = list(good)
+        for at, value in changes:
+            args[at] = value
+        return getattr(L(), call)(*args)
+
+    fwd = list(GOOD)
+    fwd[0], fwd[2], fwd[4], fwd[5] = A, C, D, F
+    for at in (0, 2, 4):
+        assert rc("moe_linear", fwd, (15, fwd[at])) == 1
+    assert rc("moe_linear", fwd, (15, F), (17, 2)) == 1            # residual: fp32, out: not
+    assert rc("moe_linear", fwd, (15, F), (16, 98)) == 1           # another stride
+    back = list(GOOD_BACK)
+    back[0], back[2], back[4] = A, F, H
+    for at, value in [(12, F), (12, H), (14, A), (14, H), (16, H), (12, C), (16, C), (16, B)]:
+        assert rc("moe_linear_backward", back, (at, value)) == 1, (at, value)
+    #        g ldg u ldu dt act T f h ldh g8 gs u8 us stream
+    act = [A, 64, B, 64, 2, 2, 8, 64, C, 64, D, F, H, H + 4096, N]
+    for changes in [((8, A), (9, 72)), ((8, B), (9, 72)), ((12, D),), ((13, F),)]:
+        assert rc("moe_act_forward", act, *changes) == 1, changes
+    #         g8 gs u8 us dh lddh dt act T f dg lddg du lddu h ldh stream
+    grad = [H, H, H, H, A, 64, 2, 2, 8, 64, B, 64, C, 64, D, 64, N]
+    for changes in [((10, A), (11, 72)), ((12, A), (13, 72)), ((14, A), (15, 72)), ((12, B),),
+                    ((14, B),), ((14, C),)]:
+        assert rc("moe_act_backward", grad, *changes) == 1, changes
 
 
 def test_helpers_refuse_host_tensors():
@@ -201,6 +231,6 @@ def test_no_device_gives_ehip_without_crash():
     assert L().moe_linear(*GOOD) == 3
     assert L().moe_linear_backward(*GOOD_BACK) == 3
     assert L().moe_balance_loss(A, A, 64, 8, 2, A, 1 << 20, A, A, A, N) == 3
-    assert L().moe_route_backward(A, A, A, A, A, A, 64, 8, 2, A, 0, N) == 3
-    assert L().moe_act_forward(A, 64, A, 64, 2, 2, 8, 64, A, 64, A, A, A, A, N) == 3
-    assert L().moe_act_backward(A, A, A, A, A, 64, 2, 2, 8, 64, A, 64, A, 64, A, 64, N) == 3
+    assert L().moe_route_backward(A, A, A, A, A, A, 64, 8, 2, B, 0, N) == 3
+    assert L().moe_act_forward(A, 64, A, 64, 2, 2, 8, 64, A, 64, B, C, D, F, N) == 3
+    assert L().moe_act_backward(A, A, A, A, A, 64, 2, 2, 8, 64, A, 64, B, 64, C, 64, N) == 3

@@ -194,3 +194,27 @@ def test_helper_refuses():
                  lambda: abi.act_backward({k: ck[k] for k in ("g8", "gs")}, z, du=z.clone())):
         with pytest.raises((TypeError, ValueError, KeyError, abi.MoeError)):
             call()
+
+
+@pytest.mark.parametrize("T,f", [(70, 264), (5, 1003)])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_results_in_place_of_an_input(T, f, dtype):
+    """h on g or u, and one of dg, du and h on dh, give the bits that they give elsewhere"""
+    say(f"[act in place] T={T} f={f} {dtype}")
+    r = np.random.default_rng(f)
+    g, u, dh = (torch.from_numpy(r.standard_normal((T, f))).to("cuda", DT[dtype]) for _ in range(3))
+    want, ck = abi.act_forward(g, u, ckpt=True)
+    back = abi.act_backward(ck, dh)
+    for on in (0, 1):
+        a, b = g.clone(), u.clone()
+        h, again = abi.act_forward(a, b, ckpt=True, h=(a, b)[on])
+        torch.cuda.synchronize()
+        assert torch.equal(h, want)
+        assert all(torch.equal(again[k].view(torch.uint8), ck[k].view(torch.uint8)) for k in ck)
+    for k in ("dg", "du", "h"):
+        a = dh.clone()
+        got = abi.act_backward(ck, a, **{k: a})
+        torch.cuda.synchronize()
+        assert all(torch.equal(got[q], back[q]) for q in back), k
+    with pytest.raises(abi.MoeError):
+        abi.act_backward(ck, dh, dg=g, du=g)

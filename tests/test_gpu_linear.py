@@ -225,6 +225,24 @@ def test_bias_gradient_of_rows_that_end_in_half_a_piece(T, n):
     check_backward(T, 8, n, "f32", "f32", 4)
 
 
+def test_results_on_operands_are_refused():
+    x = torch.zeros(64, 64, device="cuda")
+    w, y = torch.zeros_like(x), torch.zeros_like(x)
+    for call in (lambda: abi.linear(x, w, out=x), lambda: abi.linear(x, w, out=w),
+                 lambda: abi.linear_backward(x, w, y, dx=y),
+                 lambda: abi.linear_backward(x, w, y, dw=x),
+                 lambda: abi.linear_backward(x, w, y, dx=w),
+                 lambda: abi.route_backward(x, torch.zeros(64, 2, dtype=torch.int32, device="cuda"),
+                                            None, None, torch.zeros(66, dtype=torch.int32,
+                                                                    device="cuda"),
+                                            torch.zeros(2, device="cuda"), out=x)):
+        with pytest.raises(abi.MoeError):
+            call()
+    # the operand that a gradient does not read may be overwritten by it
+    got, _ = abi.linear_backward(x, w, y, grads=("dx",), dx=x)
+    assert got["dx"] is x
+
+
 def test_linear_backward_is_the_difference_quotient():
     """<dz, z(x + h v) - z(x - h v)> / 2h = <dx, v>, and so for w: z is linear, so
     what is left is 32-bit rounding of z (2^-24 |z| over h, with h = 1/4)"""
