@@ -778,26 +778,54 @@ __global__ __launch_bounds__(256) void k_gemm_reduce(const float *__restrict__ p
     }
 }
 
-// dst [R][ldd] = src [R][C] (rows of lds units), columns C .. ldd zero. U is the
-// unit that is copied: the element, or 2 or 4 of the 16-bit types (2 of fp32)
-// together where a row is whole units and starts at one. One 16-byte chunk of
-// dst per thread. Bound by memory: 32,768 rows of 500 (66 MB in and out) 16 us, 4.1 TB/s.
-template <typename U>
-__global__ __launch_bounds__(256) void k_pad_rows(const U *__restrict__ src, int64_t lds, int64_t R,
-                                                  int C, U *__restrict__ dst, int ldd)
+// dst [R][ldd] = src [R][C] (row stride lds), columns C .. ldd zero; in units of
+// `unit` bytes: the element, or 2 or 4 of the 16-bit types (2 of fp32) together
+// where a row is whole units and starts at one.
+struct PadJob {
+    const char *src;
+    char *dst;
+    int64_t lds, R;
+    int C, ldd, unit;
+    int blocks;  // workgroups of the launch that take it
+};
+// an operation's operands, in one launch
+struct PadJobs {
+    PadJob j[3];
+    int n;
+};
+
+// one 16-byte chunk of dst per thread
+template <typename U> __device__ __forceinline__ void pad_rows(const PadJob &p, int64_t first)
 {
     constexpr int EPC = 16 / sizeof(U);
-    const int per = ldd / EPC;
-    for (int64_t q = (int64_t)blockIdx.x * 256 + threadIdx.x; q < R * per;
-         q += (int64_t)gridDim.x * 256) {
+    const U *src = reinterpret_cast<const U *>(p.src);
+    U *dst = reinterpret_cast<U *>(p.dst);
+    const int per = p.ldd / EPC;
+    for (int64_t q = first; q < p.R * per; q += (int64_t)p.blocks * 256) {
         const int64_t r = q / per;
         const int c = (int)(q - r * per) * EPC;
         typedef U vec __attribute__((ext_vector_type(EPC)));
         vec v;
 #pragma unroll
-        for (int i = 0; i < EPC; ++i) v[i] = c + i < C ? src[r * lds + c + i] : U(0);
-        *reinterpret_cast<vec *>(dst + r * ldd + c) = v;
+        for (int i = 0; i < EPC; ++i) v[i] = c + i < p.C ? src[r * p.lds + c + i] : U(0);
+        *reinterpret_cast<vec *>(dst + r * p.ldd + c) = v;
     }
+}
+
+// Bound by memory: 32,768 and 2,560 rows of 500 (71 MB in and out) 13.6 us, 5.2 TB/s
+// (two launches: 18 us; 509 x 1,003 and 1,003 x 517 of fp32: 5.8 us, two launches 7.6).
+__global__ __launch_bounds__(256) void k_pad_rows(const PadJobs all)
+{
+    int job = 0, block = blockIdx.x;
+    while (job + 1 < all.n && block >= all.j[job].blocks) block -= all.j[job++].blocks;
+    const PadJob &p = all.j[job];
+    const int64_t first = (int64_t)block * 256 + threadIdx.x;
+    if (p.unit == 8)
+        pad_rows<uint64_t>(p, first);
+    else if (p.unit == 4)
+        pad_rows<uint32_t>(p, first);
+    else
+        pad_rows<uint16_t>(p, first);
 }
 
 // Column sums of dz [rows][n]: a workgroup adds `per` rows from blockIdx.y * per
@@ -964,32 +992,31 @@ struct Matrix {
     int cols;
 };
 
-hipError_t place(const void *src, int64_t R, int64_t C, int64_t ld, int dtype, const Padded &z,
-                 char *dst, hipStream_t s, Matrix *m)
+// the operand where it lies, or where its padded copy will be, which `jobs` then makes
+Matrix place(const void *src, int64_t R, int64_t C, int64_t ld, int dtype, char *dst, PadJobs *jobs)
 {
+    const Padded z = padded(R, C, ld, dtype);
     const int es = elem_size(dtype);
-    m->cols = (int)z.cols;
-    if (!z.copy) {
-        m->p = static_cast<const char *>(src);
-        m->ld = ld * es;
-        return hipSuccess;
-    }
-    m->p = dst;
-    m->ld = z.cols * es;
-    const int64_t chunks = R * (z.cols * es / 16);
-    const dim3 grid((unsigned)(chunks / 256 + 1 < 8192 ? chunks / 256 + 1 : 8192)), block(256);
-    auto copy = [&](auto unit) {
-        typedef decltype(unit) U;
-        const int64_t per = sizeof(U) / es;
-        hipLaunchKernelGGL(k_pad_rows<U>, grid, block, 0, s, static_cast<const U *>(src), ld / per,
-                           R, (int)(C / per), reinterpret_cast<U *>(dst), (int)(z.cols / per));
-    };
-    if (C * es % 8 == 0 && ld * es % 8 == 0)
-        copy(uint64_t());
-    else if (C * es % 4 == 0 && ld * es % 4 == 0)
-        copy(uint32_t());
-    else
-        copy(uint16_t());
+    if (!z.copy) return Matrix{static_cast<const char *>(src), ld * es, (int)z.cols};
+    PadJob &p = jobs->j[jobs->n++];
+    p.unit = C * es % 8 == 0 && ld * es % 8 == 0 ? 8 : C * es % 4 == 0 && ld * es % 4 == 0 ? 4 : 2;
+    const int64_t per = p.unit / es, blocks = div_up(R * (z.cols * es / 16), 256);
+    p.src = static_cast<const char *>(src);
+    p.dst = dst;
+    p.lds = ld / per;
+    p.R = R;
+    p.C = (int)(C / per);
+    p.ldd = (int)(z.cols / per);
+    p.blocks = (int)(blocks < 8192 ? blocks : 8192);
+    return Matrix{dst, z.cols * es, (int)z.cols};
+}
+
+hipError_t launch_pads(const PadJobs &jobs, hipStream_t s)
+{
+    if (!jobs.n) return hipSuccess;
+    int blocks = 0;
+    for (int i = 0; i < jobs.n; ++i) blocks += jobs.j[i].blocks;
+    hipLaunchKernelGGL(k_pad_rows, dim3(blocks), dim3(256), 0, s, jobs);
     return hipGetLastError();
 }
 
@@ -1045,11 +1072,10 @@ hipError_t linear_t(const LinearCall &c, char *ws, hipStream_t s)
 {
     const LinearSpace z = linear_space(c.T, c.d, c.n, c.ldx, c.ldw, c.dtype);
     const int es = elem_size(c.dtype);
-    Matrix X, W;
-    hipError_t rc = place(c.x, c.T, c.d, c.ldx, c.dtype, padded(c.T, c.d, c.ldx, c.dtype),
-                          ws + z.x, s, &X);
-    if (rc != hipSuccess) return rc;
-    rc = place(c.w, c.d, c.n, c.ldw, c.dtype, padded(c.d, c.n, c.ldw, c.dtype), ws + z.w, s, &W);
+    PadJobs jobs{};
+    const Matrix X = place(c.x, c.T, c.d, c.ldx, c.dtype, ws + z.x, &jobs);
+    const Matrix W = place(c.w, c.d, c.n, c.ldw, c.dtype, ws + z.w, &jobs);
+    const hipError_t rc = launch_pads(jobs, s);
     if (rc != hipSuccess) return rc;
     Epilogue e;
     e.bias = c.bias;
@@ -1074,14 +1100,11 @@ hipError_t linear_backward_t(const LinearBackwardCall &c, char *ws, hipStream_t 
         c.T, c.d, c.n, c.ldx, c.ldw, c.lddz, c.dtype, c.dx, c.dw, c.db);
     const int es = elem_size(c.dtype);
     Matrix X{}, W{}, D{};
-    hipError_t rc = hipSuccess;
-    if (c.dx || c.dw)
-        rc = place(c.dz, c.T, c.n, c.lddz, c.dtype, padded(c.T, c.n, c.lddz, c.dtype), ws + z.dz, s,
-                   &D);
-    if (rc == hipSuccess && c.dx)
-        rc = place(c.w, c.d, c.n, c.ldw, c.dtype, padded(c.d, c.n, c.ldw, c.dtype), ws + z.w, s, &W);
-    if (rc == hipSuccess && c.dw)
-        rc = place(c.x, c.T, c.d, c.ldx, c.dtype, padded(c.T, c.d, c.ldx, c.dtype), ws + z.x, s, &X);
+    PadJobs jobs{};
+    if (c.dx || c.dw) D = place(c.dz, c.T, c.n, c.lddz, c.dtype, ws + z.dz, &jobs);
+    if (c.dx) W = place(c.w, c.d, c.n, c.ldw, c.dtype, ws + z.w, &jobs);
+    if (c.dw) X = place(c.x, c.T, c.d, c.ldx, c.dtype, ws + z.x, &jobs);
+    hipError_t rc = launch_pads(jobs, s);
     if (rc != hipSuccess) return rc;
     float *part = reinterpret_cast<float *>(ws + z.part);
     Epilogue e{};
