@@ -937,7 +937,7 @@ double product_us(int64_t M, int64_t N, int64_t steps, int dtype, int tile, int6
     } else {
         const double c = dtype == 0 ? (tile == 64 ? 0.6 : 1.9)
                          : tile == 64 ? 0.2 + 0.1 * full : 0.42 + 0.12 * full;
-        const double c2 = dtype == 0 ? 2 * c : tile == 64 ? 0.5 : 1.05;
+        const double c2 = dtype == 0 ? 2 * c : tile == 64 ? 0.5 : 1.1;
         t = (tile == 64 ? 4.5 : 6) +
             (wgs <= 256 ? n * c : (double)div_up((int64_t)wgs, 512) * (1 + n * c2));
     }
