@@ -43,9 +43,9 @@
 // result does not depend on timing.
 //
 // What bounds them, measured (times in a stream of calls, bf16 / fp16):
-//   32,768 x 2,048 over 4,096     495 us, 1.11 PFLOP/s     power: the matrix cores are
+//   32,768 x 2,048 over 4,096     500 us, 1.10 PFLOP/s     power: the matrix cores are
 //   8,192 x 4,096 over 2,048      118 us, 1.16 PFLOP/s     busy 59-72 % of the cycles at
-//   4,096 x 2,048 over 8,192      125 us, 1.10 PFLOP/s     a clock that falls from 2.4 to
+//   4,096 x 2,048 over 8,192      114 + 17 us (2 ranges)   a clock that falls from 2.4 to
 //                                 2 GHz under them; the same product of zeros takes 0.7
 //                                 of the time
 //   2,048 x 512 over 2,560        14.5 us, 370 TFLOP/s     operands into LDS: 168 MB for
