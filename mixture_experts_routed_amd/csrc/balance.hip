@@ -268,33 +268,38 @@ __global__ __launch_bounds__(256) void k_balance_join(int blocks, int E, const B
     constexpr int PARTS = 256 / kJoinCols;
     __shared__ float s_p[PARTS][kJoinCols];
     __shared__ int s_c[PARTS][kJoinCols];
-    __shared__ double s_z[256];
-    __shared__ int s_t[256];
+    __shared__ double s_z[4];
+    __shared__ int s_t[4];
     __shared__ int s_last;
     const int tid = threadIdx.x, col = tid & (kJoinCols - 1), part = tid / kJoinCols;
     const int e = blockIdx.x * kJoinCols + col;
     float p = 0.f;
     int c = 0;
     if (e < E)
-#pragma unroll 8
+#pragma unroll 16
         for (int b = part; b < blocks; b += PARTS) {
             p += w.prob[(int64_t)b * E + e];
             c += w.cnt[(int64_t)b * E + e];
         }
     s_p[part][col] = p;
     s_c[part][col] = c;
-    // (at most 256 workgroups in the first launch)
-    s_z[tid] = tid < blocks ? (double)w.z[tid] : 0.;
-    s_t[tid] = tid < blocks ? w.tokens[tid] : 0;
-    for (int h = 128; h > 0; h >>= 1) {
-        __syncthreads();
-        if (tid < h) {
-            s_z[tid] += s_z[tid + h];
-            s_t[tid] += s_t[tid + h];
+    // (at most 256 workgroups in the first launch) 64 at a time, then in order
+    {
+        double z = tid < blocks ? (double)w.z[tid] : 0.;
+        int n = tid < blocks ? w.tokens[tid] : 0;
+#pragma unroll
+        for (int h = 32; h > 0; h >>= 1) {
+            z += __shfl_xor(z, h);
+            n += __shfl_xor(n, h);
+        }
+        if ((tid & 63) == 0) {
+            s_z[tid >> 6] = z;
+            s_t[tid >> 6] = n;
         }
     }
     __syncthreads();
-    const int nt = s_t[0];
+    const int nt = s_t[0] + s_t[1] + s_t[2] + s_t[3];
+    const double zsum = s_z[0] + s_z[1] + s_z[2] + s_z[3];
     const float tokens = (float)max(nt, 1);
     if (part == 0) {
         p = 0.f;
@@ -342,7 +347,7 @@ __global__ __launch_bounds__(256) void k_balance_join(int blocks, int E, const B
         term += terms[b];
         entries += counts[b];
     }
-    write_losses(E, term, entries, s_z[0], nt, cnt, loss);
+    write_losses(E, term, entries, zsum, nt, cnt, loss);
 }
 
 template <int G, int NJ, int V, typename T>
