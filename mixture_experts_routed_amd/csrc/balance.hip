@@ -23,7 +23,7 @@
 //
 // Measured, 32,768 tokens, 512 experts, 10 picks: losses 13.7 us for the rows (68
 // MB, 5.0 TB/s) and 6.2 us for the join, which is the latency of a second
-// launch, two rounds of loads and one counter; gradient in fp16 22.4 us (105 MB,
+// launch, a round of loads and one counter; gradient in fp16 22.4 us (105 MB,
 // 4.7 TB/s). 64 tokens, 8 experts: 4.3 us, one launch. Rows of the next round
 // loaded ahead of this one's arithmetic gained nothing: 16 wavefronts a CU
 // already cover the latency.
