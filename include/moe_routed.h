@@ -563,7 +563,9 @@ int moe_linear_backward(const void *x, int64_t ldx, const void *w, int64_t ldw, 
  * In:  logits [T][E] fp32, ids [T*K] (moe_route_topk's).
  * Out: cnt [E+2] int32: c_e, then n_t at cnt[E] and n_a at cnt[E+1];
  *      prob [E] fp32; loss [2] fp32.
- * Errors: as moe_route_topk; MOE_EINVAL also for a small workspace.
+ * Errors: as moe_route_topk; MOE_EINVAL also for a small workspace, and for an
+ *      output that is another argument or the workspace (not looked at where
+ *      logits and ids are one address).
  */
 int moe_balance_workspace(int T, int E, int K, size_t *bytes);
 int moe_balance_loss(const float *logits, const int32_t *ids, int T, int E, int K, void *workspace,
@@ -583,7 +585,8 @@ int moe_balance_loss(const float *logits, const int32_t *ids, int T, int E, int 
  *      first term. Not both NULL. Values of w and dw at invalid ids are not used.
  * Out: dlogits [T][E] of dtype (MOE_F32, or the type of the router's product,
  *      whose moe_linear_backward takes it as dz). Every element is written.
- * Errors: as moe_route_topk.
+ * Errors: as moe_route_topk; MOE_EINVAL also for a dlogits that is one of the
+ *      arrays that are read.
  */
 int moe_route_backward(const float *logits, const int32_t *ids, const float *w, const float *dw,
                        const int32_t *cnt, const float *dloss, int T, int E, int K, void *dlogits,

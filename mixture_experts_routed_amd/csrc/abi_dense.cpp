@@ -4,6 +4,8 @@
 #include "checks.hpp"
 #include "launch.hpp"
 
+#include <initializer_list>
+
 namespace {
 
 constexpr int64_t kMaxCols = (int64_t)1 << 20;  // row lengths and strides, elements
@@ -26,6 +28,14 @@ bool in_place_ok(const void *out, int64_t ldo, const void *in, int64_t ldi, int 
 
 // outputs that are asked for lie apart
 bool apart(const void *a, const void *b) { return !a || a != b; }
+
+// an output that is asked for is none of a call's other arguments
+bool apart_from(const void *out, std::initializer_list<const void *> others)
+{
+    for (const void *p : others)
+        if (!apart(out, p)) return false;
+    return true;
+}
 
 int linear_sizes(int T, int d, int n, int64_t ldx, int64_t ldw, int dtype)
 {
@@ -179,6 +189,12 @@ int moe_balance_loss(const float *logits, const int32_t *ids, int T, int E, int 
     if (!aligned(logits, 4) || !aligned(ids, 4) || !aligned(cnt, 4) || !aligned(prob, 4) ||
         !aligned(loss, 4) || !workspace_ok(workspace, ws_bytes, need))
         return MOE_EINVAL;
+    // (with one address for both inputs there are no results to keep apart)
+    if (static_cast<const void *>(logits) != ids &&
+        (!apart_from(cnt, {logits, ids, workspace, prob, loss}) ||
+         !apart_from(prob, {logits, ids, workspace, loss}) ||
+         !apart_from(loss, {logits, ids, workspace})))
+        return MOE_EINVAL;
     return moe::launch_balance_loss(logits, ids, T, E, K, cnt, prob, loss, workspace,
                                     as_stream(stream)) == hipSuccess
                ? MOE_OK
@@ -194,7 +210,9 @@ int moe_route_backward(const float *logits, const int32_t *ids, const float *w, 
     if (!dtype_ok(dtype) || (!dw && !dloss)) return MOE_EINVAL;
     if (!aligned(logits, 4) || !aligned(ids, 4) || !aligned(cnt, 4) ||
         !aligned(dlogits, (size_t)elem_bytes(dtype)) || !aligned_or_null(dw, 4) ||
-        !aligned_or_null(dloss, 4) || (dw && !aligned(w, 4)) || dlogits == logits)
+        !aligned_or_null(dloss, 4) || (dw && !aligned(w, 4)))
+        return MOE_EINVAL;
+    if (!apart_from(dlogits, {logits, ids, dw, cnt, dloss}) || (dw && dlogits == w))
         return MOE_EINVAL;
     return moe::launch_route_backward(logits, ids, w, dw, cnt, dloss, T, E, K, dlogits, dtype,
                                       as_stream(stream)) == hipSuccess
