@@ -610,14 +610,16 @@ int moe_route_backward(const float *logits, const int32_t *ids, const float *w, 
  *      scales, contiguous (g8 16-byte aligned); u8 and us likewise, given
  *      exactly when g8 and u are.
  * Errors: MOE_EINVAL for T or f < 1, a bad stride, dtype or act, NULL or
- *      misaligned pointers, a checkpoint given in part; MOE_EHIP on a failed launch.
+ *      misaligned pointers, a checkpoint given in part, codes or scales that are
+ *      another argument; MOE_EHIP on a failed launch.
  *
  * moe_act_backward -- from that checkpoint (g, u: the values it stands for)
  * and dh [T][f] of dtype:
  *   dg = dh * u * act'(g),  du = dh * act(g),  h = act(g) * u
  * (u8, us and du NULL: dg = dh * act'(g), h = act(g)). relu'(0) = 0.
  * h may be NULL; it is the operand x of the following product's dw. One of dg,
- * du and h may be dh itself. Errors: as above.
+ * du and h may be dh itself. Errors: as above; MOE_EINVAL also for an output
+ * that is one of the codes or scales (not looked at where it is dh itself).
  */
 #define MOE_ACT8_BLOCK 32
 int moe_act_forward(const void *g, int64_t ldg, const void *u, int64_t ldu, int dtype, int act,

@@ -232,8 +232,9 @@ int moe_act_forward(const void *g, int64_t ldg, const void *u, int64_t ldu, int 
     if ((gs != nullptr) != keep || (u8 != nullptr) != (keep && u) || (us != nullptr) != (keep && u))
         return MOE_EINVAL;
     if (!aligned_or_null(g8, 16) || !aligned_or_null(u8, 16)) return MOE_EINVAL;
-    if (!in_place_ok(h, ldh, g, ldg, T) || !in_place_ok(h, ldh, u, ldu, T) || !apart(g8, u8) ||
-        !apart(gs, us))
+    if (!in_place_ok(h, ldh, g, ldg, T) || !in_place_ok(h, ldh, u, ldu, T) ||
+        !apart_from(g8, {g, u, h, gs, u8, us}) || !apart_from(gs, {g, u, h, u8, us}) ||
+        !apart_from(u8, {g, u, h, us}) || !apart_from(us, {g, u, h}))
         return MOE_EINVAL;
     return moe::launch_act_forward(g, ldg, u, ldu, dtype, act, T, f, h, ldh, g8, gs, u8, us,
                                    as_stream(stream)) == hipSuccess
@@ -256,6 +257,9 @@ int moe_act_backward(const uint8_t *g8, const uint8_t *gs, const uint8_t *u8, co
     if (!in_place_ok(dg, lddg, dh, lddh, T) || !in_place_ok(dh, lddh, du, lddu, T) ||
         !in_place_ok(dh, lddh, h, ldh, T) || !apart(dg, du) || !apart(dg, h) || !apart(du, h))
         return MOE_EINVAL;
+    // (in place of dh, an output lies where dh lies)
+    for (const void *out : {(const void *)dg, (const void *)du, (const void *)h})
+        if (out != dh && !apart_from(out, {g8, gs, u8, us})) return MOE_EINVAL;
     return moe::launch_act_backward(g8, gs, u8, us, dh, lddh, dtype, act, T, f, dg, lddg, du, lddu,
                                     h, ldh, as_stream(stream)) == hipSuccess
                ? MOE_OK

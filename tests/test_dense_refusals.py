@@ -36,3 +36,28 @@ def test_router_outputs_apart():
         assert status("moe_route_backward", ROUTE_BACKWARD, (9, P[other])) == 1, other
     # w is not read without dw
     assert status("moe_route_backward", ROUTE_BACKWARD, (3, N), (9, P[2])) == 3
+
+
+#              g     ldg u     ldu dt act T  f   h     ldh g8    gs    u8    us    stream
+ACT_FORWARD = [P[0], 64, P[1], 64, 2, 2, 8, 64, P[2], 64, P[3], P[4], P[5], P[6], N]
+#               g8    gs    u8    us    dh    lddh dt act T f dg    lddg du   lddu h    ldh stream
+ACT_BACKWARD = [P[0], P[1], P[2], P[3], P[4], 64, 2, 2, 8, 64, P[5], 64, P[6], 64, P[7], 64, N]
+
+
+def test_activation_outputs_apart():
+    assert status("moe_act_forward", ACT_FORWARD) == 3
+    codes = (10, 11, 12, 13)
+    for a in codes:
+        for b in (0, 2, 8, *codes):
+            if a != b:
+                assert status("moe_act_forward", ACT_FORWARD, (a, ACT_FORWARD[b])) == 1, (a, b)
+    for at in (0, 2):  # h on g or on u is documented
+        assert status("moe_act_forward", ACT_FORWARD, (8, ACT_FORWARD[at])) == 3
+
+    assert status("moe_act_backward", ACT_BACKWARD) == 3
+    for a in (10, 12, 14):
+        for b in (0, 1, 2, 3, 10, 12, 14):
+            if a != b:
+                assert status("moe_act_backward", ACT_BACKWARD, (a, ACT_BACKWARD[b])) == 1, (a, b)
+        # one of them on dh is documented
+        assert status("moe_act_backward", ACT_BACKWARD, (a, ACT_BACKWARD[4])) == 3
