@@ -491,9 +491,12 @@ int moe_forward_packed_noalloc(const void *x, const int32_t *ids, const float *w
  *  - a workspace is needed only where its size is not 0 (then 256-byte
  *    aligned); it starts with any contents, and calls that may overlap need
  *    one each;
- *  - an output overlaps no other argument, but where a call names one that it
- *    may be: then it is that array itself, from its first element and with its
- *    stride (otherwise MOE_EINVAL where the addresses are equal);
+ *  - an output, or a workspace that is needed, overlaps no other argument, but
+ *    where a call names one that an output may be: then it is that array itself,
+ *    from its first element and with its stride. An output whose address is
+ *    another argument's is refused otherwise (MOE_EINVAL), but where a call says
+ *    that it does not look; ranges that overlap from different addresses, and a
+ *    workspace that is an input, are the caller's to avoid;
  *  - results do not depend on timing: the same call gives the same bits.
  */
 
@@ -519,9 +522,9 @@ enum moe_act { MOE_ACT_NONE = 0, MOE_ACT_RELU = 1, MOE_ACT_SILU = 2, MOE_ACT_GEL
  *      computed in: the forward product is T x n over d, dx is T x d over n, dw
  *      d x n over T. Errors: MOE_EINVAL for a size < 1, a bad dtype, NULL.
  * Errors: MOE_EINVAL for T, d or n < 1, a stride below the row length or above
- *      2^20, a bad dtype or act, NULL or misaligned pointers, a small
- *      workspace, a product of more than 2^23 tiles (moe_linear_shape);
- *      MOE_EHIP on a failed launch.
+ *      2^20, a bad dtype or act, NULL or misaligned pointers, an out that is
+ *      another argument, a small workspace, a product of more than 2^23 tiles
+ *      (moe_linear_shape); MOE_EHIP on a failed launch.
  */
 int moe_linear_shape(int M, int N, int K, int dtype, int *tile, int *split);
 int moe_linear_workspace(int T, int d, int n, int64_t ldx, int64_t ldw, int dtype, size_t *bytes);

@@ -93,7 +93,7 @@ int moe_linear(const void *x, int64_t ldx, const void *w, int64_t ldw, const voi
     if (!aligned(x, 16) || !aligned(w, 16) || !aligned(out, 16) || !aligned_or_null(bias, 16) ||
         !aligned_or_null(residual, 16) || !workspace_ok(workspace, ws_bytes, need))
         return MOE_EINVAL;
-    if (out == x || out == w || out == bias) return MOE_EINVAL;
+    if (out == x || out == w || out == bias || (need && out == workspace)) return MOE_EINVAL;
     if (out == residual && (residual_dtype != out_dtype || (ldr != ldo && T > 1))) return MOE_EINVAL;
     moe::LinearCall c;
     c.x = x;
@@ -149,7 +149,8 @@ int moe_linear_backward(const void *x, int64_t ldx, const void *w, int64_t ldw, 
     if (db && !aligned(db, 16)) return MOE_EINVAL;
     if ((dw || db) && !result_ok(grad_dtype, dtype)) return MOE_EINVAL;
     for (const void *p : {(const void *)dx, (const void *)dw, (const void *)db})
-        if (p && (p == dz || (dw && p == x) || (dx && p == w))) return MOE_EINVAL;
+        if (p && (p == dz || (dw && p == x) || (dx && p == w) || (need && p == workspace)))
+            return MOE_EINVAL;
     if (!apart(dx, dw) || !apart(dx, db) || !apart(dw, db)) return MOE_EINVAL;
     moe::LinearBackwardCall c;
     c.x = x;

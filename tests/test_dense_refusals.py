@@ -61,3 +61,22 @@ def test_activation_outputs_apart():
                 assert status("moe_act_backward", ACT_BACKWARD, (a, ACT_BACKWARD[b])) == 1, (a, b)
         # one of them on dh is documented
         assert status("moe_act_backward", ACT_BACKWARD, (a, ACT_BACKWARD[4])) == 3
+
+
+# (97 columns: operands are copied into padded rows, so a workspace is needed)
+#         x     ldx w     ldw bias  res   ldr rdt dt act T   d   n   ws    bytes    out   ldo odt stream
+LINEAR = [P[0], 64, P[1], 97, P[2], P[3], 97, 0, 2, 2, 64, 64, 97, P[4], 1 << 30, P[5], 97, 0, N]
+#                  x     ldx w     ldw dz    lddz dt T  d   n   ws    bytes    dx    lddx dw lddw db    gdt stream
+LINEAR_BACKWARD = [P[0], 64, P[1], 97, P[2], 97, 2, 64, 64, 97, P[3], 1 << 30, P[4], 64, P[5], 97,
+                   P[6], 0, N]
+
+
+def test_product_outputs_apart_from_the_workspace():
+    assert status("moe_linear", LINEAR) == 3
+    assert status("moe_linear", LINEAR, (15, P[4])) == 1
+    assert status("moe_linear_backward", LINEAR_BACKWARD) == 3
+    for out in (12, 14, 16):
+        assert status("moe_linear_backward", LINEAR_BACKWARD, (out, P[3])) == 1, out
+    # a workspace that is not needed is not looked at: whole chunks, many tiles
+    whole = [P[0], 64, P[1], 8, N, N, 0, 2, 2, 0, 64, 64, 8, P[5], 0, P[5], 8, 2, N]
+    assert status("moe_linear", whole) == 3
