@@ -352,6 +352,15 @@ __global__ __launch_bounds__(256) void k_balance_join(int blocks, int E, const B
     write_losses(E, term, entries, zsum, nt, cnt, loss);
 }
 
+// What a wavefront's lanes did in LDS before stands before what they do after, for
+// the compiler too (the hardware keeps one wavefront's LDS operations in order; no
+// instruction comes of it)
+__device__ __forceinline__ void wave_order()
+{
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+}
+
 template <int G, int NJ, int V, typename T>
 __global__ __launch_bounds__(256) void k_route_backward(
     const float *__restrict__ logits, const int32_t *__restrict__ ids, const float *__restrict__ w,
@@ -406,8 +415,10 @@ __global__ __launch_bounds__(256) void k_route_backward(
         }
         if (dw) {
             s = group_sum<G>(s);
+            wave_order();  // (the reads of the row before)
 #pragma unroll
             for (int j = 0; j < NJ; ++j) mine[column<G, V>(sub, j)] = 0.f;
+            wave_order();
 #pragma unroll
             for (int q = 0; q < KS; ++q)
                 if (q * G < K && id[q] >= 0) atomicAdd(mine + id[q], pw[q] - wk[q] * s);
@@ -426,6 +437,7 @@ __global__ __launch_bounds__(256) void k_route_backward(
             for (int j = 0; j < NJ; ++j) v[j] = 0.f;
         }
         if (dw) {
+            wave_order();
 #pragma unroll
             for (int j = 0; j < NJ; ++j) v[j] += mine[column<G, V>(sub, j)];
         }
