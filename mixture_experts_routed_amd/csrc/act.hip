@@ -140,6 +140,13 @@ __device__ __forceinline__ void decode8(uint2 c, int scale, float (&v)[8])
         v[4 * h + 2] = b[0] * unit;
         v[4 * h + 3] = b[1] * unit;
     }
+    // The largest code that a value of fp32 or bf16 is rounded to stands for 256 *
+    // 2^120 = 2^128; read as fp32's largest value it is off by half a step, where an
+    // infinity would make silu, gelu and their slopes NaN (-inf * 0).
+    if (scale >= kMaxExp + 127)
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (__builtin_isinf(v[i])) v[i] = copysignf(3.4028234663852886e38f, v[i]);
 }
 
 struct ActArg {
