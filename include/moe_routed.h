@@ -483,9 +483,10 @@ int moe_forward_packed_noalloc(const void *x, const int32_t *ids, const float *w
  * bits. Conventions as above (device pointers, the caller's stream and
  * workspace, no host wait, argument checks before any HIP call); in addition
  *  - matrices are row-major with a row stride in elements (ld >= row length,
- *    at most 2^20) and a 16-byte aligned first element; every size from 1 on
- *    is served, rows that are not whole 16-byte chunks at the price of a copy
- *    in the workspace;
+ *    at most 2^20); every size and stride from 1 on is served, rows that are not
+ *    whole 16-byte chunks at the price of a copy in the workspace. The first
+ *    element of a matrix, bias or bias gradient lies at a 16-byte boundary
+ *    (MOE_EINVAL otherwise: a slice that starts elsewhere is to be copied);
  *  - products are accumulated and epilogues computed in fp32 and rounded once
  *    to the result's type;
  *  - a workspace is needed only where its size is not 0 (then 256-byte

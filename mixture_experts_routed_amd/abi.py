@@ -161,19 +161,38 @@ def _mat(t, name, dev, rows, cols, dtype, other=None):
         s0 = cols
     elif s0 < cols:
         raise ValueError(f"{name}: overlapping rows")
-    return t.data_ptr(), s0
+    p = t.data_ptr()
+    if p & 15:
+        raise ValueError(f"{name}: the first element is not 16-byte aligned")
+    return p, s0
 
 
-def _vec(t, name, dev, n, dtype):
+def _vec(t, name, dev, n, dtype, align=1):
     """device address of a contiguous array of n elements of dtype on GPU `dev` (or None)"""
     if t is None:
         return None
     p = _dev(t, name)
+    if p % align:
+        raise ValueError(f"{name}: the first element is not {align}-byte aligned")
     if t.get_device() != dev:
         raise ValueError(f"{name}: on {t.device}, expected GPU {dev}")
     if t.numel() != n or t.dtype is not dtype:
         raise ValueError(f"{name}: expected {n} elements of {dtype}, got {tuple(t.shape)} {t.dtype}")
     return p
+
+
+def _dtype(name, dtype):
+    """the C ABI's code of a torch type"""
+    if dtype not in DTYPE_OF:
+        raise TypeError(f"{name}: expected float32, float16 or bfloat16, got {dtype}")
+    return DTYPE_OF[dtype]
+
+
+def _act(act):
+    """the C ABI's code of an activation's name"""
+    if act not in ACTS:
+        raise ValueError(f"act: expected one of {', '.join(ACTS)}, got {act!r}")
+    return ACTS[act]
 
 
 def _host(t, name):
@@ -511,10 +530,11 @@ def moe_balance_workspace(T: int, E: int, K: int) -> int:
     return v.value
 
 
-# The short-named helpers take row-major GPU matrices (rows may be strided),
-# check shapes and types, allocate what is not given, on the stream that the
-# kernels run on, and launch on the tensors' device. `workspace` may be kept
-# from call to call; it is replaced when it is too small.
+# The short-named helpers take row-major GPU matrices (rows may be strided, the
+# first element lies at a 16-byte boundary), check shapes and types, allocate what
+# is not given, on the stream that the kernels run on, and launch on the tensors'
+# device. `workspace` may be kept from call to call; it is replaced when it is too
+# small.
 
 class _On:
     """Device and stream of one call: the tensors' device made current, `handle` the
@@ -580,11 +600,11 @@ def linear(x, w, bias=None, residual=None, act: str = "none", out_dtype=None, wo
         pw, ldw = _mat(w, "w", dev, d, n, D)
         pr, ldr = _mat(residual, "residual", dev, T, n, D, torch.float32)
         po, ldo = _mat(out, "out", dev, T, n, D, torch.float32)
-        dtype = DTYPE_OF[D]
+        dtype = _dtype("x", D)
         workspace, ws, have = at.workspace(workspace,
                                            moe_linear_workspace(T, d, n, ldx, ldw, dtype))
-        rc = lib().moe_linear(px, ldx, pw, ldw, _vec(bias, "bias", dev, n, D), pr, ldr,
-                              dtype if pr is None else DTYPE_OF[residual.dtype], dtype, ACTS[act],
+        rc = lib().moe_linear(px, ldx, pw, ldw, _vec(bias, "bias", dev, n, D, 16), pr, ldr,
+                              dtype if pr is None else DTYPE_OF[residual.dtype], dtype, _act(act),
                               T, d, n, ws, have, po, ldo, DTYPE_OF[out.dtype], at.handle)
     _check("moe_linear", rc)
     return out, workspace
@@ -622,8 +642,8 @@ def linear_backward(x, w, dz, grads=("dx", "dw", "db"), grad_dtype=None, workspa
             mask |= MOE_GRAD_BIAS
         pdx, lddx = _mat(got.get("dx"), "dx", dev, T, d, D)
         pdw, lddw = _mat(got.get("dw"), "dw", dev, d, n, G)
-        pdb = _vec(got.get("db"), "db", dev, n, G)
-        dtype = DTYPE_OF[D]
+        pdb = _vec(got.get("db"), "db", dev, n, G, 16)
+        dtype = _dtype("dz", D)
         workspace, ws, have = at.workspace(
             workspace, moe_linear_backward_workspace(T, d, n, ldx, ldw, lddz, dtype, mask))
         rc = lib().moe_linear_backward(px, ldx, pw, ldw, pz, lddz, dtype, T, d, n, ws, have, pdx,
@@ -671,7 +691,7 @@ def route_backward(logits, ids, w, dw, cnt, dloss, out_dtype=None, out=None, str
             _vec(ids, "ids", dev, T * K, torch.int32), _vec(w, "w", dev, T * K, torch.float32),
             _vec(dw, "dw", dev, T * K, torch.float32), _vec(cnt, "cnt", dev, E + 2, torch.int32),
             _vec(dloss, "dloss", dev, 2, torch.float32), T, E, K,
-            _vec(out, "out", dev, T * E, out.dtype), DTYPE_OF[out.dtype], at.handle)
+            _vec(out, "out", dev, T * E, out.dtype), _dtype("out", out.dtype), at.handle)
     _check("moe_route_backward", rc)
     return out
 
@@ -694,8 +714,8 @@ def act_forward(g, u=None, act: str = "silu", ckpt=None, h=None, stream=None):
         pu, ldu = _mat(u, "u", dev, T, f, D)
         ph, ldh = _mat(h, "h", dev, T, f, D)
         g8, gs, u8, us = _ckpt(dev, ckpt, T, f, u is not None)
-        rc = lib().moe_act_forward(pg, ldg, pu, ldu, DTYPE_OF[D], ACTS[act], T, f, ph, ldh, g8, gs,
-                                   u8, us, at.handle)
+        rc = lib().moe_act_forward(pg, ldg, pu, ldu, _dtype("g", D), _act(act), T, f, ph, ldh, g8,
+                                   gs, u8, us, at.handle)
     _check("moe_act_forward", rc)
     return h, ckpt
 
@@ -721,7 +741,7 @@ def act_backward(ckpt, dh, act: str = "silu", dg=None, du=None, h=None, need_h: 
         pdu, lddu = _mat(got.get("du"), "du", dev, T, f, D)
         ph, ldh = _mat(got.get("h"), "h", dev, T, f, D)
         g8, gs, u8, us = _ckpt(dev, ckpt, T, f, gated)
-        rc = lib().moe_act_backward(g8, gs, u8, us, pz, lddh, DTYPE_OF[D], ACTS[act], T, f, pdg,
+        rc = lib().moe_act_backward(g8, gs, u8, us, pz, lddh, _dtype("dh", D), _act(act), T, f, pdg,
                                     lddg, pdu, lddu, ph, ldh, at.handle)
     _check("moe_act_backward", rc)
     return got
@@ -734,7 +754,7 @@ def _ckpt(dev, ckpt, T, f, gated):
     if ("u8" in ckpt) != gated:
         raise ValueError("ckpt: made for another kind of activation (with or without u)")
     nb = T * -(-f // ACT8_BLOCK)
-    g = (_vec(ckpt["g8"], "g8", dev, T * f, torch.float8_e4m3fn),
+    g = (_vec(ckpt["g8"], "g8", dev, T * f, torch.float8_e4m3fn, 16),
          _vec(ckpt["gs"], "gs", dev, nb, torch.uint8))
-    return g + ((_vec(ckpt["u8"], "u8", dev, T * f, torch.float8_e4m3fn),
+    return g + ((_vec(ckpt["u8"], "u8", dev, T * f, torch.float8_e4m3fn, 16),
                  _vec(ckpt["us"], "us", dev, nb, torch.uint8)) if gated else (None, None))
