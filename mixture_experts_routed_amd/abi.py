@@ -545,6 +545,10 @@ class _On:
         if not isinstance(t, torch.Tensor) or not t.is_cuda:
             raise TypeError(f"{name}: expected a GPU tensor")
         self.index, self.stream, self.before = t.get_device(), stream, -1
+        # (a handle does not say where it belongs)
+        there = getattr(stream, "device_index", self.index)
+        if there != self.index:
+            raise ValueError(f"stream: on GPU {there}, expected GPU {self.index}")
 
     def __enter__(self):
         if self.index != torch._C._cuda_getDevice():
