@@ -277,12 +277,24 @@ __global__ __launch_bounds__(256) void k_balance_join(int blocks, int E, const B
     const int e = blockIdx.x * kJoinCols + col;
     float p = 0.f;
     int c = 0;
-    if (e < E)
-#pragma unroll 16
-        for (int b = part; b < blocks; b += PARTS) {
-            p += w.prob[(int64_t)b * E + e];
-            c += w.cnt[(int64_t)b * E + e];
+    // (at most 256 rows: 16 a thread, all in flight together; a thread without one reads
+    // the last row and adds nothing)
+    if (e < E) {
+        float q[256 / PARTS];
+        int n[256 / PARTS];
+#pragma unroll
+        for (int i = 0; i < 256 / PARTS; ++i) {
+            const int64_t at = (int64_t)min(part + PARTS * i, blocks - 1) * E + e;
+            q[i] = w.prob[at];
+            n[i] = w.cnt[at];
         }
+#pragma unroll
+        for (int i = 0; i < 256 / PARTS; ++i)
+            if (part + PARTS * i < blocks) {
+                p += q[i];
+                c += n[i];
+            }
+    }
     s_p[part][col] = p;
     s_c[part][col] = c;
     // (at most 256 workgroups in the first launch) 64 at a time, then in order
@@ -488,31 +500,39 @@ bool whole_rows(const void *p, int E, int es)
     return E % 4 == 0 && reinterpret_cast<uintptr_t>(p) % (4 * es) == 0;
 }
 
-// Workgroups of the forward's first launch: at most 256 (one per CU), each at
-// least one round of its groups of at least 8 lanes; one, and no second launch,
-// for batches that one workgroup takes in 4 rounds (64 tokens, 8 experts: 4 us
-// in one launch, 9 in two).
-int balance_blocks(int T, int E)
+// rows of logits that a workgroup of the forward's first launch takes at a time, as
+// by_width groups its lanes
+int rows_at_once(int E, bool vec)
 {
-    const int per = kRowThreads / (E <= 32 ? 8 : E <= 64 ? 16 : E <= 128 ? 32 : 64);
-    if (T <= 4 * per) return 1;
-    const int64_t b = ((int64_t)T + 15) / 16;
+    const int lanes = E <= (vec ? 32 : 8) ? 8 : E <= 64 ? 16 : E <= 128 ? 32 : 64;
+    return kRowThreads / lanes;
+}
+
+// Workgroups of the forward's first launch: at most 256 (one per CU), each with a
+// row in its first round; one, and no second launch, for batches that one workgroup
+// takes in 4 rounds (64 tokens, 8 experts: 4 us in one launch, 9 in two; 8 rounds of
+// 9 to 32 experts whose rows are not whole 16-byte chunks).
+int balance_blocks(int T, int E, bool vec)
+{
+    if (T <= 4 * rows_at_once(E, true)) return 1;
+    const int rows = rows_at_once(E, vec);
+    const int64_t b = ((int64_t)T + rows - 1) / rows;
     return (int)(b < 256 ? b : 256);
 }
 
-size_t place_scratch(int T, int E, char *p, BalanceScratch *w)
+size_t place_scratch(int blocks, int E, char *p, BalanceScratch *w)
 {
-    const size_t blocks = balance_blocks(T, E), join = (E + kJoinCols - 1) / kJoinCols;
+    const size_t join = (E + kJoinCols - 1) / kJoinCols;
     size_t at = 0;
     auto take = [&](size_t bytes) {
         char *q = p + at;
         at += (bytes + 255) / 256 * 256;
         return q;
     };
-    w->prob = reinterpret_cast<float *>(take(blocks * E * 4));
-    w->cnt = reinterpret_cast<int *>(take(blocks * E * 4));
-    w->z = reinterpret_cast<float *>(take(blocks * 4));
-    w->tokens = reinterpret_cast<int *>(take(blocks * 4));
+    w->prob = reinterpret_cast<float *>(take((size_t)blocks * E * 4));
+    w->cnt = reinterpret_cast<int *>(take((size_t)blocks * E * 4));
+    w->z = reinterpret_cast<float *>(take((size_t)blocks * 4));
+    w->tokens = reinterpret_cast<int *>(take((size_t)blocks * 4));
     w->term = reinterpret_cast<float *>(take(join * 4));
     w->entries = reinterpret_cast<int *>(take(join * 4));
     w->arrived = reinterpret_cast<int *>(take(4));
@@ -523,17 +543,19 @@ size_t place_scratch(int T, int E, char *p, BalanceScratch *w)
 
 int64_t balance_workspace(int T, int E)
 {
+    // (for any address of the logits: the form with the fewer rows at once)
     BalanceScratch w;
-    return (int64_t)place_scratch(T, E, nullptr, &w);
+    return (int64_t)place_scratch(balance_blocks(T, E, false), E, nullptr, &w);
 }
 
 hipError_t launch_balance_loss(const float *logits, const int32_t *ids, int T, int E, int K,
                                int32_t *cnt, float *prob, float *loss, void *ws, hipStream_t s)
 {
+    const bool vec = whole_rows(logits, E, 4);
+    const int blocks = balance_blocks(T, E, vec);
     BalanceScratch w;
-    place_scratch(T, E, static_cast<char *>(ws), &w);
-    const int blocks = balance_blocks(T, E);
-    const hipError_t rc = by_width(E, whole_rows(logits, E, 4), [&](auto z) {
+    place_scratch(blocks, E, static_cast<char *>(ws), &w);
+    const hipError_t rc = by_width(E, vec, [&](auto z) {
         typedef decltype(z) Z;
         auto rows = blocks == 1 ? k_balance_rows<Z::g, Z::nj, Z::v, true>
                                 : k_balance_rows<Z::g, Z::nj, Z::v, false>;
