@@ -28,40 +28,17 @@ constexpr int kMinExp = -110, kMaxExp = 120;
 
 // v[0..n) of columns c.. of a row; absent columns are 0
 template <typename T, bool VEC>
-__device__ __forceinline__ void load8(const T *p, int left, float (&v)[8])
+__device__ __forceinline__ void load_part(const T *p, int left, float (&v)[8])
 {
-    if (VEC) {
-        if (sizeof(T) == 2) {
-            Vec<T, 8>::load(p, v);
-        } else {
-            float a[4], b[4];
-            Vec<T, 4>::load(p, a);
-            Vec<T, 4>::load(p + 4, b);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                v[i] = a[i];
-                v[4 + i] = b[i];
-            }
-        }
-        return;
-    }
+    if (VEC) return load8<T>(p, v);
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = i < left ? to_f32(p[i]) : 0.f;
 }
 
 template <typename T, bool VEC>
-__device__ __forceinline__ void store8(T *p, int left, const float (&v)[8])
+__device__ __forceinline__ void store_part(T *p, int left, const float (&v)[8])
 {
-    if (VEC) {
-        if (sizeof(T) == 2) {
-            Vec<T, 8>::store(p, v);
-        } else {
-            const float a[4] = {v[0], v[1], v[2], v[3]}, b[4] = {v[4], v[5], v[6], v[7]};
-            Vec<T, 4>::store(p, a);
-            Vec<T, 4>::store(p + 4, b);
-        }
-        return;
-    }
+    if (VEC) return store8<T>(p, v);
 #pragma unroll
     for (int i = 0; i < 8; ++i)
         if (i < left) p[i] = from_f32<T>(v[i]);
@@ -169,8 +146,8 @@ __global__ __launch_bounds__(256) void k_act_forward(const ActArg p)
     const bool have = left > 0;
     const int64_t code = (int64_t)row * p.f + c, block = (int64_t)row * nb + (at >> 2);
     float g[8] = {}, u[8] = {}, h[8];
-    if (have) load8<T, VEC>(static_cast<const T *>(p.g) + row * p.ldg + c, left, g);
-    if (p.u && have) load8<T, VEC>(static_cast<const T *>(p.u) + row * p.ldu + c, left, u);
+    if (have) load_part<T, VEC>(static_cast<const T *>(p.g) + row * p.ldg + c, left, g);
+    if (p.u && have) load_part<T, VEC>(static_cast<const T *>(p.u) + row * p.ldu + c, left, u);
     if (p.g8) {
         int s;
         const uint2 w = encode8(g, &s);
@@ -188,7 +165,7 @@ __global__ __launch_bounds__(256) void k_act_forward(const ActArg p)
         h[i] = act_apply(g[i], p.act);
         if (p.u) h[i] *= u[i];
     }
-    store8<T, VEC>(static_cast<T *>(p.h) + row * p.ldh + c, left, h);
+    store_part<T, VEC>(static_cast<T *>(p.h) + row * p.ldh + c, left, h);
 }
 
 template <typename T, bool VEC>
@@ -203,7 +180,7 @@ __global__ __launch_bounds__(256) void k_act_backward(const ActArg p)
     float g[8], u[8], dh[8], dg[8], h[8];
     decode8(load_codes<VEC>(p.g8 + code, left), p.gs[block], g);
     if (p.u8) decode8(load_codes<VEC>(p.u8 + code, left), p.us[block], u);
-    load8<T, VEC>(static_cast<const T *>(p.dh) + row * p.lddh + c, left, dh);
+    load_part<T, VEC>(static_cast<const T *>(p.dh) + row * p.lddh + c, left, dh);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         float a;
@@ -212,9 +189,9 @@ __global__ __launch_bounds__(256) void k_act_backward(const ActArg p)
         h[i] = p.u8 ? a * u[i] : a;
         dh[i] *= a;
     }
-    store8<T, VEC>(static_cast<T *>(p.dg) + row * p.lddg + c, left, dg);
-    if (p.u8) store8<T, VEC>(static_cast<T *>(p.du) + row * p.lddu + c, left, dh);
-    if (p.h) store8<T, VEC>(static_cast<T *>(p.h) + row * p.ldh + c, left, h);
+    store_part<T, VEC>(static_cast<T *>(p.dg) + row * p.lddg + c, left, dg);
+    if (p.u8) store_part<T, VEC>(static_cast<T *>(p.du) + row * p.lddu + c, left, dh);
+    if (p.h) store_part<T, VEC>(static_cast<T *>(p.h) + row * p.ldh + c, left, h);
 }
 
 // rows per launch: thread indices stay in 32 bits

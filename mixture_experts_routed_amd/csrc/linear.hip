@@ -162,34 +162,6 @@ template <int W> __device__ __forceinline__ void act_all(float (&v)[W], int act)
     }
 }
 
-// 8 elements from a 16-byte aligned address
-template <typename T> __device__ __forceinline__ void load8(const T *p, float (&v)[8])
-{
-    if constexpr (sizeof(T) == 2) {
-        Vec<T, 8>::load(p, v);
-    } else {
-        float a[4], b[4];
-        Vec<T, 4>::load(p, a);
-        Vec<T, 4>::load(p + 4, b);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            v[i] = a[i];
-            v[4 + i] = b[i];
-        }
-    }
-}
-template <typename T, bool NT = false>
-__device__ __forceinline__ void store8(T *p, const float (&v)[8])
-{
-    if constexpr (sizeof(T) == 2) {
-        Vec<T, 8>::template store<NT>(p, v);
-    } else {
-        const float a[4] = {v[0], v[1], v[2], v[3]}, b[4] = {v[4], v[5], v[6], v[7]};
-        Vec<T, 4>::template store<NT>(p, a);
-        Vec<T, 4>::template store<NT>(p + 4, b);
-    }
-}
-
 // columns c .. c + 7 of row r (those below N); c is a multiple of 8. NT: whole
 // chunks are stored non-temporally (outputs that are larger than the caches)
 template <typename T, bool NT = false>
@@ -266,8 +238,9 @@ __device__ __forceinline__ uint32_t lds_at(const void *p)
 #endif
 }
 
-// A buffer resource (as buffer_of) in two halves: base address; range in bytes
-// and the raw-buffer word. A range of 0 bytes makes every load zeros.
+// A buffer resource (word 3: raw buffer of the gfx9 family) in two halves: base
+// address; range in bytes and that word. A load past the range returns zeros; a
+// range of 0 bytes makes every load zeros.
 struct Rsrc {
     uint64_t lo, hi;
 };
@@ -587,22 +560,20 @@ __global__ __launch_bounds__(256, (BM + BN > 256 ? 1 : 2)) void k_gemm(const Gem
     }
     // Each wavefront's own part of LDS holds 32 of its rows; rows are padded by
     // 4 floats, which spreads the rows of a store over the banks.
-    constexpr int COLS = TN * 32, PITCH = COLS + 4, RG = 1, LPR = COLS / 8;
-    static_assert(RG * 32 * PITCH * 4 * 4 <= (int)LDS_BYTES && TM % RG == 0, "fits");
-    float *mine = reinterpret_cast<float *>(lds) + wave * (RG * 32 * PITCH);
+    constexpr int COLS = TN * 32, PITCH = COLS + 4, LPR = COLS / 8;
+    static_assert(32 * PITCH * 4 * 4 <= (int)LDS_BYTES, "fits");
+    float *mine = reinterpret_cast<float *>(lds) + wave * (32 * PITCH);
 #pragma unroll
-    for (int h = 0; h < TM; h += RG) {
+    for (int h = 0; h < TM; ++h) {
 #pragma unroll
-        for (int i = 0; i < RG; ++i)
+        for (int j = 0; j < TN; ++j)
 #pragma unroll
-            for (int j = 0; j < TN; ++j)
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const float16_t &c = acc[h + i][j];
-                    *reinterpret_cast<float4_t *>(mine + (i * 32 + (lane & 31)) * PITCH + j * 32 +
-                                                  8 * q + 4 * (lane >> 5)) =
-                        float4_t{c[4 * q], c[4 * q + 1], c[4 * q + 2], c[4 * q + 3]};
-                }
+            for (int q = 0; q < 4; ++q) {
+                const float16_t &c = acc[h][j];
+                *reinterpret_cast<float4_t *>(mine + (lane & 31) * PITCH + j * 32 + 8 * q +
+                                              4 * (lane >> 5)) =
+                    float4_t{c[4 * q], c[4 * q + 1], c[4 * q + 2], c[4 * q + 3]};
+            }
         // (LDS operations of one wavefront stay in order; the compiler keeps it)
         asm volatile("" ::: "memory");
         const int n = col0 + (lane % LPR) * 8;
@@ -618,10 +589,10 @@ __global__ __launch_bounds__(256, (BM + BN > 256 ? 1 : 2)) void k_gemm(const Gem
         };
         if (p.e.plain && n + 8 <= p.N) {
 #pragma unroll 4
-            for (int r = lane / LPR; r < RG * 32; r += 64 / LPR) one(r, true);
+            for (int r = lane / LPR; r < 32; r += 64 / LPR) one(r, true);
         } else {
 #pragma unroll 2
-            for (int r = lane / LPR; r < RG * 32; r += 64 / LPR) one(r, false);
+            for (int r = lane / LPR; r < 32; r += 64 / LPR) one(r, false);
         }
         asm volatile("" ::: "memory");
     }

@@ -1,22 +1,14 @@
 // Device-side pieces of the dense operators (products, activations, their
-// gradients): buffer descriptors, element conversion, activations.
+// gradients): element conversion, activations.
 #pragma once
 
 #include "common.hpp"
 
 namespace moe {
 
-// A buffer resource over `bytes` bytes from `base` (word 3: raw buffer of the
-// gfx9 family); a load at an offset past them returns zeros and touches no
-// memory, kOutside is past any of them.
+// An offset past the end of any buffer resource: a load there returns zeros and
+// touches no memory.
 constexpr uint32_t kOutside = 0x80000000u;
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const void *base, uint32_t bytes)
-{
-    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(base), (short)0, (int)bytes,
-                                             0x00020000);
-}
-
-typedef __attribute__((address_space(3))) void *lds_ptr_t;
 
 // ---- element types ---------------------------------------------------------
 
@@ -48,6 +40,34 @@ template <typename T, int N> struct Vec {
             *reinterpret_cast<type *>(p) = x;
     }
 };
+
+// 8 elements at a 16-byte aligned address. NT: stored non-temporally
+template <typename T> __device__ __forceinline__ void load8(const T *p, float (&v)[8])
+{
+    if constexpr (sizeof(T) == 2) {
+        Vec<T, 8>::load(p, v);
+    } else {
+        float a[4], b[4];
+        Vec<T, 4>::load(p, a);
+        Vec<T, 4>::load(p + 4, b);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            v[i] = a[i];
+            v[4 + i] = b[i];
+        }
+    }
+}
+template <typename T, bool NT = false>
+__device__ __forceinline__ void store8(T *p, const float (&v)[8])
+{
+    if constexpr (sizeof(T) == 2) {
+        Vec<T, 8>::template store<NT>(p, v);
+    } else {
+        const float a[4] = {v[0], v[1], v[2], v[3]}, b[4] = {v[4], v[5], v[6], v[7]};
+        Vec<T, 4>::template store<NT>(p, a);
+        Vec<T, 4>::template store<NT>(p + 4, b);
+    }
+}
 
 // ---- activations (in 32 bits) ----------------------------------------------
 // silu(z) = z s, s = 1 / (1 + e^-z); gelu(z) = z Phi(z), Phi(z) = erfc(-z / sqrt 2) / 2
