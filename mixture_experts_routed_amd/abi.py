@@ -141,9 +141,9 @@ def _dev(t, name):
     return t.data_ptr()
 
 
-def _mat(t, name, dev, rows, cols, dtype, other=None):
+def _mat(t, name, dev, rows, cols, dtype, other=None, read=True):
     """(device address, row stride) of a row-major matrix [rows, cols] of dtype (or
-    `other`) on GPU `dev`; (None, 0) for None"""
+    `other`) on GPU `dev`; (None, 0) for None. read: by this call, or written"""
     if t is None:
         return None, 0
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
@@ -162,7 +162,7 @@ def _mat(t, name, dev, rows, cols, dtype, other=None):
     elif s0 < cols:
         raise ValueError(f"{name}: overlapping rows")
     p = t.data_ptr()
-    if p & 15:
+    if p & 15 and read:
         raise ValueError(f"{name}: the first element is not 16-byte aligned")
     return p, s0
 
@@ -628,8 +628,8 @@ def linear_backward(x, w, dz, grads=("dx", "dw", "db"), grad_dtype=None, workspa
         dev, D = at.index, dz.dtype
         T, n = _matrix_shape(dz, "dz")
         d = _matrix_shape(x, "x")[1] if x is not None else _matrix_shape(w, "w")[0]
-        px, ldx = _mat(x, "x", dev, T, d, D)
-        pw, ldw = _mat(w, "w", dev, d, n, D)
+        px, ldx = _mat(x, "x", dev, T, d, D, read="dw" in grads)
+        pw, ldw = _mat(w, "w", dev, d, n, D, read="dx" in grads)
         pz, lddz = _mat(dz, "dz", dev, T, n, D)
         G = grad_dtype or (dw.dtype if dw is not None else db.dtype if db is not None else D)
         if G is not D and G is not torch.float32:

@@ -61,3 +61,12 @@ def test_a_slice_at_16_bytes_is_served():
     want, _ = abi.linear(x, w)
     got, _ = abi.linear(x[2:], w)  # two rows of 64 bytes on
     assert torch.equal(got, want[2:])
+
+
+def test_operands_that_are_not_read_may_start_anywhere():
+    x, w, y = z(4, 8).normal_(), z(8, 12).normal_(), z(4, 12).normal_()
+    ox, ow = z(5, 9)[1:, 1:], z(8, 13)[:, 1:]
+    want, _ = abi.linear_backward(x, w, y)
+    assert torch.equal(abi.linear_backward(ox, w, y, grads=("dx",))[0]["dx"], want["dx"])
+    assert torch.equal(abi.linear_backward(x, ow, y, grads=("dw",))[0]["dw"], want["dw"])
+    assert torch.equal(abi.linear_backward(ox, ow, y, grads=("db",))[0]["db"], want["db"])
