@@ -617,9 +617,10 @@ int moe_route_backward(const float *logits, const int32_t *ids, const float *w, 
  *      misaligned pointers, a checkpoint given in part, codes or scales that are
  *      another argument; MOE_EHIP on a failed launch.
  *
- * moe_act_backward -- from that checkpoint (g, u: the values it stands for;
- * +-2^128, which magnitudes of 248 * 2^120 and more are rounded to, is read as
- * fp32's largest value) and dh [T][f] of dtype:
+ * moe_act_backward -- from that checkpoint (g, u: the values it stands for; in a
+ * block of the largest scale, 2^120, they are read times 1 - 2^-24, so that 2^128,
+ * which magnitudes of 248 * 2^120 and more are rounded to, is fp32's largest
+ * value) and dh [T][f] of dtype:
  *   dg = dh * u * act'(g),  du = dh * act(g),  h = act(g) * u
  * (u8, us and du NULL: dg = dh * act'(g), h = act(g)). relu'(0) = 0.
  * h may be NULL; it is the operand x of the following product's dw. One of dg,

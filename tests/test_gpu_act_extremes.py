@@ -52,8 +52,8 @@ def test_gradients_of_the_largest_magnitudes(dtype, kind, gated, on):
     dH, a = ref.f64(dh), ref.act(Z, kind)
     # (beyond 100 the slopes are 0 and 1 with nothing left to add)
     terms = np.where(np.abs(Z) > 100, 1.0, ref.slope_terms(Z, kind))
-    # as for ordinary values, and half a step more: +-2^128 is read as the largest value
-    # of fp32, 2^-24 below it (their activations, 0 or z, and slopes, 0 or 1, move by no more)
+    # as for ordinary values, and half a step more: in a block with +-2^128 values are read
+    # 2^-24 below themselves (the activations and slopes of the others move by no more)
     rel = np.maximum(ref.act_rel(np.clip(np.nan_to_num(Z), -20, 20), kind), 16 * ref.U32) + 6 * ref.U32
     for k, v, s in (("dg", dH * V * ref.act_slope(Z, kind), np.abs(dH * V) * terms),
                     ("du", dH * a, np.abs(dH * a)), ("h", a * V, np.abs(a * V))):
