@@ -31,11 +31,8 @@ def extremes(dtype):
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("kind", ["relu", "silu", "gelu"])
-@pytest.mark.parametrize("gated", [True, False])
-@pytest.mark.parametrize("on", ["g", "u"])
+@pytest.mark.parametrize("gated,on", [(True, "g"), (True, "u"), (False, "g")])
 def test_gradients_of_the_largest_magnitudes(dtype, kind, gated, on):
-    if on == "u" and not gated:
-        pytest.skip("no u")
     say(f"[act extremes] {dtype} {kind} gated={gated} on={on}")
     D, g = DT[dtype], np.random.default_rng(9)
     z = extremes(dtype)
