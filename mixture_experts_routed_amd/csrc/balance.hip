@@ -21,10 +21,10 @@
 // term through LDS: each group has a row there, the picks' lanes add to it (one
 // instruction, in lane order), and every lane reads its columns back.
 //
-// Measured, 32,768 tokens, 512 experts, 10 picks: losses 13.7 us for the rows (68
-// MB, 5.0 TB/s) and 6.2 us for the join, which is the latency of a second
-// launch, a round of loads and one counter; gradient in fp16 22.4 us (105 MB,
-// 4.7 TB/s). 64 tokens, 8 experts: 4.3 us, one launch. Rows of the next round
+// Measured, 32,768 tokens, 512 experts, 10 picks: losses 13.7-14.8 us for the rows
+// (68 MB, 4.6-5.0 TB/s) and 6.2-6.5 us for the join, which is the latency of a
+// second launch, a round of loads and one counter; gradient in fp16 22.4 us (105
+// MB, 4.7 TB/s). 64 tokens, 8 experts: 4.3 us, one launch. Rows of the next round
 // loaded ahead of this one's arithmetic gained nothing: 16 wavefronts a CU
 // already cover the latency.
 #include "launch.hpp"
@@ -146,8 +146,9 @@ struct BalanceScratch {
     int *arrived;   // join workgroups done; cleared by the first launch
 };
 
-// columns of a workgroup of the second launch; 512 experts: 8, 16, 32 and 64 columns 9.4,
-// 6.2, 6.0 and 6.9 us (arrivals at one counter wait for one another), 32 by 512 threads 6.3
+// columns of a workgroup of the second launch; 512 experts (the only count compared): 8,
+// 16, 32 and 64 columns 9.4, 6.2, 6.0 and 6.9 us (arrivals at one counter wait for one
+// another), 32 by 512 threads 6.3
 constexpr int kJoinCols = 16;
 constexpr int kRowThreads = 1024;  // of a workgroup of the forward's first launch
 

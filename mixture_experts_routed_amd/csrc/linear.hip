@@ -51,7 +51,8 @@
 //   2,048 x 512 over 2,560        14.5 us, 370 TFLOP/s     operands into LDS: 168 MB for
 //                                 256 tiles of 64 x 64, 14 TB/s
 //   4 x 2,816 over 704            7.4 us                   one memory round trip after
-//                                 another: launch, first loads, 4 MB of w, the store
+//                                 another on 44 workgroups: first loads, 4 MB of w, the
+//                                 store (an empty kernel of them: 1.4 us in such a trace)
 #include "launch.hpp"
 #include "mfma.hpp"
 
@@ -896,7 +897,11 @@ struct Product {
 //   2,560 x 512 over 32,768        159 /  112 / 95
 //   32,768 x 2,048 over 4,096        - /  555 / 485
 // and, in fp32 (bound by the matrix cores), 512 x 512 over 1,024: 14.8 / 21,
-// 2,048 x 2,048 over 2,048: 164 / 134.
+// 2,048 x 2,048 over 2,048: 164 / 134. The estimate names each row's fastest, but is
+// off by up to a fifth for it, and twice by more than the choice turns on: 512 x
+// 2,048 over 4,096 is estimated at 23.7 / 23.4 in tiles of 64 / 128, 2,560 x 512 over
+// 32,768 at 105 / 104 in tiles of 128 / 256. Sizes near such a border may get the
+// slower tile.
 double product_us(int64_t M, int64_t N, int64_t steps, int dtype, int tile, int64_t split)
 {
     const double wgs = (double)(div_up(M, tile) * div_up(N, tile) * split);
