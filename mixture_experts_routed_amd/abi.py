@@ -565,8 +565,10 @@ class _On:
     def empty(self, shape, dtype):
         if self.stream is None:
             return torch.empty(shape, dtype=dtype, device=torch.device("cuda", self.index))
+        # (ExternalStream(0) is not the default stream, but one of torch's own)
         s = (self.stream if hasattr(self.stream, "cuda_stream")
-             else torch.cuda.ExternalStream(self.handle))
+             else torch.cuda.ExternalStream(self.handle) if self.handle
+             else torch.cuda.default_stream(self.index))
         with torch.cuda.stream(s):
             return torch.empty(shape, dtype=dtype, device=torch.device("cuda", self.index))
 

@@ -83,3 +83,18 @@ def test_two_streams_at_once():
     for i in range(2):
         for p, q in zip(got[i], want[i]):
             assert all(torch.equal(u, v) for u, v in zip(p, q))
+
+
+def test_the_default_stream_by_its_handle():
+    """what a call allocates for the default stream, whose handle is 0, belongs to that
+    stream: once freed, it is what the stream's next request of that size gets"""
+    x, w = torch.randn(5003, 40, device="cuda"), torch.randn(40, 1900, device="cuda")
+    want, _ = abi.linear(x, w)
+    for stream in (None, 0, torch.cuda.default_stream()):
+        torch.cuda.synchronize()
+        torch.cuda.empty_cache()
+        out, _ = abi.linear(x, w, stream=stream)
+        assert torch.equal(out, want)
+        at = out.data_ptr()
+        del out
+        assert torch.empty_like(want).data_ptr() == at, stream
