@@ -45,5 +45,5 @@ def kernels(tmp_path_factory):
 def test_zero_add_and_read_back_are_ordered(kernels):
     assert len(kernels) == 3 * 14  # types; widths
     for name, ops in kernels.items():
-        # before a round's zeroing (the last round's reads), before the adds, before the reads
+        # before a row's zeroing (the reads of the row before), before the adds, before the reads
         assert re.fullmatch(r"F+Z+F+A+F+L+", ops), (name, ops)
