@@ -338,6 +338,56 @@ int moe_forward_packed(const void *x, const int32_t *ids, const float *w, const 
                        moe_stream_t stream);
 
 /*
+ * Expert weights in microscaled 4-bit floating point: 4.25 bits a weight with its
+ * share of a scale, 17/64 of the 16-bit weights' bytes.
+ *
+ * Format: 32 weights that follow one another along the reduction (the input
+ * index; the last block of a column may be shorter) share a scale 2^(s - 127), s a
+ * byte, 255 meaning NaN; each weight is a 4-bit e2m1 code (sign, 2 exponent bits,
+ * 1 fraction bit: 0, 0.5, 1, 1.5, 2, 3, 4, 6) and stands for code * 2^(s - 127).
+ * The packed layout is moe_pack_weights' for 16-bit types (expert, column group,
+ * K-step, slice, stream), a tile of 32 x 64 weights being 1024 bytes of codes and
+ * 64 of scales: byte 16 l + 4 c + i / 2 (low half for even i) holds the code of
+ * K-value 8 (l / 16) + i, column 4 (l % 16) + c; byte 1024 + j the scale of column
+ * j. Positions past d or f hold zeros.
+ *
+ * moe_mx4_weight_bytes -- host only: size of one packed matrix set. Errors: as
+ * moe_packed_weight_bytes; MOE_EINVAL also for matrices of more than 2^30 weights.
+ *
+ * moe_mx4_quantize -- from w [E][d][f] (MOE_W_GATE_UP) or [E][f][d] (MOE_W_DOWN)
+ * of dtype. With M a block's largest magnitude, s - 127 is the least e with M <=
+ * 6 * 2^e, within [-110, 120] (-110 for M = 0), and codes are nearest, ties to the
+ * even code: no value is clamped but magnitudes above 6 * 2^120. The relative error
+ * is at most 1/5 for magnitudes of at least 2^e, the absolute one at most 2^(e-2)
+ * below that. A block with a value that is not finite has s = 255. Weights that are
+ * values of this format already (whatever rule chose their scales) are kept exactly.
+ *
+ * moe_mx4_dequantize -- the values that packed weights stand for, row-major, in
+ * dtype (rounded to nearest even where the type does not hold them).
+ *
+ * moe_forward_mx4 -- moe_forward_packed with such weights (pw_gate, pw_up:
+ * MOE_W_GATE_UP; pw_down: MOE_W_DOWN) and 16-bit activations: a weight is its
+ * value in dtype, products are summed in fp32 and h is kept in dtype, so that the
+ * result is moe_forward_packed's on the dequantised weights -- bit for bit with
+ * MOE_BF16 and out_dtype MOE_F32; with MOE_F16 the expert outputs are kept in fp32
+ * rows (as in the four calls), not in the compact format.
+ * In:  x, ids, w as moe_forward; dtype MOE_F16 or MOE_BF16.
+ * Out: out [T][d] of out_dtype (dtype or MOE_F32; one rounding of the fp32 sum).
+ * workspace: moe_forward_workspace() bytes.
+ * Errors: those of moe_forward; MOE_EUNSUPPORTED for MOE_F32; MOE_EINVAL also for
+ * another out_dtype and for an out that is another argument.
+ */
+int moe_mx4_weight_bytes(int E, int d, int f, int kind, size_t *bytes);
+int moe_mx4_quantize(const void *w, int dtype, int E, int d, int f, int kind, void *packed,
+                     size_t packed_bytes, moe_stream_t stream);
+int moe_mx4_dequantize(const void *packed, size_t packed_bytes, int E, int d, int f, int kind,
+                       void *w, int dtype, moe_stream_t stream);
+int moe_forward_mx4(const void *x, const int32_t *ids, const float *w, const void *pw_gate,
+                    const void *pw_up, const void *pw_down, int dtype, int T, int K, int E, int d,
+                    int f, int tm, void *workspace, size_t ws_bytes, void *out, int out_dtype,
+                    moe_stream_t stream);
+
+/*
  * Expert weights in host memory, for layers whose experts do not all fit in
  * device memory ("#372 Prompt path: an MMQ group's experts gathered in one
  * launch, after one wait, released by one event", description: the routed
@@ -635,6 +685,117 @@ int moe_act_backward(const uint8_t *g8, const uint8_t *gs, const uint8_t *u8, co
                      const void *dh, int64_t lddh, int dtype, int act, int T, int f, void *dg,
                      int64_t lddg, void *du, int64_t lddu, void *h, int64_t ldh,
                      moe_stream_t stream);
+
+/*
+ * ---- Operators around the routed layer's block ----
+ *
+ * The router's other forms and the norms that a block stands between. Conventions
+ * as for the dense operators.
+ *
+ * moe_route_scored -- routing by scores. Per token, over the experts that are
+ * there (NaN and -inf logits, and NaN and -inf biases, mark an absent expert):
+ *   s_e = softmax of the logits, or 1 / (1 + exp(-l_e))
+ *   c_e = s_e + bias_e                          (bias NULL: c_e = s_e)
+ * The experts form `groups` groups of E / groups neighbours; a group is worth the
+ * sum of its group_top largest c (of fewer if fewer are there), and the `keep`
+ * groups of the largest worth stay (groups = keep = 1: no groups). Of their
+ * experts the K with the largest c are picked, in descending order, and
+ *   w_k = scale s_k / (sum over the picks of s_j)    (renorm != 0)
+ *   w_k = scale s_k                                  (renorm == 0)
+ * Equal c, and groups of equal worth, go to the lower index. Choices are those of c
+ * and worth in 64-bit arithmetic (without a bias experts go by their logits, of which
+ * s is a rising function); weights are within a few roundings of fp32.
+ * Where fewer than K experts are there, the remaining picks are id -1 with weight
+ * 0. A softmax with +inf logits is shared evenly among them.
+ * In:  logits [T][E] fp32, bias [E] fp32 or NULL. score: enum moe_score.
+ * Out: ids [T*K] int32, w [T*K] fp32 (the inputs of moe_plan / moe_forward).
+ * Errors: as moe_route_topk; MOE_EINVAL also for an unknown score, groups that do
+ *      not divide E, keep outside [1, groups], group_top outside [1, E / groups],
+ *      K above keep E / groups, a scale that is not finite, an output that is
+ *      another argument; MOE_EUNSUPPORTED for more than MOE_SCORE_MAX_GROUPS groups
+ *      or group_top above 2.
+ *
+ * moe_route_scored_backward -- the gradient of the logits from dw, that of w, for
+ * the choice made (ids, as moe_route_scored gave them). With u_k = scale dw_k over
+ * the entries with a valid id (others have no part; an id may come twice):
+ *   renorm:  g_k = (s_k / S) (u_k - sum_j (s_j / S) u_j),  S = sum_j s_j
+ *   else:    g_k = s_k u_k
+ *   sigmoid:               dl_e = sum over k of e: g_k (1 - s_e)
+ *   softmax, renorm:       dl_e = sum over k of e: g_k
+ *   softmax, not renorm:   dl_e = (sum over k of e: g_k) - s_e sum_j g_j
+ * (the softmax over the experts that are there; dl_e = 0 for those that are not).
+ * In:  logits [T][E] fp32, ids [T*K], dw [T*K] fp32; add [T][E] of dtype or NULL:
+ *      a gradient that is added (the balance loss's, say). It may be dlogits.
+ * Out: dlogits [T][E] of dtype. Every element is written.
+ * Errors: as moe_route_backward; MOE_EINVAL also for an unknown score and a scale
+ *      that is not finite.
+ */
+enum moe_score { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 };
+#define MOE_SCORE_MAX_GROUPS 64
+int moe_route_scored(const float *logits, const float *bias, int score, int T, int E, int K,
+                     int groups, int keep, int group_top, int renorm, float scale, int32_t *ids,
+                     float *w, moe_stream_t stream);
+int moe_route_scored_backward(const float *logits, const int32_t *ids, const float *dw,
+                              const void *add, int score, int T, int E, int K, int renorm,
+                              float scale, void *dlogits, int dtype, moe_stream_t stream);
+
+/*
+ * moe_norm -- the norms after and before a block, with its gate, scale and
+ * residual, in one pass (rms(v) = sqrt(mean of v^2 + eps), per row):
+ *   n = y / rms(y) * w_post      (w_post NULL: n = y)
+ *   z = r + alpha * gate * n     (gate NULL: 1; y NULL: z = r)
+ *   h = z / rms(z) * w_pre       (w_pre NULL: no h)
+ * In:  r [T][d] of r_dtype, the residual stream; y [T][d] of y_dtype (each dtype or
+ *      MOE_F32) or NULL, the block's output (the routed layer's, say); w_post and
+ *      w_pre [d] and the gate of dtype. gate_kind: enum moe_gate -- one value per
+ *      token [T], per channel [d], or per element [T][d] (stride ldgate).
+ *      y or w_pre is given; w_post and gate only with y.
+ * Out: z [T][d] of r_dtype (given exactly when y is; it may be r itself); h [T][d]
+ *      of dtype, the next block's input (given exactly when w_pre is; it may be y
+ *      itself); stats [T][2] fp32 or NULL: 1 / rms(y) and 1 / rms(z), 0 where there
+ *      is no such norm (what moe_norm_backward takes). h comes from z before its
+ *      rounding.
+ * Sums are in fp32; rows whose squares overflow it are summed scaled.
+ * Errors: MOE_EINVAL for T or d < 1, a bad stride, dtype or gate kind, eps below
+ *      2^-100 or not finite, alpha not finite, NULL or misaligned pointers, arguments that
+ *      do not go together, an output that is another argument; MOE_EUNSUPPORTED for
+ *      d > MOE_NORM_MAX_D; MOE_EHIP on a failed launch.
+ *
+ * moe_norm_backward -- from dz [T][d] of r_dtype (the gradient that reaches z from
+ * behind, or NULL) and dh [T][d] of dtype (given exactly when w_pre is). With
+ * zn = z * stats[1], yn = y * stats[0]:
+ *   dr = dz + stats[1] (dh w_pre - zn mean(dh w_pre zn))       w_pre: the mean over d
+ *   dw_pre = sum over t of dh zn
+ *   dgate = alpha dr n, summed over the elements that share a gate's value
+ *   q = alpha gate dr;  dw_post = sum over t of q yn
+ *   dy = stats[0] (q w_post - yn mean(q w_post yn))            (w_post NULL: dy = q)
+ * dr here is in fp32, before its rounding. z: the forward's (r without y).
+ * Out: dr [T][d] of r_dtype (may be dz itself); dy [T][d] of y_dtype; dgate in the
+ *      gate's shape, of dtype -- but per channel of grad_dtype; dw_post, dw_pre [d]
+ *      of grad_dtype (dtype or MOE_F32). dy, dgate, dw_post and dw_pre may each be
+ *      NULL: not computed.
+ * workspace: moe_norm_backward_workspace() bytes (partial column sums).
+ * Errors: as moe_norm.
+ */
+enum moe_gate {
+    MOE_GATE_NONE = 0,
+    MOE_GATE_TOKEN = 1,
+    MOE_GATE_CHANNEL = 2,
+    MOE_GATE_FULL = 3
+};
+#define MOE_NORM_MAX_D 32768
+int moe_norm(const void *r, int64_t ldr, int r_dtype, const void *y, int64_t ldy, int y_dtype,
+             const void *w_post, const void *gate, int64_t ldgate, int gate_kind,
+             const void *w_pre, int dtype, int T, int d, float alpha, float eps, void *z,
+             int64_t ldz, void *h, int64_t ldh, float *stats, moe_stream_t stream);
+int moe_norm_backward_workspace(int T, int d, size_t *bytes);
+int moe_norm_backward(const void *dz, int64_t lddz, const void *dh, int64_t lddh, const void *z,
+                      int64_t ldz, int r_dtype, const void *y, int64_t ldy, int y_dtype,
+                      const void *w_post, const void *gate, int64_t ldgate, int gate_kind,
+                      const void *w_pre, const float *stats, int dtype, int T, int d, float alpha,
+                      void *workspace, size_t ws_bytes, void *dr, int64_t lddr, void *dy,
+                      int64_t lddy, void *dgate, int64_t lddgate, void *dw_post, void *dw_pre,
+                      int grad_dtype, moe_stream_t stream);
 
 /* Static description of a status code. */
 const char *moe_status_str(int status);

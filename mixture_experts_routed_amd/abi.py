@@ -32,6 +32,9 @@ META_N = 11
 ACTS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3}  # enum moe_act
 MOE_GRAD_X, MOE_GRAD_W, MOE_GRAD_BIAS = 1, 2, 4
 ACT8_BLOCK = 32  # MOE_ACT8_BLOCK
+SCORES = {"softmax": 0, "sigmoid": 1}  # enum moe_score
+GATES = {"none": 0, "token": 1, "channel": 2, "full": 3}  # enum moe_gate
+MX4_KINDS = {"gate": MOE_W_GATE_UP, "down": MOE_W_DOWN}  # gate: gate and up matrices
 STAGES = ("hist", "scan", "place", "gather", "worklist", "gateup", "down", "combine")
 TORCH_DTYPE = {MOE_F32: torch.float32, MOE_F16: torch.float16, MOE_BF16: torch.bfloat16}
 DTYPE_OF = {torch.float32: MOE_F32, torch.float16: MOE_F16, torch.bfloat16: MOE_BF16}
@@ -57,6 +60,7 @@ class ForwardLayout(ctypes.Structure):
 
 _lib = None
 P, I32, I64, SZ = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_size_t
+F32 = ctypes.c_float
 
 _SIGS = {
     "moe_route_topk": [P, I32, I32, I32, P, P, P],
@@ -101,6 +105,17 @@ _SIGS = {
     "moe_route_backward": [P, P, P, P, P, P, I32, I32, I32, P, I32, P],
     "moe_act_forward": [P, I64, P, I64, I32, I32, I32, I32, P, I64, P, P, P, P, P],
     "moe_act_backward": [P, P, P, P, P, I64, I32, I32, I32, I32, P, I64, P, I64, P, I64, P],
+    "moe_mx4_weight_bytes": [I32, I32, I32, I32, ctypes.POINTER(ctypes.c_size_t)],
+    "moe_mx4_quantize": [P, I32, I32, I32, I32, I32, P, SZ, P],
+    "moe_mx4_dequantize": [P, SZ, I32, I32, I32, I32, P, I32, P],
+    "moe_forward_mx4": [P, P, P, P, P, P, I32, I32, I32, I32, I32, I32, I32, P, SZ, P, I32, P],
+    "moe_route_scored": [P, P, I32, I32, I32, I32, I32, I32, I32, I32, F32, P, P, P],
+    "moe_route_scored_backward": [P, P, P, P, I32, I32, I32, I32, I32, F32, P, I32, P],
+    "moe_norm": [P, I64, I32, P, I64, I32, P, P, I64, I32, P, I32, I32, I32, F32, F32, P, I64, P,
+                 I64, P, P],
+    "moe_norm_backward_workspace": [I32, I32, ctypes.POINTER(ctypes.c_size_t)],
+    "moe_norm_backward": [P, I64, P, I64, P, I64, I32, P, I64, I32, P, P, I64, I32, P, P, I32, I32,
+                          I32, F32, P, SZ, P, I64, P, I64, P, I64, P, P, I32, P],
     "moe_forward_packed_noalloc": [P, P, P, P, P, P, I32, I32, I32, I32, I32, I32, I32, P, P],
 }
 
@@ -190,9 +205,14 @@ def _dtype(name, dtype):
 
 def _act(act):
     """the C ABI's code of an activation's name"""
-    if act not in ACTS:
-        raise ValueError(f"act: expected one of {', '.join(ACTS)}, got {act!r}")
-    return ACTS[act]
+    return _named("act", act, ACTS)
+
+
+def _named(name, value, of):
+    """the C ABI's code of a named choice"""
+    if value not in of:
+        raise ValueError(f"{name}: expected one of {', '.join(of)}, got {value!r}")
+    return of[value]
 
 
 def _host(t, name):
@@ -764,3 +784,265 @@ def _ckpt(dev, ckpt, T, f, gated):
          _vec(ckpt["gs"], "gs", dev, nb, torch.uint8))
     return g + ((_vec(ckpt["u8"], "u8", dev, T * f, torch.float8_e4m3fn, 16),
                  _vec(ckpt["us"], "us", dev, nb, torch.uint8)) if gated else (None, None))
+
+
+# ------------------------------------- operators around the routed layer's block --
+
+def moe_mx4_weight_bytes(E: int, d: int, f: int, kind: int) -> int:
+    v = ctypes.c_size_t()
+    _check("moe_mx4_weight_bytes", lib().moe_mx4_weight_bytes(E, d, f, kind, ctypes.byref(v)))
+    return v.value
+
+
+@functools.lru_cache(maxsize=1024)
+def moe_norm_backward_workspace(T: int, d: int) -> int:
+    v = ctypes.c_size_t()
+    _check("moe_norm_backward_workspace", lib().moe_norm_backward_workspace(T, d, ctypes.byref(v)))
+    return v.value
+
+
+@functools.lru_cache(maxsize=1024)
+def _forward_workspace(T, K, E, d, f, tm, dtype):
+    return moe_forward_workspace(T, K, E, d, f, tm, dtype)
+
+
+def route_scored(logits, K: int, bias=None, score: str = "softmax", groups: int = 1, keep=None,
+                 group_top: int = 1, renorm: bool = True, scale: float = 1.0, ids=None, w=None,
+                 stream=None):
+    """Routing of logits [T, E] fp32 by softmax or sigmoid scores: the K experts with the
+    largest score + bias [E] of the `keep` (None: all) of `groups` groups whose group_top
+    best experts add up to most; weights are the scores (without the bias) times scale,
+    renormalised to sum to it or not. Returns (ids [T, K] int32, w [T, K] fp32)."""
+    with _On(logits, "logits", stream) as at:
+        dev = at.index
+        T, E = _matrix_shape(logits, "logits")
+        ids = at.empty((T, K), torch.int32) if ids is None else ids
+        w = at.empty((T, K), torch.float32) if w is None else w
+        rc = lib().moe_route_scored(
+            _vec(logits, "logits", dev, T * E, torch.float32),
+            _vec(bias, "bias", dev, E, torch.float32), _named("score", score, SCORES), T, E, K,
+            groups, groups if keep is None else keep, group_top, int(bool(renorm)), scale,
+            _vec(ids, "ids", dev, T * K, torch.int32), _vec(w, "w", dev, T * K, torch.float32),
+            at.handle)
+    _check("moe_route_scored", rc)
+    return ids, w
+
+
+def route_scored_backward(logits, ids, dw, score: str = "softmax", renorm: bool = True,
+                          scale: float = 1.0, add=None, out_dtype=None, out=None, stream=None):
+    """Gradient of the logits [T, E] from dw [T, K], that of route_scored()'s weights, for
+    its ids. add [T, E], of the result's type, is added to it and may be out itself.
+    out_dtype: fp32, or the type of the router's product."""
+    with _On(logits, "logits", stream) as at:
+        dev = at.index
+        T, E = _matrix_shape(logits, "logits")
+        K = _matrix_shape(ids, "ids")[1]
+        if out is None:
+            out = at.empty((T, E), out_dtype or (add.dtype if add is not None else torch.float32))
+        elif out_dtype is not None and out.dtype is not out_dtype:
+            raise TypeError(f"out: expected {out_dtype}, got {out.dtype}")
+        rc = lib().moe_route_scored_backward(
+            _vec(logits, "logits", dev, T * E, torch.float32),
+            _vec(ids, "ids", dev, T * K, torch.int32), _vec(dw, "dw", dev, T * K, torch.float32),
+            _vec(add, "add", dev, T * E, out.dtype), _named("score", score, SCORES), T, E, K,
+            int(bool(renorm)), scale, _vec(out, "out", dev, T * E, out.dtype),
+            _dtype("out", out.dtype), at.handle)
+    _check("moe_route_scored_backward", rc)
+    return out
+
+
+def _mx4_shape(name, w, kind):
+    if w.dim() != 3:
+        raise ValueError(f"{name}: expected [E, in, out] matrices, got {tuple(w.shape)}")
+    E, a, b = w.shape
+    return (E, a, b) if kind == MOE_W_GATE_UP else (E, b, a)
+
+
+def mx4_quantize(w, kind: str, packed=None, stream=None):
+    """Expert matrices in microscaled 4-bit floating point: w [E, d, f] (kind "gate": gate
+    or up matrices) or [E, f, d] ("down"). Returns the packed bytes, in the layout that
+    forward_mx4 streams; a given `packed` is filled."""
+    with _On(w, "w", stream) as at:
+        k = _named("kind", kind, MX4_KINDS)
+        E, d, f = _mx4_shape("w", w, k)
+        need = moe_mx4_weight_bytes(E, d, f, k)
+        packed = at.empty((need,), torch.uint8) if packed is None else packed
+        rc = lib().moe_mx4_quantize(
+            _vec(w, "w", at.index, E * d * f, w.dtype, 16), _dtype("w", w.dtype), E, d, f, k,
+            _vec(packed, "packed", at.index, need, torch.uint8, 16), need, at.handle)
+    _check("moe_mx4_quantize", rc)
+    return packed
+
+
+def mx4_dequantize(packed, E: int, d: int, f: int, kind: str, dtype=None, out=None, stream=None):
+    """The values of packed matrices, row-major in `dtype` (out's, or bfloat16): [E, d, f]
+    (kind "gate") or [E, f, d] ("down")."""
+    with _On(packed, "packed", stream) as at:
+        k = _named("kind", kind, MX4_KINDS)
+        need = moe_mx4_weight_bytes(E, d, f, k)
+        shape = (E, d, f) if k == MOE_W_GATE_UP else (E, f, d)
+        if out is None:
+            out = at.empty(shape, dtype or torch.bfloat16)
+        elif dtype is not None and out.dtype is not dtype:
+            raise TypeError(f"out: expected {dtype}, got {out.dtype}")
+        elif tuple(out.shape) != shape:
+            raise ValueError(f"out: expected {shape}, got {tuple(out.shape)}")
+        rc = lib().moe_mx4_dequantize(
+            _vec(packed, "packed", at.index, need, torch.uint8, 16), need, E, d, f, k,
+            _vec(out, "out", at.index, E * d * f, out.dtype, 16), _dtype("out", out.dtype),
+            at.handle)
+    _check("moe_mx4_dequantize", rc)
+    return out
+
+
+def pack_mx4(w_gate, w_up, w_down, stream=None) -> dict:
+    """The three matrix sets of a layer in 4 bits, keyed gate / up / down."""
+    return {"gate": mx4_quantize(w_gate, "gate", stream=stream),
+            "up": mx4_quantize(w_up, "gate", stream=stream),
+            "down": mx4_quantize(w_down, "down", stream=stream)}
+
+
+def forward_mx4(x, ids, w, packed, E: int, f: int, tm: int = 16, out_dtype=None, workspace=None,
+                out=None, stream=None):
+    """One routed MoE layer with expert weights in 4 bits (pack_mx4()'s dict, for E experts
+    of intermediate size f): x [T, d] float16 or bfloat16, ids and w [T, K]; out [T, d] in
+    x's type or torch.float32. Returns (out, workspace)."""
+    with _On(x, "x", stream) as at:
+        dev, D = at.index, x.dtype
+        T, d = _matrix_shape(x, "x")
+        K = _matrix_shape(ids, "ids")[1]
+        if out is None:
+            out = at.empty((T, d), out_dtype or D)
+        elif out_dtype is not None and out.dtype is not out_dtype:
+            raise TypeError(f"out: expected {out_dtype}, got {out.dtype}")
+        dtype = _dtype("x", D)
+        bgu, bdn = _mx4_bytes(E, d, f)
+        workspace, ws, have = at.workspace(workspace, _forward_workspace(T, K, E, d, f, tm, dtype))
+        rc = lib().moe_forward_mx4(
+            _vec(x, "x", dev, T * d, D, 16), _vec(ids, "ids", dev, T * K, torch.int32),
+            _vec(w, "w", dev, T * K, torch.float32),
+            _vec(packed["gate"], "packed['gate']", dev, bgu, torch.uint8, 16),
+            _vec(packed["up"], "packed['up']", dev, bgu, torch.uint8, 16),
+            _vec(packed["down"], "packed['down']", dev, bdn, torch.uint8, 16), dtype, T, K, E, d,
+            f, tm, ws, have, _vec(out, "out", dev, T * d, out.dtype, 16),
+            _dtype("out", out.dtype), at.handle)
+    _check("moe_forward_mx4", rc)
+    return out, workspace
+
+
+@functools.lru_cache(maxsize=1024)
+def _mx4_bytes(E, d, f):
+    return (moe_mx4_weight_bytes(E, d, f, MOE_W_GATE_UP),
+            moe_mx4_weight_bytes(E, d, f, MOE_W_DOWN))
+
+
+def _gate(gate, kind, name, dev, T, d, dtype, channel=None):
+    """(address, row stride) of a gate or its gradient; channel: a per-channel one's type"""
+    if gate is None:
+        return None, 0
+    if kind == GATES["full"]:
+        return _mat(gate, name, dev, T, d, dtype)
+    per_channel = kind == GATES["channel"]
+    return _vec(gate, name, dev, d if per_channel else T, channel if per_channel and channel
+                else dtype, 16), 0
+
+
+def _norm_dtype(*given):
+    """the type that the weights and the gate share, or the first matrix's"""
+    for t in given:
+        if t is not None:
+            return t.dtype
+    raise ValueError("y or w_pre is needed")
+
+
+def norm(r, y=None, w_post=None, gate=None, gate_kind: str = "none", w_pre=None,
+         alpha: float = 1.0, eps: float = 1e-6, z=None, h=None, stats=None, stream=None):
+    """The norms after and before a block (root mean square over a row), its gate, scale and
+    residual in one pass: n = y / rms(y) * w_post (or y), z = r + alpha * gate * n (or r
+    without y), h = z / rms(z) * w_pre. r [T, d], the residual stream, and y [T, d], the
+    block's output, each in the weights' type or torch.float32; gate [T] ("token"), [d]
+    ("channel") or [T, d] ("full"). z may be r itself, h may be y. stats: a [T, 2] fp32
+    tensor, or True for a new one, that receives 1 / rms(y) and 1 / rms(z) for
+    norm_backward. Returns a dict of z (with y), h (with w_pre) and stats (if asked for)."""
+    with _On(r, "r", stream) as at:
+        dev, R = at.index, r.dtype
+        T, d = _matrix_shape(r, "r")
+        D = _norm_dtype(w_pre, w_post, gate, y)
+        kind = _named("gate_kind", gate_kind, GATES)
+        got = {}
+        if y is not None:
+            got["z"] = at.empty((T, d), R) if z is None else z
+        elif z is not None:
+            raise ValueError("z: there is no y, z is r")
+        if w_pre is not None:
+            got["h"] = at.empty((T, d), D) if h is None else h
+        elif h is not None:
+            raise ValueError("h: there is no w_pre")
+        if stats is not None:
+            got["stats"] = at.empty((T, 2), torch.float32) if stats is True else stats
+        F = torch.float32
+        pr, ldr = _mat(r, "r", dev, T, d, D, F)
+        py, ldy = _mat(y, "y", dev, T, d, D, F)
+        pg, ldg = _gate(gate, kind, "gate", dev, T, d, D)
+        pz, ldz = _mat(got.get("z"), "z", dev, T, d, R)
+        ph, ldh = _mat(got.get("h"), "h", dev, T, d, D)
+        dtype = _dtype("the weights", D)
+        rc = lib().moe_norm(
+            pr, ldr, _dtype("r", R), py, ldy, dtype if y is None else _dtype("y", y.dtype),
+            _vec(w_post, "w_post", dev, d, D, 16), pg, ldg, kind,
+            _vec(w_pre, "w_pre", dev, d, D, 16), dtype, T, d, alpha, eps, pz, ldz, ph, ldh,
+            _vec(got.get("stats"), "stats", dev, 2 * T, F), at.handle)
+    _check("moe_norm", rc)
+    return got
+
+
+def norm_backward(z, stats, dz=None, dh=None, y=None, w_post=None, gate=None,
+                  gate_kind: str = "none", w_pre=None, alpha: float = 1.0, grad_dtype=None,
+                  grads=None, workspace=None, dr=None, dy=None, dgate=None, dw_post=None,
+                  dw_pre=None, stream=None):
+    """Gradients of norm() from dz (of z, from behind; or None) and dh (of h, given with
+    w_pre), with its z (r where there was no y), stats and other arguments. Returns (dict,
+    workspace): dr, and those of dy, dgate, dw_post, dw_pre that apply (or that `grads`
+    names); dr may be dz itself. dw_post, dw_pre and a per-channel dgate are in
+    grad_dtype (the weights' type, or torch.float32)."""
+    with _On(z, "z", stream) as at:
+        dev, R, F = at.index, z.dtype, torch.float32
+        T, d = _matrix_shape(z, "z")
+        D = _norm_dtype(w_pre, w_post, gate, y)
+        kind = _named("gate_kind", gate_kind, GATES)
+        given = {"dr": dr, "dy": dy, "dgate": dgate, "dw_post": dw_post, "dw_pre": dw_pre}
+        able = {"dr": True, "dy": y is not None, "dgate": gate is not None,
+                "dw_post": w_post is not None, "dw_pre": w_pre is not None}
+        ask = set(k for k in able if able[k]) if grads is None else set(grads) | {"dr"}
+        for k in ask | {k for k in given if given[k] is not None}:
+            if not able.get(k):
+                raise ValueError(f"{k}: there is no such gradient in this call")
+        sums = [given[k].dtype for k in ("dw_post", "dw_pre") if given[k] is not None]
+        if given["dgate"] is not None and gate_kind == "channel":
+            sums.append(given["dgate"].dtype)
+        G = grad_dtype or (sums[0] if sums else D)
+        if G is not D and G is not F:
+            raise TypeError(f"grad_dtype: expected {D} or torch.float32, got {G}")
+        like = {"dr": ((T, d), R), "dy": ((T, d), y.dtype if y is not None else D),
+                "dgate": (((T,), (d,), (T, d))[max(kind, 1) - 1], G if gate_kind == "channel" else D),
+                "dw_post": ((d,), G), "dw_pre": ((d,), G)}
+        got = {k: at.empty(*like[k]) if given[k] is None else given[k] for k in like if k in ask}
+        pdz, lddz = _mat(dz, "dz", dev, T, d, R)
+        pdh, lddh = _mat(dh, "dh", dev, T, d, D)
+        pz, ldz = _mat(z, "z", dev, T, d, D, F)
+        py, ldy = _mat(y, "y", dev, T, d, D, F)
+        pg, ldg = _gate(gate, kind, "gate", dev, T, d, D)
+        pdr, lddr = _mat(got["dr"], "dr", dev, T, d, R)
+        pdy, lddy = _mat(got.get("dy"), "dy", dev, T, d, like["dy"][1])
+        pdg, lddg = _gate(got.get("dgate"), kind, "dgate", dev, T, d, D, G)
+        workspace, ws, have = at.workspace(workspace, moe_norm_backward_workspace(T, d))
+        dtype = _dtype("the weights", D)
+        rc = lib().moe_norm_backward(
+            pdz, lddz, pdh, lddh, pz, ldz, _dtype("z", R), py, ldy,
+            dtype if y is None else _dtype("y", y.dtype), _vec(w_post, "w_post", dev, d, D, 16),
+            pg, ldg, kind, _vec(w_pre, "w_pre", dev, d, D, 16),
+            _vec(stats, "stats", dev, 2 * T, F), dtype, T, d, alpha, ws, have, pdr, lddr, pdy,
+            lddy, pdg, lddg, _vec(got.get("dw_post"), "dw_post", dev, d, G, 16),
+            _vec(got.get("dw_pre"), "dw_pre", dev, d, G, 16), DTYPE_OF[G], at.handle)
+    _check("moe_norm_backward", rc)
+    return got, workspace

@@ -5,6 +5,7 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <initializer_list>
 #include <new>
 
 #include "checks.hpp"
@@ -92,7 +93,10 @@ struct Rec {
 
 // the work list puts the runs of 4 first when a big-cell kernel takes them
 // (packed weights, 16-bit, shape as ffn_shape decides)
-bool runs_first(const moe::FfnShape &z, bool packed) { return packed && (z.big_gu || z.big_dn); }
+bool runs_first(const moe::FfnShape &z, int wf)
+{
+    return wf == moe::kPacked && (z.big_gu || z.big_dn);
+}
 
 bool timer_room(const moe_timer_t *t)
 {
@@ -170,7 +174,7 @@ int ffn_impl(const void *xs, const void *wg, const void *wu, const void *wd, int
              int d, int f, int tm, const int32_t *eoff, const int32_t *stok, const float *sw,
              const int32_t *meta, int64_t max_rows, void *h, float *y, void *scratch,
              size_t scratch_bytes, hipStream_t s, moe_timer_t *tmr, bool have_items = false,
-             const void *x = nullptr, int T = 0, bool packed = false, int8_t *yexp = nullptr,
+             const void *x = nullptr, int T = 0, int wf = moe::kRowMajor, int8_t *yexp = nullptr,
              const moe::WavePlan *wp = nullptr)
 {
     const int rc = ffn_check(xs, wg, wu, wd, dtype, E, d, f, tm, eoff, stok, sw, meta, max_rows, h,
@@ -179,21 +183,21 @@ int ffn_impl(const void *xs, const void *wg, const void *wu, const void *wd, int
     const moe::FfnShape z = moe::ffn_shape(E, tm, max_rows, d, f, dtype);
     if (!have_items) {
         Rec r(tmr, s, MOE_STAGE_WORKLIST);
-        if (moe::launch_worklist(eoff, E, max_rows, scratch, z.max_items, runs_first(z, packed),
+        if (moe::launch_worklist(eoff, E, max_rows, scratch, z.max_items, runs_first(z, wf),
                                  s) != hipSuccess)
             return MOE_EHIP;
     }
     {
         Rec r(tmr, s, MOE_STAGE_GATEUP);
         const hipError_t e =
-            x ? moe::launch_gateup_gathered(z, dtype, packed, x, T, stok, wg, wu, d, f, meta,
+            x ? moe::launch_gateup_gathered(z, dtype, wf, x, T, stok, wg, wu, d, f, meta,
                                             scratch, h, s, wp)
-              : moe::launch_gateup(z, dtype, packed, xs, stok, wg, wu, d, f, meta, scratch, h, s);
+              : moe::launch_gateup(z, dtype, wf, xs, stok, wg, wu, d, f, meta, scratch, h, s);
         if (e != hipSuccess) return MOE_EHIP;
     }
     {
         Rec r(tmr, s, MOE_STAGE_DOWN);
-        if (moe::launch_down(z, dtype, packed, h, wd, d, f, stok, sw, meta, scratch, y, yexp, s) !=
+        if (moe::launch_down(z, dtype, wf, h, wd, d, f, stok, sw, meta, scratch, y, yexp, s) !=
             hipSuccess)
             return MOE_EHIP;
     }
@@ -202,7 +206,8 @@ int ffn_impl(const void *xs, const void *wg, const void *wu, const void *wd, int
 
 // yexp != nullptr: y holds the compact format (see ffn_impl)
 int combine_impl(const float *y, int64_t max_rows, const int32_t *pos, int T, int K, int d,
-                 float *out, hipStream_t s, moe_timer_t *tmr, const int8_t *yexp = nullptr)
+                 void *out, hipStream_t s, moe_timer_t *tmr, const int8_t *yexp = nullptr,
+                 int out_dtype = MOE_F32)
 {
     if (T < 1 || K < 1 || d < 8 || d % 8 || max_rows < 1 || (int64_t)T * K > kI32Max)
         return MOE_EINVAL;
@@ -210,8 +215,8 @@ int combine_impl(const float *y, int64_t max_rows, const int32_t *pos, int T, in
     Rec r(tmr, s, MOE_STAGE_COMBINE);
     const hipError_t e =
         yexp ? moe::launch_combine_y16(reinterpret_cast<const uint16_t *>(y), yexp, max_rows, pos,
-                                       T, K, d, out, s)
-             : moe::launch_combine(y, max_rows, pos, T, K, d, out, s);
+                                       T, K, d, out, out_dtype, s)
+             : moe::launch_combine(y, max_rows, pos, T, K, d, out, out_dtype, s);
     return e == hipSuccess ? MOE_OK : MOE_EHIP;
 }
 
@@ -328,8 +333,8 @@ struct HostStage {
 
 int forward_impl(const void *x, const int32_t *ids, const float *w, const void *wg, const void *wu,
                  const void *wd, int dtype, int T, int K, int E, int d, int f, int tm, void *ws,
-                 size_t ws_bytes, float *out, hipStream_t s, moe_timer_t *tmr, bool packed = false,
-                 const HostStage *hs = nullptr)
+                 size_t ws_bytes, void *out, hipStream_t s, moe_timer_t *tmr,
+                 int wf = moe::kRowMajor, const HostStage *hs = nullptr, int out_dtype = MOE_F32)
 {
     moe_forward_layout_t L;
     moe_plan_sizes_t z;
@@ -364,14 +369,14 @@ int forward_impl(const void *x, const int32_t *ids, const float *w, const void *
     } else {
         rc = plan_impl(ids, w, T, K, E, tm, i32(L.cnt), i32(L.eoff), i32(L.tiles), i32(L.stok),
                        f32(L.sw), i32(L.pos), i32(L.boff), i32(L.meta), b + L.plan_scratch,
-                       z.scratch_bytes, s, tmr, b + L.ffn_scratch, &items, runs_first(fz, packed));
+                       z.scratch_bytes, s, tmr, b + L.ffn_scratch, &items, runs_first(fz, wf));
         if (rc != MOE_OK) return rc;
     }
     if (hs) {
         // the routed experts' weights into the cache, the work list to slots
         if (!items) {
             if (moe::launch_worklist(i32(L.eoff), E, z.max_rows, b + L.ffn_scratch, fz.max_items,
-                                     runs_first(fz, packed), s) != hipSuccess)
+                                     runs_first(fz, wf), s) != hipSuccess)
                 return MOE_EHIP;
             items = true;
         }
@@ -389,15 +394,18 @@ int forward_impl(const void *x, const int32_t *ids, const float *w, const void *
     // 16-bit types: the expert outputs in the compact format, binary16 rows at
     // L.y and their block exponents right after them (2d + ceil(d/128) bytes per
     // row fit in the region's 4d)
-    int8_t *yexp = dtype == MOE_F32
+    // (fp16 layers with 4-bit weights keep fp32 rows: their output is asked for in
+    // fp16, and the compact format's rounding would be as large as that one)
+    int8_t *yexp = dtype == MOE_F32 || (wf == moe::kMx4 && dtype == MOE_F16)
                        ? nullptr
                        : reinterpret_cast<int8_t *>(b + L.y + (size_t)z.max_rows * d * 2);
     rc = ffn_impl(b + L.xs, wg, wu, wd, dtype, E, d, f, tm, i32(L.eoff), i32(L.stok), f32(L.sw),
                   i32(L.meta), z.max_rows, b + L.h, f32(L.y), b + L.ffn_scratch,
                   fz.scratch_bytes, s, tmr, items,
-                  fused_gather ? x : nullptr, T, packed, yexp, wp.ids ? &wp : nullptr);
+                  fused_gather ? x : nullptr, T, wf, yexp, wp.ids ? &wp : nullptr);
     if (rc != MOE_OK) return rc;
-    return combine_impl(f32(L.y), z.max_rows, i32(L.pos), T, K, d, out, s, tmr, yexp);
+    return combine_impl(f32(L.y), z.max_rows, i32(L.pos), T, K, d, out, s, tmr, yexp,
+                        out_dtype);
 }
 
 }  // namespace
@@ -514,7 +522,7 @@ int moe_expert_ffn_packed(const void *xs, const void *pw_gate, const void *pw_up
 {
     return ffn_impl(xs, pw_gate, pw_up, pw_down, dtype, E, d, f, tm, eoff, stok, sw, meta,
                     max_rows, h, y, scratch, scratch_bytes, as_stream(stream), nullptr, false,
-                    nullptr, 0, true);
+                    nullptr, 0, moe::kPacked);
 }
 
 int moe_forward_packed(const void *x, const int32_t *ids, const float *w, const void *pw_gate,
@@ -523,7 +531,7 @@ int moe_forward_packed(const void *x, const int32_t *ids, const float *w, const 
                        moe_stream_t stream)
 {
     return forward_impl(x, ids, w, pw_gate, pw_up, pw_down, dtype, T, K, E, d, f, tm, workspace,
-                        ws_bytes, out, as_stream(stream), nullptr, true);
+                        ws_bytes, out, as_stream(stream), nullptr, moe::kPacked);
 }
 
 int moe_forward_packed_timed(const void *x, const int32_t *ids, const float *w,
@@ -533,7 +541,67 @@ int moe_forward_packed_timed(const void *x, const int32_t *ids, const float *w,
                              moe_timer_t *timer)
 {
     return forward_impl(x, ids, w, pw_gate, pw_up, pw_down, dtype, T, K, E, d, f, tm, workspace,
-                        ws_bytes, out, as_stream(stream), timer, true);
+                        ws_bytes, out, as_stream(stream), timer, moe::kPacked);
+}
+
+int moe_mx4_weight_bytes(int E, int d, int f, int kind, size_t *bytes)
+{
+    if (!bytes || E < 1 || d < 8 || f < 8 || d % 8 || f % 8 ||
+        (kind != MOE_W_GATE_UP && kind != MOE_W_DOWN))
+        return MOE_EINVAL;
+    if (E > MOE_MAX_EXPERTS) return MOE_EUNSUPPORTED;
+    // (as the layer: a matrix's elements of 2 bytes are at most 2 GiB)
+    if ((int64_t)d * f > ((int64_t)1 << 30) || d > (1 << 22) || f > (1 << 22)) return MOE_EINVAL;
+    const bool gu = kind == MOE_W_GATE_UP;
+    *bytes = moe::mx4_weight_bytes(E, gu ? d : f, gu ? f : d, gu);
+    return MOE_OK;
+}
+
+int moe_mx4_quantize(const void *w, int dtype, int E, int d, int f, int kind, void *packed,
+                     size_t packed_bytes, moe_stream_t stream)
+{
+    size_t need = 0;
+    const int rc = moe_mx4_weight_bytes(E, d, f, kind, &need);
+    if (rc != MOE_OK) return rc;
+    if (!dtype_ok(dtype) || !aligned(w, 16) || !aligned(packed, 16) || packed_bytes < need ||
+        packed == w)
+        return MOE_EINVAL;
+    const bool gu = kind == MOE_W_GATE_UP;
+    return moe::launch_mx4_quantize(dtype, w, E, gu ? d : f, gu ? f : d, gu, packed,
+                                    as_stream(stream)) == hipSuccess
+               ? MOE_OK
+               : MOE_EHIP;
+}
+
+int moe_mx4_dequantize(const void *packed, size_t packed_bytes, int E, int d, int f, int kind,
+                       void *w, int dtype, moe_stream_t stream)
+{
+    size_t need = 0;
+    const int rc = moe_mx4_weight_bytes(E, d, f, kind, &need);
+    if (rc != MOE_OK) return rc;
+    if (!dtype_ok(dtype) || !aligned(w, 16) || !aligned(packed, 16) || packed_bytes < need ||
+        packed == w)
+        return MOE_EINVAL;
+    const bool gu = kind == MOE_W_GATE_UP;
+    return moe::launch_mx4_dequantize(dtype, packed, E, gu ? d : f, gu ? f : d, gu, w,
+                                      as_stream(stream)) == hipSuccess
+               ? MOE_OK
+               : MOE_EHIP;
+}
+
+int moe_forward_mx4(const void *x, const int32_t *ids, const float *w, const void *pw_gate,
+                    const void *pw_up, const void *pw_down, int dtype, int T, int K, int E, int d,
+                    int f, int tm, void *workspace, size_t ws_bytes, void *out, int out_dtype,
+                    moe_stream_t stream)
+{
+    if (!dtype_ok(dtype)) return MOE_EINVAL;
+    if (dtype == MOE_F32) return MOE_EUNSUPPORTED;
+    if (out_dtype != dtype && out_dtype != MOE_F32) return MOE_EINVAL;
+    for (const void *p : {x, (const void *)ids, (const void *)w, pw_gate, pw_up, pw_down,
+                          (const void *)workspace})
+        if (p == out) return MOE_EINVAL;
+    return forward_impl(x, ids, w, pw_gate, pw_up, pw_down, dtype, T, K, E, d, f, tm, workspace,
+                        ws_bytes, out, as_stream(stream), nullptr, moe::kMx4, nullptr, out_dtype);
 }
 
 int moe_host_cache_bytes(int T, int K, int E, int d, int f, int dtype, int packed, int slots,
@@ -585,7 +653,8 @@ int moe_forward_host_weights(const void *x, const int32_t *ids, const float *w,
     hs.max_new = smin;
     // the cache's matrices stand in for the device weights (checked as such)
     return forward_impl(x, ids, w, hs.st.gate, hs.st.up, hs.st.down, dtype, T, K, E, d, f, tm,
-                        workspace, ws_bytes, out, as_stream(stream), nullptr, packed != 0, &hs);
+                        workspace, ws_bytes, out, as_stream(stream), nullptr,
+                        packed ? moe::kPacked : moe::kRowMajor, &hs);
 }
 
 int moe_combine(const float *y, int64_t max_rows, const int32_t *pos, int T, int K, int d,

@@ -46,6 +46,8 @@
 #include "launch.hpp"
 #include "plan_wave.hpp"
 
+#include <type_traits>
+
 namespace moe {
 
 constexpr int kMT = kItemRows / 16;     // 16-row m-tiles per work item
@@ -57,8 +59,7 @@ constexpr int big_cols(bool gateup) { return gateup ? 128 : 256; }
 
 int ffn_rows_per_item() { return kItemRows; }
 
-// Packed weight layout (written once by k_pack, read by the GEMMs with
-// PACKED): a matrix [E][Kd][N] becomes, per expert, column group g (4 slices
+// Packed weight layout (kPacked, written once by k_pack): a matrix [E][Kd][N] becomes, per expert, column group g (4 slices
 // of 64*m columns), K-step s, wave slice w and stream m (gate/up: m = 1 stream
 // of 64 columns; down: m = 2 halves of 64 columns), a 4 KB tile of 4 x 64
 // 16-byte words, word [c][lane] = what MFMA lane `lane` takes as its c-th B
@@ -67,19 +68,29 @@ int ffn_rows_per_item() { return kItemRows; }
 // (4g+w)*64m + 64*stream + 4*(lane&15) .. +3 of K-row 16s + 4*(lane>>4) + c.
 // Outside [0,Kd) x [0,N) the words hold zeros. A workgroup's K range of one
 // column group is then one contiguous run of 16 KB (x m) steps.
+//
+// Microscaled 4-bit weights (kMx4, written by mx4.hip) have the same order of
+// tiles with 16-bit K-steps; a tile is 1024 bytes of codes and 64 of scales:
+// word [lane] (16 bytes) holds the 4 columns' operands of that lane as above, 8
+// codes of 4 bits each (K-value i in bits 4 i of dword c), and scale byte
+// 4*(lane&15) + c the power of two 2^(byte - 127) of the 32 K-values of that
+// column: a K-step is one block of the format.
 struct PackedGeom {
     int gs, nst, m;       // column groups, K-steps, streams
+    uint32_t tile_bytes;  // of one K-step of one slice's stream
     uint32_t step_bytes;  // bytes of one K-step of one column group
 };
 
-__host__ __device__ inline PackedGeom packed_geom(int Kd, int N, bool gateup, int es)
+__host__ __device__ inline PackedGeom packed_geom(int Kd, int N, bool gateup, int es,
+                                                  bool mx4 = false)
 {
     PackedGeom z;
     z.m = gateup ? 1 : 2;
     const int kstep = es == 2 ? 32 : 16;
     z.gs = (N + 256 * z.m - 1) / (256 * z.m);
     z.nst = (Kd + kstep - 1) / kstep;
-    z.step_bytes = 16384u * (uint32_t)z.m;
+    z.tile_bytes = mx4 ? kMx4Tile : 4096u;
+    z.step_bytes = 4 * z.tile_bytes * (uint32_t)z.m;
     return z;
 }
 
@@ -344,6 +355,15 @@ template <> struct Elt<_Float16> {
         return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8_t, a),
                                                       __builtin_bit_cast(half8_t, b), c, 0, 0, 0);
     }
+    // 8 codes of 4 bits times their scale (exact within the type's range)
+    static __device__ __forceinline__ uint4 mx4(uint32_t codes, float scale)
+    {
+        return make_uint4(
+            __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(codes, scale, 0)),
+            __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(codes, scale, 1)),
+            __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(codes, scale, 2)),
+            __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(codes, scale, 3)));
+    }
     static __device__ __forceinline__ uint32_t pack2(float lo, float hi)
     {
         const _Float16 l = (_Float16)lo, h = (_Float16)hi;
@@ -358,6 +378,14 @@ template <> struct Elt<__bf16> {
     {
         return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a),
                                                        __builtin_bit_cast(bf16x8_t, b), c, 0, 0, 0);
+    }
+    static __device__ __forceinline__ uint4 mx4(uint32_t codes, float scale)
+    {
+        return make_uint4(
+            __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, scale, 0)),
+            __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, scale, 1)),
+            __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, scale, 2)),
+            __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, scale, 3)));
     }
     static __device__ __forceinline__ uint32_t pack2(float lo, float hi)
     {
@@ -412,6 +440,26 @@ __device__ __forceinline__ float lanef(const uint4 &v, int q)
 __device__ __forceinline__ uint4 mask4(uint4 v, uint32_t m)
 {
     return make_uint4(v.x & m, v.y & m, v.z & m, v.w & m);
+}
+
+// A lane's weights of one K-step and stream in 4 bits: the 4 columns' codes and
+// scale bytes; column c as an MFMA operand
+struct Mx4Word {
+    uint4 codes;
+    uint32_t scales;
+};
+template <int POLICY = 0>
+__device__ __forceinline__ Mx4Word load_mx4(__amdgpu_buffer_rsrc_t r, uint32_t tile, int lane)
+{
+    Mx4Word w;
+    w.codes = Ld<16, POLICY>::run(r, tile + (uint32_t)lane * 16u, 0u);
+    w.scales = (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(
+        r, tile + (uint32_t)(lane & 15) * 4u, kMx4Codes, POLICY);
+    return w;
+}
+template <typename T> __device__ __forceinline__ uint4 mx4_operand(const Mx4Word &w, int c)
+{
+    return Elt<T>::mx4(word(w.codes, c), __uint_as_float(((w.scales >> (8 * c)) & 0xffu) << 23));
 }
 
 // Arguments of one grouped GEMM launch.
@@ -625,6 +673,8 @@ constexpr int kDeepBelowCells = 512;
 // Pipeline depth of the wide cells for NMT m-tiles: stage = 32 B-operand + 4
 // A-operand VGPRs, accumulators = 32*NMT VGPRs; S stages + accumulators stay
 // <= ~232.
+// 4-bit weights: 14 VGPRs a stage.
+constexpr int kMx4Stages = 4;
 constexpr int stages_for(int nmt) { return nmt >= 4 ? 2 : nmt == 3 ? 3 : nmt == 2 ? 4 : 5; }
 
 // Shared A tile of one K-step: 64 rows x 32 K (16-bit) or 64 rows x 16 K
@@ -668,7 +718,7 @@ constexpr int kLdsU4 = 2 * tall_buf_u4(2) > 2 * kATileU4 ? 2 * tall_buf_u4(2) : 
 // GATHERED (gate/up only): A is the token activation x [a_rows][Kd] and row r
 // of the item reads x[stok[r]] -- the gather fused into the A-tile loads.
 // The K range is [kb, ke) (a split of the reduction, or all of it).
-template <typename T, bool GATEUP, bool GATHERED, bool PACKED, bool DEEP, int NMT>
+template <typename T, bool GATEUP, bool GATHERED, int WF, bool DEEP, int NMT>
 __device__ __forceinline__ void wide_cells(const GemmArgs &p, const WorkItem it, int slice,
                                            int kb, int ke, int split, uint4 *__restrict__ a_lds,
                                            float2 *__restrict__ rinfo, const int *ltok)
@@ -699,22 +749,23 @@ __device__ __forceinline__ void wide_cells(const GemmArgs &p, const WorkItem it,
     // slice: its loads return zeros without memory traffic), this item's rows
     __amdgpu_buffer_rsrc_t rb0, rb1;
     uint32_t vcol, rowb, bstep;  // lane offset, B row stride, B bytes per K-step
-    if constexpr (PACKED) {
-        // this wavefront's tiles (g, s, w, m) for s in [s0, s1): 4 KB each,
-        // one K-step apart (16 KB x streams)
+    if constexpr (WF != kRowMajor) {
+        // this wavefront's tiles (g, s, w, m) for s in [s0, s1): 4 KB (4-bit
+        // weights: 1088 bytes) each, one K-step of the group apart
         const int g = slice >> 2, w = slice & 3;
-        const PackedGeom z = packed_geom(Kd, N, GATEUP, ES);
+        const PackedGeom z = packed_geom(Kd, N, GATEUP, ES, WF == kMx4);
         const int s0 = kb / KSTEP, s1 = (ke + KSTEP - 1) / KSTEP;
-        const size_t tb = ((((size_t)it.expert * z.gs + g) * z.nst + s0) * 4 + w) * z.m * 4096;
+        const size_t tb =
+            ((((size_t)it.expert * z.gs + g) * z.nst + s0) * 4 + w) * z.m * z.tile_bytes;
         const uint32_t span = (uint32_t)(s1 - s0) * z.step_bytes;
         const uint32_t r0 = (uint32_t)__builtin_amdgcn_readfirstlane(
-            (int)(slice_ok ? span - (uint32_t)(w * z.m) * 4096u : 0u));
+            (int)(slice_ok ? span - (uint32_t)(w * z.m) * z.tile_bytes : 0u));
         const uint32_t r1 = (uint32_t)__builtin_amdgcn_readfirstlane(
-            (int)(slice_ok ? span - (uint32_t)(w * z.m + z.m - 1) * 4096u : 0u));
+            (int)(slice_ok ? span - (uint32_t)(w * z.m + z.m - 1) * z.tile_bytes : 0u));
         const char *b0c = static_cast<const char *>(p.B0);
         rb0 = make_rsrc(b0c + tb, r0);
         rb1 = GATEUP ? make_rsrc(static_cast<const char *>(p.B1) + tb, r0)
-                     : make_rsrc(b0c + tb + 4096, r1);
+                     : make_rsrc(b0c + tb + z.tile_bytes, r1);
         vcol = (uint32_t)lane * 16;
         rowb = 1024;  // between fragments c of one lane
         bstep = z.step_bytes;
@@ -760,21 +811,30 @@ __device__ __forceinline__ void wide_cells(const GemmArgs &p, const WorkItem it,
 #pragma unroll
             for (int c = 0; c < NPL; ++c) acc[m][mt][c] = float4_t{0.f, 0.f, 0.f, 0.f};
 
-    // packed: 4 fragments (fp32: 4 rows) of 16 bytes per stream and step
-    constexpr int NB = PACKED ? 4 : KR;
-    constexpr int LBB = PACKED ? 16 : LB;
-    typedef typename Ld<LBB>::type BT;
+    // packed: 4 fragments (fp32: 4 rows) of 16 bytes per stream and step; 4-bit
+    // weights: one word of 4 fragments and their scales
+    constexpr int NB = WF == kMx4 ? 1 : WF == kPacked ? 4 : KR;
+    constexpr int LBB = WF == kRowMajor ? LB : 16;
+    typedef typename std::conditional<WF == kMx4, Mx4Word, typename Ld<LBB>::type>::type BT;
     struct Stage {
         BT b[NMAT][NB];
         uint4 a;
     };
     auto load = [&](Stage &st, int k0) {
-        const uint32_t vb = PACKED ? vcol + (uint32_t)((k0 - kb) / KSTEP) * bstep
-                                   : vcol + (uint32_t)(k0 + KR * kg - kb) * rowb;
+        const uint32_t step = (uint32_t)((k0 - kb) / KSTEP);
+        if constexpr (WF == kMx4) {
+            st.b[0][0] = load_mx4<kNT>(rb0, step * bstep, lane);
+            st.b[1][0] = load_mx4<kNT>(rb1, step * bstep, lane);
+        } else {
+            const uint32_t vb = WF == kPacked ? vcol + step * bstep
+                                              : vcol + (uint32_t)(k0 + KR * kg - kb) * rowb;
 #pragma unroll
-        for (int i = 0; i < NB; ++i) st.b[0][i] = Ld<LBB, kNT>::run(rb0, vb, (uint32_t)i * rowb);
+            for (int i = 0; i < NB; ++i)
+                st.b[0][i] = Ld<LBB, kNT>::run(rb0, vb, (uint32_t)i * rowb);
 #pragma unroll
-        for (int i = 0; i < NB; ++i) st.b[1][i] = Ld<LBB, kNT>::run(rb1, vb, (uint32_t)i * rowb);
+            for (int i = 0; i < NB; ++i)
+                st.b[1][i] = Ld<LBB, kNT>::run(rb1, vb, (uint32_t)i * rowb);
+        }
         // K past the range: the weights read as zero; zero A too so that no
         // non-finite value of a neighbouring row can leak in as 0 * inf.
         // Shallow: masked here, which makes the wavefront wait for the step's
@@ -797,7 +857,9 @@ __device__ __forceinline__ void wide_cells(const GemmArgs &p, const WorkItem it,
 #pragma unroll
                 for (int m = 0; m < NMAT; ++m) {
                     uint4 fb;
-                    if constexpr (PACKED)
+                    if constexpr (WF == kMx4)
+                        fb = mx4_operand<T>(st.b[m][0], c);
+                    else if constexpr (WF == kPacked)
                         fb = st.b[m][c];
                     else
                         fb = column_of_rows(st.b[m], c);
@@ -823,7 +885,7 @@ __device__ __forceinline__ void wide_cells(const GemmArgs &p, const WorkItem it,
         }
     };
 
-    constexpr int S = stages_for(NMT);
+    constexpr int S = WF == kMx4 ? kMx4Stages : stages_for(NMT);
     const int nsteps = (ke - kb + KSTEP - 1) / KSTEP;
     Stage st[S];
     // deep: the prologue's loads stay in step order (the load-count waits at
@@ -861,7 +923,7 @@ __device__ __forceinline__ void wide_cells(const GemmArgs &p, const WorkItem it,
 // Every wavefront computes 4 m-tiles (a short last item computes zero rows).
 // The weight loads keep the default cache policy here: the other runs of the
 // same expert read the same tile, often while it is still in L2.
-template <typename T, bool GATEUP, bool GATHERED, bool PACKED, bool DEEP, int R>
+template <typename T, bool GATEUP, bool GATHERED, int WF, bool DEEP, int R>
 __device__ __forceinline__ void tall_cells(const GemmArgs &p, const WorkItem *__restrict__ items,
                                            int i0, int nitems, int g, int j, int kb, int ke,
                                            int split, uint4 *__restrict__ lds,
@@ -907,19 +969,21 @@ __device__ __forceinline__ void tall_cells(const GemmArgs &p, const WorkItem *__
     const int plu = C == 1 ? ((tid >> 1) & 63) : lane;
     const int hh = C == 1 ? (tid & 1) : 0;
     const int pslice = 4 * g + C * j + pcs;
-    // packed: a producer thread copies 4/H whole fragments (fp32: rows) of its unit
-    constexpr int PNB = PACKED ? 4 / H : RP;
+    // packed: a producer thread copies 4/H whole fragments (fp32: rows) of its unit;
+    // 4-bit weights: it makes the unit's 4 fragments from its codes
+    static_assert(WF != kMx4 || H == 1, "a unit's word has one producer");
+    constexpr int PNB = WF == kMx4 ? 1 : WF == kPacked ? 4 / H : RP;
     __amdgpu_buffer_rsrc_t rbp;
     uint32_t rowb, vpb, bstep;
-    if constexpr (PACKED) {
-        const PackedGeom z = packed_geom(Kd, N, GATEUP, ES);
+    if constexpr (WF != kRowMajor) {
+        const PackedGeom z = packed_geom(Kd, N, GATEUP, ES, WF == kMx4);
         const int s0 = kb / KSTEP, s1 = (ke + KSTEP - 1) / KSTEP;
         const int wp = C * j + pcs, mm = GATEUP ? 0 : pm;  // tile slot in the group
         const size_t tb =
-            (((((size_t)expert * z.gs + g) * z.nst + s0) * 4 + wp) * z.m + mm) * 4096;
+            (((((size_t)expert * z.gs + g) * z.nst + s0) * 4 + wp) * z.m + mm) * z.tile_bytes;
         const uint32_t span = (uint32_t)(s1 - s0) * z.step_bytes;
         const uint32_t pbytes = (uint32_t)__builtin_amdgcn_readfirstlane(
-            (int)(pslice * SW >= N ? 0u : span - (uint32_t)(wp * z.m + mm) * 4096u));
+            (int)(pslice * SW >= N ? 0u : span - (uint32_t)(wp * z.m + mm) * z.tile_bytes));
         const char *bb = static_cast<const char *>(GATEUP && pm ? p.B1 : p.B0);
         rbp = make_rsrc(bb + tb, pbytes);
         rowb = 1024;
@@ -968,16 +1032,21 @@ __device__ __forceinline__ void tall_cells(const GemmArgs &p, const WorkItem *__
 #pragma unroll
             for (int c = 0; c < NPL; ++c) acc[m][mt][c] = float4_t{0.f, 0.f, 0.f, 0.f};
 
-    constexpr int LBB = PACKED ? 16 : LB;
-    typedef typename Ld<LBB>::type BT;
+    constexpr int LBB = WF == kRowMajor ? LB : 16;
+    typedef typename std::conditional<WF == kMx4, Mx4Word, typename Ld<LBB>::type>::type BT;
     struct Stage {
         BT b[PNB];
         uint4 a[NMT];
     };
     auto load = [&](Stage &st, int k0) {
-        const uint32_t vb = vpb + (uint32_t)((k0 - kb) / KSTEP) * bstep;
+        const uint32_t step = (uint32_t)((k0 - kb) / KSTEP);
+        if constexpr (WF == kMx4) {
+            st.b[0] = load_mx4(rbp, step * bstep, plu);
+        } else {
+            const uint32_t vb = vpb + step * bstep;
 #pragma unroll
-        for (int i = 0; i < PNB; ++i) st.b[i] = Ld<LBB>::run(rbp, vb, (uint32_t)i * rowb);
+            for (int i = 0; i < PNB; ++i) st.b[i] = Ld<LBB>::run(rbp, vb, (uint32_t)i * rowb);
+        }
         // A past the K range masked here (shallow) or at its use (deep), as in
         // the wide cells
         const int ka = k0 + KR * kg;
@@ -996,7 +1065,10 @@ __device__ __forceinline__ void tall_cells(const GemmArgs &p, const WorkItem *__
         uint4 a[NMT];
 #pragma unroll
         for (int mt = 0; mt < NMT; ++mt) a[mt] = DEEP ? mask4(st.a[mt], am) : st.a[mt];
-        if constexpr (PACKED) {
+        if constexpr (WF == kMx4) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c) buf[frag(pcs, pm, c, plu)] = mx4_operand<T>(st.b[0], c);
+        } else if constexpr (WF == kPacked) {
 #pragma unroll
             for (int i = 0; i < PNB; ++i) buf[frag(pcs, pm, PNB * hh + i, plu)] = st.b[i];
         } else if constexpr (ES == 2) {
@@ -1064,7 +1136,7 @@ __device__ __forceinline__ void tall_cells(const GemmArgs &p, const WorkItem *__
 }
 
 // The cell of item i: a tall cell for an item in a run, else a wide cell.
-template <typename T, bool GATEUP, bool GATHERED, bool PACKED, bool DEEP>
+template <typename T, bool GATEUP, bool GATHERED, int WF, bool DEEP>
 __device__ __forceinline__ void gemm_cell(const GemmArgs &p, const WorkItem *__restrict__ items,
                                           const WorkItem it, int i, int nitems, int g, int kb,
                                           int ke, int split, uint4 *__restrict__ lds,
@@ -1074,12 +1146,12 @@ __device__ __forceinline__ void gemm_cell(const GemmArgs &p, const WorkItem *__r
     // a run of 4 is taken as two runs of 2 (4-item cells, one column slice of
     // 256 rows each: the skewed long prompt's layer 0.8% slower)
     if (run == 4 && j < 4 && i >= j) {
-        tall_cells<T, GATEUP, GATHERED, PACKED, DEEP, 2>(p, items, i - (j & 1), nitems, g, j & 1,
+        tall_cells<T, GATEUP, GATHERED, WF, DEEP, 2>(p, items, i - (j & 1), nitems, g, j & 1,
                                                          kb, ke, split, lds, rinfo);
         return;
     }
     if (run == 2 && j < 2 && i >= j) {
-        tall_cells<T, GATEUP, GATHERED, PACKED, DEEP, 2>(p, items, i - j, nitems, g, j, kb, ke,
+        tall_cells<T, GATEUP, GATHERED, WF, DEEP, 2>(p, items, i - j, nitems, g, j, kb, ke,
                                                          split, lds, rinfo);
         return;
     }
@@ -1087,15 +1159,15 @@ __device__ __forceinline__ void gemm_cell(const GemmArgs &p, const WorkItem *__r
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int slice = g * kWavesPerBlock + wave;
     switch ((it.nrows + 15) >> 4) {  // m-tiles of this item (uniform per workgroup)
-    case 1: wide_cells<T, GATEUP, GATHERED, PACKED, DEEP, 1>(p, it, slice, kb, ke, split, lds, rinfo, nullptr); break;
-    case 2: wide_cells<T, GATEUP, GATHERED, PACKED, DEEP, 2>(p, it, slice, kb, ke, split, lds, rinfo, nullptr); break;
-    case 3: wide_cells<T, GATEUP, GATHERED, PACKED, DEEP, 3>(p, it, slice, kb, ke, split, lds, rinfo, nullptr); break;
-    default: wide_cells<T, GATEUP, GATHERED, PACKED, DEEP, kMT>(p, it, slice, kb, ke, split, lds, rinfo, nullptr); break;
+    case 1: wide_cells<T, GATEUP, GATHERED, WF, DEEP, 1>(p, it, slice, kb, ke, split, lds, rinfo, nullptr); break;
+    case 2: wide_cells<T, GATEUP, GATHERED, WF, DEEP, 2>(p, it, slice, kb, ke, split, lds, rinfo, nullptr); break;
+    case 3: wide_cells<T, GATEUP, GATHERED, WF, DEEP, 3>(p, it, slice, kb, ke, split, lds, rinfo, nullptr); break;
+    default: wide_cells<T, GATEUP, GATHERED, WF, DEEP, kMT>(p, it, slice, kb, ke, split, lds, rinfo, nullptr); break;
     }
 }
 
 // A single item's wide cell, its token rows from LDS (ltok[r] for row r).
-template <typename T, bool GATEUP, bool GATHERED, bool PACKED, bool DEEP>
+template <typename T, bool GATEUP, bool GATHERED, int WF, bool DEEP>
 __device__ __forceinline__ void single_cell(const GemmArgs &p, const WorkItem it, int g, int kb,
                                             int ke, int split, uint4 *__restrict__ lds,
                                             float2 *__restrict__ rinfo, const int *ltok)
@@ -1103,10 +1175,10 @@ __device__ __forceinline__ void single_cell(const GemmArgs &p, const WorkItem it
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int slice = g * kWavesPerBlock + wave;
     switch ((it.nrows + 15) >> 4) {  // m-tiles of this item (uniform per workgroup)
-    case 1: wide_cells<T, GATEUP, GATHERED, PACKED, DEEP, 1>(p, it, slice, kb, ke, split, lds, rinfo, ltok); break;
-    case 2: wide_cells<T, GATEUP, GATHERED, PACKED, DEEP, 2>(p, it, slice, kb, ke, split, lds, rinfo, ltok); break;
-    case 3: wide_cells<T, GATEUP, GATHERED, PACKED, DEEP, 3>(p, it, slice, kb, ke, split, lds, rinfo, ltok); break;
-    default: wide_cells<T, GATEUP, GATHERED, PACKED, DEEP, kMT>(p, it, slice, kb, ke, split, lds, rinfo, ltok); break;
+    case 1: wide_cells<T, GATEUP, GATHERED, WF, DEEP, 1>(p, it, slice, kb, ke, split, lds, rinfo, ltok); break;
+    case 2: wide_cells<T, GATEUP, GATHERED, WF, DEEP, 2>(p, it, slice, kb, ke, split, lds, rinfo, ltok); break;
+    case 3: wide_cells<T, GATEUP, GATHERED, WF, DEEP, 3>(p, it, slice, kb, ke, split, lds, rinfo, ltok); break;
+    default: wide_cells<T, GATEUP, GATHERED, WF, DEEP, kMT>(p, it, slice, kb, ke, split, lds, rinfo, ltok); break;
     }
 }
 
@@ -1119,7 +1191,7 @@ __device__ __forceinline__ void single_cell(const GemmArgs &p, const WorkItem it
 // to read) and keeps the item's tokens in LDS for its A-operand rows. A
 // template instance of its own, so that the other launches' code is
 // untouched.
-template <typename T, bool GATEUP, bool GATHERED, bool PACKED, bool WP = false>
+template <typename T, bool GATEUP, bool GATHERED, int WF, bool WP = false>
 __global__ __launch_bounds__(256, 2) void k_expert_gemm(const GemmArgs p,
                                                         const int32_t *__restrict__ ctl,
                                                         const WorkItem *__restrict__ items,
@@ -1167,9 +1239,9 @@ __global__ __launch_bounds__(256, 2) void k_expert_gemm(const GemmArgs p,
         const int kb = split * p.split_steps * KSTEP;
         const int ke = min(p.Kd, kb + p.split_steps * KSTEP);
         if (nitems * per_item < kDeepBelowCells)  // (no runs)
-            single_cell<T, true, true, PACKED, true>(p, it, g, kb, ke, split, lds, rinfo, s_tok);
+            single_cell<T, true, true, WF, true>(p, it, g, kb, ke, split, lds, rinfo, s_tok);
         else
-            single_cell<T, true, true, PACKED, false>(p, it, g, kb, ke, split, lds, rinfo, s_tok);
+            single_cell<T, true, true, WF, false>(p, it, g, kb, ke, split, lds, rinfo, s_tok);
     } else {
         const int nitems = ctl[0];
         const int ifirst = p.skip_quads ? min(ctl[1], nitems) : 0;
@@ -1186,10 +1258,10 @@ __global__ __launch_bounds__(256, 2) void k_expert_gemm(const GemmArgs p,
         // are in runs or when the cells do not fill the GPU's workgroup slots,
         // else shallow (the same for every workgroup)
         if (2 * ctl[2] >= nitems || (nitems - ifirst) * per_item < kDeepBelowCells)
-            gemm_cell<T, GATEUP, GATHERED, PACKED, true>(p, items, it, i, nitems, g, kb, ke, split,
+            gemm_cell<T, GATEUP, GATHERED, WF, true>(p, items, it, i, nitems, g, kb, ke, split,
                                                          lds, rinfo);
         else
-            gemm_cell<T, GATEUP, GATHERED, PACKED, false>(p, items, it, i, nitems, g, kb, ke,
+            gemm_cell<T, GATEUP, GATHERED, WF, false>(p, items, it, i, nitems, g, kb, ke,
                                                           split, lds, rinfo);
     }
 }
@@ -1662,7 +1734,7 @@ GemmArgs gemm_args(const FfnShape &z, const void *scratch, bool gateup)
 
 unsigned reduce_blocks(int64_t rows, int N) { return (unsigned)((rows * (N / 4) + 255) / 256); }
 
-template <typename T, bool PACKED>
+template <typename T, int WF>
 hipError_t gateup_t(const FfnShape &z, const void *a, int a_rows, bool gathered,
                     const int32_t *stok, const void *wg, const void *wu, int d, int f,
                     const int32_t *meta, const void *scratch, void *h, hipStream_t s,
@@ -1678,7 +1750,7 @@ hipError_t gateup_t(const FfnShape &z, const void *a, int a_rows, bool gathered,
     p.Kd = d;
     p.N = f;
     const dim3 grid((unsigned)z.blocks_gu);
-    if constexpr (PACKED && sizeof(T) == 2) {
+    if constexpr (WF == kPacked && sizeof(T) == 2) {
         if (z.big_gu && z.blocks_big_gu > 0) {
             p.skip_quads = 1;
             const dim3 bgrid((unsigned)z.blocks_big_gu);
@@ -1692,13 +1764,13 @@ hipError_t gateup_t(const FfnShape &z, const void *a, int a_rows, bool gathered,
     }
     const WavePlan none{};
     if (gathered && wp && wp->ids)  // planned here: 8 workgroups before the cells'
-        hipLaunchKernelGGL((k_expert_gemm<T, true, true, PACKED, true>), dim3(grid.x + 8),
+        hipLaunchKernelGGL((k_expert_gemm<T, true, true, WF, true>), dim3(grid.x + 8),
                            dim3(256), 0, s, p, ctl_of(scratch), items_of(scratch), *wp);
     else if (gathered)  // rows gathered from x through stok
-        hipLaunchKernelGGL((k_expert_gemm<T, true, true, PACKED>), grid, dim3(256), 0, s, p,
+        hipLaunchKernelGGL((k_expert_gemm<T, true, true, WF>), grid, dim3(256), 0, s, p,
                            ctl_of(scratch), items_of(scratch), none);
     else
-        hipLaunchKernelGGL((k_expert_gemm<T, true, false, PACKED>), grid, dim3(256), 0, s, p,
+        hipLaunchKernelGGL((k_expert_gemm<T, true, false, WF>), grid, dim3(256), 0, s, p,
                            ctl_of(scratch), items_of(scratch), none);
     if (z.split_gu > 1) {
         const hipError_t e = reduce_gateup<T>(p.nsplit, dim3(reduce_blocks(z.max_rows, f)), s,
@@ -1709,7 +1781,7 @@ hipError_t gateup_t(const FfnShape &z, const void *a, int a_rows, bool gathered,
     return hipGetLastError();
 }
 
-template <typename T, bool PACKED>
+template <typename T, int WF>
 hipError_t down_t(const FfnShape &z, const void *h, const void *wd, int d, int f,
                   const int32_t *stok, const float *sw, const int32_t *meta, const void *scratch,
                   void *y, int8_t *yexp, hipStream_t s)
@@ -1728,14 +1800,14 @@ hipError_t down_t(const FfnShape &z, const void *h, const void *wd, int d, int f
         p.estride = z.max_rows;
         nyb = (d + kY16Block - 1) / kY16Block;
     }
-    if constexpr (PACKED && sizeof(T) == 2) {
+    if constexpr (WF == kPacked && sizeof(T) == 2) {
         if (z.big_dn && z.blocks_big_dn > 0) {
             p.skip_quads = 1;
             hipLaunchKernelGGL((k_big<T, false, false>), dim3((unsigned)z.blocks_big_dn),
                                dim3(kBigThreads), 0, s, p, ctl_of(scratch), items_of(scratch));
         }
     }
-    hipLaunchKernelGGL((k_expert_gemm<T, false, false, PACKED>), dim3((unsigned)z.blocks_dn),
+    hipLaunchKernelGGL((k_expert_gemm<T, false, false, WF>), dim3((unsigned)z.blocks_dn),
                        dim3(256), 0, s, p, ctl_of(scratch), items_of(scratch), WavePlan{});
     if (z.split_dn > 1) {
         const hipError_t e =
@@ -1750,61 +1822,76 @@ hipError_t down_t(const FfnShape &z, const void *h, const void *wd, int d, int f
     return hipGetLastError();
 }
 
+// the weight format as a template argument (fp32 has no 4-bit form: the caller refuses it)
 template <typename T>
-hipError_t gateup_any(const FfnShape &z, bool packed, const void *a, int a_rows, bool gathered,
+hipError_t gateup_any(const FfnShape &z, int wf, const void *a, int a_rows, bool gathered,
                       const int32_t *stok, const void *wg, const void *wu, int d, int f,
                       const int32_t *meta, const void *scratch, void *h, hipStream_t s,
                       const WavePlan *wp = nullptr)
 {
-    return packed ? gateup_t<T, true>(z, a, a_rows, gathered, stok, wg, wu, d, f, meta, scratch, h,
-                                      s, wp)
-                  : gateup_t<T, false>(z, a, a_rows, gathered, stok, wg, wu, d, f, meta, scratch, h,
-                                       s, wp);
+    if constexpr (sizeof(T) == 2)
+        if (wf == kMx4)
+            return gateup_t<T, kMx4>(z, a, a_rows, gathered, stok, wg, wu, d, f, meta, scratch, h,
+                                     s, wp);
+    return wf == kPacked ? gateup_t<T, kPacked>(z, a, a_rows, gathered, stok, wg, wu, d, f, meta,
+                                                scratch, h, s, wp)
+                         : gateup_t<T, kRowMajor>(z, a, a_rows, gathered, stok, wg, wu, d, f,
+                                                  meta, scratch, h, s, wp);
+}
+
+template <typename T>
+hipError_t down_any(const FfnShape &z, int wf, const void *h, const void *wd, int d, int f,
+                    const int32_t *stok, const float *sw, const int32_t *meta, const void *scratch,
+                    void *y, int8_t *yexp, hipStream_t s)
+{
+    if constexpr (sizeof(T) == 2)
+        if (wf == kMx4)
+            return down_t<T, kMx4>(z, h, wd, d, f, stok, sw, meta, scratch, y, yexp, s);
+    return wf == kPacked
+               ? down_t<T, kPacked>(z, h, wd, d, f, stok, sw, meta, scratch, y, yexp, s)
+               : down_t<T, kRowMajor>(z, h, wd, d, f, stok, sw, meta, scratch, y, yexp, s);
 }
 
 }  // namespace
 
-hipError_t launch_gateup(const FfnShape &z, int dtype, bool packed, const void *xs,
+hipError_t launch_gateup(const FfnShape &z, int dtype, int wf, const void *xs,
                          const int32_t *stok, const void *wg, const void *wu, int d, int f,
                          const int32_t *meta, const void *scratch, void *h, hipStream_t s)
 {
     if (dtype == 1)
-        return gateup_any<_Float16>(z, packed, xs, 0, false, stok, wg, wu, d, f, meta, scratch, h, s);
+        return gateup_any<_Float16>(z, wf, xs, 0, false, stok, wg, wu, d, f, meta, scratch, h, s);
     if (dtype == 2)
-        return gateup_any<__bf16>(z, packed, xs, 0, false, stok, wg, wu, d, f, meta, scratch, h, s);
-    return gateup_any<float>(z, packed, xs, 0, false, stok, wg, wu, d, f, meta, scratch, h, s);
+        return gateup_any<__bf16>(z, wf, xs, 0, false, stok, wg, wu, d, f, meta, scratch, h, s);
+    return gateup_any<float>(z, wf, xs, 0, false, stok, wg, wu, d, f, meta, scratch, h, s);
 }
 
-hipError_t launch_gateup_gathered(const FfnShape &z, int dtype, bool packed, const void *x, int T,
+hipError_t launch_gateup_gathered(const FfnShape &z, int dtype, int wf, const void *x, int T,
                                   const int32_t *stok, const void *wg, const void *wu, int d, int f,
                                   const int32_t *meta, const void *scratch, void *h, hipStream_t s,
                                   const WavePlan *wp)
 {
     if (dtype == 1)
-        return gateup_any<_Float16>(z, packed, x, T, true, stok, wg, wu, d, f, meta, scratch, h, s,
+        return gateup_any<_Float16>(z, wf, x, T, true, stok, wg, wu, d, f, meta, scratch, h, s,
                                     wp);
     if (dtype == 2)
-        return gateup_any<__bf16>(z, packed, x, T, true, stok, wg, wu, d, f, meta, scratch, h, s,
+        return gateup_any<__bf16>(z, wf, x, T, true, stok, wg, wu, d, f, meta, scratch, h, s,
                                   wp);
-    return gateup_any<float>(z, packed, x, T, true, stok, wg, wu, d, f, meta, scratch, h, s, wp);
+    return gateup_any<float>(z, wf, x, T, true, stok, wg, wu, d, f, meta, scratch, h, s, wp);
 }
 
 // every expert of a call of at most 64 entries pads to at most 64 rows (one
 // work item) when tm divides 64
 bool wave_plan_fits(int64_t nent, int tm) { return nent <= kWave && tm >= 1 && kWave % tm == 0; }
 
-hipError_t launch_down(const FfnShape &z, int dtype, bool packed, const void *h, const void *wd,
+hipError_t launch_down(const FfnShape &z, int dtype, int wf, const void *h, const void *wd,
                        int d, int f, const int32_t *stok, const float *sw, const int32_t *meta,
                        const void *scratch, void *y, int8_t *yexp, hipStream_t s)
 {
     if (dtype == 1)
-        return packed ? down_t<_Float16, true>(z, h, wd, d, f, stok, sw, meta, scratch, y, yexp, s)
-                      : down_t<_Float16, false>(z, h, wd, d, f, stok, sw, meta, scratch, y, yexp, s);
+        return down_any<_Float16>(z, wf, h, wd, d, f, stok, sw, meta, scratch, y, yexp, s);
     if (dtype == 2)
-        return packed ? down_t<__bf16, true>(z, h, wd, d, f, stok, sw, meta, scratch, y, yexp, s)
-                      : down_t<__bf16, false>(z, h, wd, d, f, stok, sw, meta, scratch, y, yexp, s);
-    return packed ? down_t<float, true>(z, h, wd, d, f, stok, sw, meta, scratch, y, nullptr, s)
-                  : down_t<float, false>(z, h, wd, d, f, stok, sw, meta, scratch, y, nullptr, s);
+        return down_any<__bf16>(z, wf, h, wd, d, f, stok, sw, meta, scratch, y, yexp, s);
+    return down_any<float>(z, wf, h, wd, d, f, stok, sw, meta, scratch, y, nullptr, s);
 }
 
 }  // namespace moe

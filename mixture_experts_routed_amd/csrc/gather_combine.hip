@@ -121,12 +121,12 @@ __global__ __launch_bounds__(kGatherWaves * kWave) void k_gather(
 // the workgroup: prefill 26.9 us, decode 8.0 us; not kept.)
 constexpr int kCombineGroup = 16;
 
-template <bool Y16, int G>
+template <bool Y16, int G, typename O>
 __global__ __launch_bounds__(1024) void k_combine(const void *__restrict__ y,
                                                  const int8_t *__restrict__ yexp,
                                                  int64_t max_rows, int d,
                                                  const int32_t *__restrict__ pos, int T, int K,
-                                                 float4 *__restrict__ out)
+                                                 O *__restrict__ out)
 {
     constexpr int COLS = Y16 ? 8 : 4;  // columns per lane
     typedef uint32_t u4 __attribute__((ext_vector_type(4)));
@@ -173,22 +173,32 @@ __global__ __launch_bounds__(1024) void k_combine(const void *__restrict__ y,
                 }
             }
         }
+        if constexpr (sizeof(O) == 4) {
 #pragma unroll
-        for (int c = 0; c < COLS; c += 4)
-            store_nt(out + (int64_t)t * (d / 4) + j * (COLS / 4) + c / 4,
-                     make_float4(acc[c], acc[c + 1], acc[c + 2], acc[c + 3]));
+            for (int c = 0; c < COLS; c += 4)
+                store_nt(reinterpret_cast<float4 *>(out) + (int64_t)t * (d / 4) + j * (COLS / 4) +
+                             c / 4,
+                         make_float4(acc[c], acc[c + 1], acc[c + 2], acc[c + 3]));
+        } else {
+            // (the only rounding of the sum: to the output's type, nearest even)
+            typedef O vec __attribute__((ext_vector_type(COLS)));
+            vec v;
+#pragma unroll
+            for (int c = 0; c < COLS; ++c) v[c] = (O)acc[c];
+            __builtin_nontemporal_store(v, reinterpret_cast<vec *>(out) + (int64_t)t * nvec + j);
+        }
     }
 }
 
 // the smallest group size of the instantiated ones that covers min(K, 16)
 // entries, so that no lane loads rows for slots past K
-template <bool Y16>
+template <bool Y16, typename O>
 void combine_any(int K, dim3 grid, dim3 block, hipStream_t s, const void *y, const int8_t *yexp,
-                 int64_t max_rows, int d, const int32_t *pos, int T, float4 *out)
+                 int64_t max_rows, int d, const int32_t *pos, int T, O *out)
 {
     const int g = K < kCombineGroup ? K : kCombineGroup;
 #define MOE_COMBINE(G)                                                                         \
-    hipLaunchKernelGGL((k_combine<Y16, G>), grid, block, 0, s, y, yexp, max_rows, d, pos, T, K, \
+    hipLaunchKernelGGL((k_combine<Y16, G, O>), grid, block, 0, s, y, yexp, max_rows, d, pos, T, K, \
                        out)
     if (g <= 2)
         MOE_COMBINE(2);
@@ -217,22 +227,34 @@ hipError_t launch_gather(const void *x, int elem_bytes, int T, int d, const int3
     return hipGetLastError();
 }
 
-hipError_t launch_combine(const float *y, int64_t max_rows, const int32_t *pos, int T, int K,
-                          int d, float *out, hipStream_t s)
+template <bool Y16>
+hipError_t combine_as(const void *y, const int8_t *yexp, int64_t max_rows, const int32_t *pos,
+                      int T, int K, int d, void *out, int out_dtype, hipStream_t s)
 {
-    const int threads = min(1024, (d / 4 + kWave - 1) / kWave * kWave);
-    combine_any<false>(K, dim3(T), dim3(threads), s, y, nullptr, max_rows, d, pos, T,
-                       reinterpret_cast<float4 *>(out));
+    const int threads = min(1024, (d / (Y16 ? 8 : 4) + kWave - 1) / kWave * kWave);
+    if (out_dtype == 1)
+        combine_any<Y16>(K, dim3(T), dim3(threads), s, y, yexp, max_rows, d, pos, T,
+                         static_cast<_Float16 *>(out));
+    else if (out_dtype == 2)
+        combine_any<Y16>(K, dim3(T), dim3(threads), s, y, yexp, max_rows, d, pos, T,
+                         static_cast<__bf16 *>(out));
+    else
+        combine_any<Y16>(K, dim3(T), dim3(threads), s, y, yexp, max_rows, d, pos, T,
+                         static_cast<float *>(out));
     return hipGetLastError();
 }
 
-hipError_t launch_combine_y16(const uint16_t *y16, const int8_t *yexp, int64_t max_rows,
-                              const int32_t *pos, int T, int K, int d, float *out, hipStream_t s)
+hipError_t launch_combine(const float *y, int64_t max_rows, const int32_t *pos, int T, int K,
+                          int d, void *out, int out_dtype, hipStream_t s)
 {
-    const int threads = min(1024, (d / 8 + kWave - 1) / kWave * kWave);
-    combine_any<true>(K, dim3(T), dim3(threads), s, y16, yexp, max_rows, d, pos, T,
-                      reinterpret_cast<float4 *>(out));
-    return hipGetLastError();
+    return combine_as<false>(y, nullptr, max_rows, pos, T, K, d, out, out_dtype, s);
+}
+
+hipError_t launch_combine_y16(const uint16_t *y16, const int8_t *yexp, int64_t max_rows,
+                              const int32_t *pos, int T, int K, int d, void *out, int out_dtype,
+                              hipStream_t s)
+{
+    return combine_as<true>(y16, yexp, max_rows, pos, T, K, d, out, out_dtype, s);
 }
 
 }  // namespace moe

@@ -34,10 +34,11 @@ hipError_t launch_route_topk(const float *logits, int T, int E, int K, int32_t *
 hipError_t launch_gather(const void *x, int elem_bytes, int T, int d, const int32_t *stok,
                          const int32_t *meta, int64_t max_rows, void *xs, hipStream_t s);
 hipError_t launch_combine(const float *y, int64_t max_rows, const int32_t *pos, int T, int K,
-                          int d, float *out, hipStream_t s);
+                          int d, void *out, int out_dtype, hipStream_t s);
 // the combine over compact expert outputs (binary16 rows y16, block exponents yexp)
 hipError_t launch_combine_y16(const uint16_t *y16, const int8_t *yexp, int64_t max_rows,
-                              const int32_t *pos, int T, int K, int d, float *out, hipStream_t s);
+                              const int32_t *pos, int T, int K, int d, void *out, int out_dtype,
+                              hipStream_t s);
 
 // ---- grouped expert FFN ----
 // rows per work item of the grouped GEMMs
@@ -80,23 +81,29 @@ struct WavePlan {
 };
 bool wave_plan_fits(int64_t nent, int tm);
 
+// Layout of the expert weights that the grouped FFN reads: as given, in MFMA order
+// (moe_pack_weights), or in MFMA order as microscaled 4-bit codes (16-bit types)
+enum : int { kRowMajor = 0, kPacked = 1, kMx4 = 2 };
+// bytes of the codes, and of codes and scales, of a 32 x 64 tile of 4-bit weights
+constexpr uint32_t kMx4Codes = 1024, kMx4Tile = 1088;
+
 // runs_first: the items in runs of 4 first (item_slot), for the big cells
 hipError_t launch_worklist(const int32_t *eoff, int E, int64_t max_rows, void *scratch,
                            int64_t max_items, bool runs_first, hipStream_t s);
-hipError_t launch_gateup(const FfnShape &z, int dtype, bool packed, const void *xs,
+hipError_t launch_gateup(const FfnShape &z, int dtype, int wf, const void *xs,
                          const int32_t *stok, const void *wg, const void *wu, int d, int f,
                          const int32_t *meta, const void *scratch, void *h, hipStream_t s);
 // gate/up reading row r straight from x[stok[r]] (the gather fused into the
 // A-tile loads); x must be smaller than 2 GiB.
 // wp != nullptr with wp->ids set: the call is planned inside this launch (WavePlan).
-hipError_t launch_gateup_gathered(const FfnShape &z, int dtype, bool packed, const void *x, int T,
+hipError_t launch_gateup_gathered(const FfnShape &z, int dtype, int wf, const void *x, int T,
                                   const int32_t *stok, const void *wg, const void *wu, int d, int f,
                                   const int32_t *meta, const void *scratch, void *h, hipStream_t s,
                                   const WavePlan *wp = nullptr);
 // yexp == nullptr: y is fp32 [rows][d]; otherwise (16-bit types only) y holds
 // binary16 rows and yexp [rows][ceil(d / 128)] their block exponents (the
 // compact format of common.hpp)
-hipError_t launch_down(const FfnShape &z, int dtype, bool packed, const void *h, const void *wd,
+hipError_t launch_down(const FfnShape &z, int dtype, int wf, const void *h, const void *wd,
                        int d, int f, const int32_t *stok, const float *sw, const int32_t *meta,
                        const void *scratch, void *y, int8_t *yexp, hipStream_t s);
 
@@ -106,6 +113,13 @@ hipError_t launch_down(const FfnShape &z, int dtype, bool packed, const void *h,
 size_t packed_weight_bytes(int E, int Kd, int N, bool gateup, int dtype);
 hipError_t launch_pack(int dtype, const void *src, int E, int Kd, int N, bool gateup, void *dst,
                        hipStream_t s);
+
+// ---- expert weights in microscaled 4-bit floating point (mx4.hip) ----
+size_t mx4_weight_bytes(int E, int Kd, int N, bool gateup);
+hipError_t launch_mx4_quantize(int dtype, const void *src, int E, int Kd, int N, bool gateup,
+                               void *dst, hipStream_t s);
+hipError_t launch_mx4_dequantize(int dtype, const void *src, int E, int Kd, int N, bool gateup,
+                                 void *dst, hipStream_t s);
 
 // Expert weights in host memory (stage.hip): a device cache of S expert slots
 // per matrix (bytes_gu per slot for gate and up, bytes_dn for down) and its
@@ -178,5 +192,50 @@ hipError_t launch_act_backward(const uint8_t *g8, const uint8_t *gs, const uint8
                                const uint8_t *us, const void *dh, int64_t lddh, int dtype, int act,
                                int T, int f, void *dg, int64_t lddg, void *du, int64_t lddu,
                                void *h, int64_t ldh, hipStream_t s);
+
+// ---- routing by scores (score.hip) ----
+struct ScoreCall {
+    const float *logits, *bias;
+    int T, E, K, groups, keep, group_top;
+    bool sigmoid, renorm;
+    float scale;
+    int32_t *ids;
+    float *w;
+};
+struct ScoreBackwardCall {
+    const float *logits, *dw;
+    const int32_t *ids;
+    const void *add;
+    void *dlogits;
+    int T, E, K, dtype;
+    bool sigmoid, renorm;
+    float scale;
+};
+hipError_t launch_route_scored(const ScoreCall &c, hipStream_t s);
+hipError_t launch_route_scored_backward(const ScoreBackwardCall &c, hipStream_t s);
+
+// ---- norms around a block (norm.hip) ----
+// Null pointers are absent operands, or outputs that are not asked for.
+struct NormCall {
+    const void *r, *y, *w_post, *gate, *w_pre;
+    void *z, *h;
+    float *stats;
+    int64_t ldr, ldy, ldgate, ldz, ldh;
+    int dtype, T, d, gate_kind;
+    bool r32, y32;  // r and z, y: fp32 (else dtype)
+    float alpha, eps;
+};
+struct NormBackwardCall {
+    const void *dz, *dh, *z, *y, *w_post, *gate, *w_pre;
+    const float *stats;
+    void *dr, *dy, *dgate, *dw_post, *dw_pre;
+    int64_t lddz, lddh, ldz, ldy, ldgate, lddr, lddy, lddgate;
+    int dtype, T, d, gate_kind;
+    bool r32, y32, grad32;
+    float alpha;
+};
+hipError_t launch_norm(const NormCall &c, hipStream_t s);
+size_t norm_backward_workspace(int T, int d);
+hipError_t launch_norm_backward(const NormBackwardCall &c, void *ws, hipStream_t s);
 
 }  // namespace moe

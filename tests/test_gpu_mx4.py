@@ -1,0 +1,192 @@
+"""Expert weights in microscaled 4-bit floating point: quantisation, the way back, and
+the routed layer computed from them."""
+import numpy as np
+import pytest
+import torch
+
+import block_ref as ref
+import oracle
+from gpu_util import TOL, TORCH16, abi, custom, dev, host, make_case, rel_err, say, synth
+from test_gpu_packed import CASES as PACKED_CASES
+
+pytestmark = pytest.mark.gpu
+F32, F16, BF16 = torch.float32, torch.float16, torch.bfloat16
+SHAPES = [(1, 8, 8), (2, 40, 72), (3, 32, 256), (2, 96, 264), (1, 328, 520), (5, 64, 64),
+          (1, 200, 1032), (7, 8, 24)]
+
+
+def shaped(E, d, f, kind):
+    return (E, d, f) if kind == "gate" else (E, f, d)
+
+
+@pytest.mark.parametrize("dtype", [F32, F16, BF16], ids=str)
+@pytest.mark.parametrize("kind", ["gate", "down"])
+@pytest.mark.parametrize("E,d,f", SHAPES)
+def test_codes_scales_and_values(E, d, f, kind, dtype):
+    say(f"[mx4] {E} {d} {f} {kind} {dtype}")
+    g = torch.Generator(device="cuda").manual_seed(d + f)
+    w = torch.randn(shaped(E, d, f, kind), generator=g, device="cuda")
+    w = (w * torch.exp(2 * torch.randn(w.shape, generator=g, device="cuda"))).to(dtype)
+    w[0, 0, :4] = torch.tensor([0.0, -0.0, 6.0, -0.25])
+    packed = abi.mx4_quantize(w, kind, packed=torch.full(
+        (abi.moe_mx4_weight_bytes(E, d, f, abi.MX4_KINDS[kind]),), 0xA5, dtype=torch.uint8,
+        device="cuda"))
+    Kd, N = w.shape[1:]
+    codes, scales = ref.mx4_encode(ref.f64(w))
+    got, gs = ref.mx4_unpack(packed.cpu().numpy(), E, Kd, N, kind == "down")
+    assert np.array_equal(gs, scales)
+    assert np.array_equal(got, codes)
+    # what lies past d and f is zero
+    code, _, size = ref.mx4_places(Kd, N, kind == "down")
+    m = 2 if kind == "down" else 1
+    whole = ref.mx4_places(-(-Kd // 32) * 32, -(-N // (256 * m)) * 256 * m, kind == "down")
+    assert whole[2] == size
+    k = np.arange(whole[0].shape[0])[:, None]
+    nib = (packed.cpu().numpy().reshape(E, size)[:, whole[0]] >> (k % 2 * 4)) & 15
+    nib[:, :Kd, :N] = 0
+    assert not nib.any()
+    values = ref.mx4_values(codes, scales)
+    for D in (F32, F16, BF16):
+        back = abi.mx4_dequantize(packed, E, d, f, kind, dtype=D)
+        assert torch.equal(back.cpu(), torch.tensor(values).to(D))
+        assert torch.equal(torch.signbit(back.cpu()), torch.tensor((codes & 8) != 0))
+    # values of the format are kept
+    again = abi.mx4_quantize(abi.mx4_dequantize(packed, E, d, f, kind, dtype=F32), kind)
+    assert torch.equal(abi.mx4_dequantize(again, E, d, f, kind, dtype=F32),
+                       abi.mx4_dequantize(packed, E, d, f, kind, dtype=F32))
+
+
+@pytest.mark.parametrize("dtype", [F32, F16, BF16], ids=str)
+def test_extremes(dtype):
+    say(f"[mx4] extremes {dtype}")
+    big = float(torch.finfo(dtype).max)
+    w = torch.randn((1, 96, 64), device="cuda").to(dtype)
+    w[0, :32, 0] = 0
+    w[0, 3, 1] = float("inf")
+    w[0, 4, 2] = float("nan")
+    w[0, :32, 3] = big
+    w[0, :32, 4] = -big
+    w[0, :32, 5] = float(torch.finfo(dtype).tiny)
+    w[0, :32, 6] = float(torch.finfo(dtype).smallest_normal) / 4
+    w[0, 32:64, 7] *= 2.0 ** -14
+    w[0, 40, 8] = -float("inf")
+    packed = abi.mx4_quantize(w, "gate")
+    codes, scales = ref.mx4_encode(ref.f64(w))
+    got, gs = ref.mx4_unpack(packed.cpu().numpy(), 1, 96, 64, False)
+    assert np.array_equal(gs, scales) and (gs == 255).sum() == 3
+    fine = np.repeat(scales != 255, 32, axis=1)
+    assert np.array_equal(got[fine], codes[fine])
+    for D in (F32, F16, BF16):
+        back = abi.mx4_dequantize(packed, 1, 96, 64, "gate", dtype=D).cpu()
+        want = torch.tensor(ref.mx4_values(codes, scales)).to(D)
+        assert torch.equal(back.isnan(), want.isnan())
+        assert torch.equal(back[~want.isnan()], want[~want.isnan()])
+
+
+def test_every_scale_byte():
+    """blocks whose scale is any byte, all codes, read back in each type"""
+    say("[mx4] scales")
+    code, scale, size = ref.mx4_places(32, 256, False)
+    p = np.zeros((1, size), np.uint8)
+    codes = (np.arange(32)[:, None] + np.arange(256)[None, :]) % 16
+    np.bitwise_or.at(p[0], code, (codes << (np.arange(32)[:, None] % 2 * 4)).astype(np.uint8))
+    p[0, scale[0]] = np.arange(256)
+    packed = torch.tensor(p.reshape(-1)).cuda()
+    values = ref.mx4_values(codes[None], np.arange(256, dtype=np.uint8)[None, None])
+    for D in (F32, F16, BF16):
+        back = abi.mx4_dequantize(packed, 1, 32, 256, "gate", dtype=D).cpu()
+        want = torch.tensor(values).to(D)
+        assert torch.equal(back.isnan(), want.isnan())
+        assert torch.equal(back[~want.isnan()], want[~want.isnan()])
+
+
+# ------------------------------------------------------------------- layer --
+
+def four_bits(case):
+    """(packed 4-bit weights, their values as the case's type)"""
+    cfg = case.cfg
+    ws = {"gate": ("wg", "gate"), "up": ("wu", "gate"), "down": ("wd", "down")}
+    packed, values = {}, {}
+    for k, (name, kind) in ws.items():
+        packed[k] = abi.mx4_quantize(case.d(name), kind)
+        values[k] = abi.mx4_dequantize(packed[k], cfg.E, cfg.d, cfg.f, kind,
+                                       dtype=TORCH16[cfg.dtype])
+    return packed, values
+
+
+def four_calls(x, ids, w, values, cfg):
+    """plan, gather, grouped FFN and combine one by one, with packed weights"""
+    T, K = ids.shape
+    D = abi.DTYPE_NAME[cfg.dtype]
+    pk = abi.pack(values["gate"], values["up"], values["down"])
+    p = abi.plan(ids, w, cfg.E, cfg.tm)
+    n = p["sizes"].max_rows
+    xs = torch.zeros((n, cfg.d), dtype=x.dtype, device="cuda")
+    h = torch.zeros((n, cfg.f), dtype=x.dtype, device="cuda")
+    y = torch.zeros((n, cfg.d), dtype=F32, device="cuda")
+    out = torch.empty((T, cfg.d), dtype=F32, device="cuda")
+    abi.moe_gather(x, D, T, cfg.d, p["stok"], p["meta"], n, xs)
+    scratch = torch.empty(abi.moe_ffn_scratch_bytes(cfg.E, cfg.d, cfg.f, cfg.tm, n, D),
+                          dtype=torch.uint8, device="cuda")
+    abi.moe_expert_ffn_packed(xs, pk["gate"], pk["up"], pk["down"], D, cfg.E, cfg.d, cfg.f, cfg.tm,
+                              p["eoff"], p["stok"], p["sw"], p["meta"], n, h, y, scratch)
+    abi.moe_combine(y, n, p["pos"], T, K, cfg.d, out)
+    return out
+
+
+LAYERS = [c for c in PACKED_CASES if c.dtype != "f32"] + [
+    custom("one_token_bf16", T=1, d=264, E=8, K=2, f=136, dtype="bf16", x_std=1.0),
+    custom("one_token_f16", T=1, d=2816, E=16, K=8, f=704, dtype="f16", x_std=1.0),
+]
+
+
+@pytest.mark.parametrize("cfg", LAYERS, ids=lambda c: c.name)
+def test_layer_is_the_packed_layer_on_the_values(cfg):
+    say(f"[mx4] layer {cfg.name}")
+    case = make_case(cfg)
+    packed, values = four_bits(case)
+    x, ids, w = case.d("x"), case.d("ids"), case.d("w")
+    out, ws = abi.forward_mx4(x, ids, w, packed, cfg.E, cfg.f, tm=cfg.tm, out_dtype=F32)
+    if cfg.dtype == "bf16":
+        want, _ = abi.forward(x, ids, w, values["gate"], values["up"], values["down"], tm=cfg.tm,
+                              packed=abi.pack(values["gate"], values["up"], values["down"]))
+    else:
+        want = four_calls(x, ids, w, values, cfg)
+    assert torch.equal(out, want)
+    # the output's type: one rounding of the same sums; another workspace's contents
+    ws.fill_(0xC3)
+    half, _ = abi.forward_mx4(x, ids, w, packed, cfg.E, cfg.f, tm=cfg.tm, workspace=ws)
+    assert torch.equal(half, want.to(x.dtype))
+
+
+@pytest.mark.parametrize("name", ["decode_bf16", "small_f16", "skipped_bf16"])
+def test_layer_against_the_oracle(name):
+    say(f"[mx4] oracle {name}")
+    cfg = synth.CONFIGS["decode_bf16"] if name == "decode_bf16" else custom(
+        name, T=150, d=328, E=12, K=3, f=200, dtype=name.split("_")[1], x_std=1.0)
+    case = make_case(cfg)
+    ids = case.ids.copy()
+    if name == "skipped_bf16":
+        ids[::3, 1] = -1
+        ids[7] = -1       # a token without an expert
+        ids[8, 0] = 4000  # not an expert
+    packed, values = four_bits(case)
+    out, _ = abi.forward_mx4(case.d("x"), dev(ids), case.d("w"), packed, cfg.E, cfg.f, tm=cfg.tm,
+                             out_dtype=F32)
+    want = oracle.ffn(case.x, ids, case.w, host(values["gate"]), host(values["up"]),
+                      host(values["down"]), cfg.dtype, round_h=True)
+    assert rel_err(host(out), want) <= TOL[cfg.dtype]
+    if name == "skipped_bf16":
+        assert not out[7].any()
+
+
+def test_a_block_that_is_not_finite_reaches_its_column_only():
+    say("[mx4] nan")
+    cfg = custom("nan_bf16", T=20, d=64, E=2, K=2, f=40, dtype="bf16", x_std=1.0, w_std=0.2)
+    case = make_case(cfg)
+    wd = case.d("wd").clone()
+    wd[1, 3, 17] = float("nan")
+    packed = abi.pack_mx4(case.d("wg"), case.d("wu"), wd)
+    out, _ = abi.forward_mx4(case.d("x"), case.d("ids"), case.d("w"), packed, 2, 40, out_dtype=F32)
+    bad = out.isnan()
+    assert bad[:, 17].all() and bad.sum() == 20
