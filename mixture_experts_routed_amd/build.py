@@ -16,7 +16,8 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(HERE, "libmoe_routed.so")
-SOURCES = ["route.hip", "plan.hip", "gather_combine.hip", "ffn.hip", "stage.hip", "linear.hip",
+SOURCES = ["route.hip", "plan.hip", "gather_combine.hip", "ffn.hip", "ffn_mx4.hip",
+           "stage.hip", "linear.hip",
            "balance.hip", "act.hip", "mx4.hip", "score.hip", "norm.hip", "abi.cpp",
            "abi_dense.cpp", "abi_block.cpp", "noalloc.hip"]
 ARCH = "gfx950"
