@@ -693,9 +693,10 @@ int moe_act_backward(const uint8_t *g8, const uint8_t *gs, const uint8_t *u8, co
  * as for the dense operators.
  *
  * moe_route_scored -- routing by scores. Per token, over the experts that are
- * there (NaN and -inf logits, and NaN and -inf biases, mark an absent expert):
+ * there (NaN and -inf logits mark an absent expert):
  *   s_e = softmax of the logits, or 1 / (1 + exp(-l_e))
  *   c_e = s_e + bias_e                          (bias NULL: c_e = s_e)
+ * An expert whose bias is NaN or -inf is never picked and adds to no group.
  * The experts form `groups` groups of E / groups neighbours; a group is worth the
  * sum of its group_top largest c (of fewer if fewer are there), and the `keep`
  * groups of the largest worth stay (groups = keep = 1: no groups). Of their

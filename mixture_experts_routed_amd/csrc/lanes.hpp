@@ -1,4 +1,5 @@
-// Sums and maxima over groups of lanes of a wavefront, on register moves.
+// Rows of experts in groups of lanes of a wavefront: sums and maxima on register moves,
+// and how a group holds a row.
 #pragma once
 
 #include "common.hpp"
@@ -41,6 +42,38 @@ template <int G> __device__ __forceinline__ float group_sum(float v)
 template <int G> __device__ __forceinline__ float group_max(float v)
 {
     return group_reduce<G>(v, [](float a, float b) { return fmaxf(a, b); });
+}
+
+// the lanes of this lane's group in a wavefront ballot
+template <int G> __device__ __forceinline__ uint64_t group_bits(uint64_t b, int lane)
+{
+    return G == 64 ? b : (b >> (lane & ~(G - 1))) & ((1ull << (G & 63)) - 1);
+}
+
+// column of value j of lane `sub` of its group
+template <int G, int V> __device__ __forceinline__ int column(int sub, int j)
+{
+    return (sub + G * (j / V)) * V + j % V;
+}
+
+// v[j] = logit of column(j), -inf past E
+template <int G, int NJ, int V>
+__device__ __forceinline__ void load_row(const float *__restrict__ row, int E, int sub,
+                                         float (&v)[NJ])
+{
+#pragma unroll
+    for (int j = 0; j < NJ; j += V) {
+        const int e = column<G, V>(sub, j);
+        if constexpr (V == 4) {
+            const float4_t x = e < E ? *reinterpret_cast<const float4_t *>(row + e)
+                                     : float4_t{-__builtin_inff(), -__builtin_inff(),
+                                                -__builtin_inff(), -__builtin_inff()};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[j + i] = x[i];
+        } else {
+            v[j] = e < E ? row[e] : -__builtin_inff();
+        }
+    }
 }
 
 }  // namespace moe

@@ -2,15 +2,43 @@
 //   s_e = softmax or sigmoid of the logits,  c_e = s_e + bias_e
 //   groups of E / G experts: worth = sum of the group_top largest c; `keep` stay
 //   the K largest c of those, ties to the lower index; w = scale s (/ sum of s)
-// One wavefront per token, lane l holding experts l, l + 64, ...
+//
+// Choices are those of 64-bit arithmetic, and nearly all of them are made in 32: L
+// lanes hold a row of logits, each with 4 consecutive columns at a time where rows
+// are whole 16-byte chunks.
+//  * The K-th largest of the lanes' own maxima bounds the K-th largest c from below.
+//    What reaches the bound, less what 32 bits may be off, are the candidates: about
+//    K to 2 K of them, one a lane, through LDS.
+//  * A candidate's place is the number of candidates before it, so ordering them takes
+//    one compare each, not K rounds over the row.
+//  * Two candidates (or groups' worths) that lie within the errors of their 32-bit
+//    values are too near to call, unless logit and bias are the same. Such rows, and
+//    those with more candidates than lanes, are taken again in 64 bits, one row a
+//    wavefront, a round per pick (exact_row). Without a bias experts are compared by
+//    their logits, which are exact.
+// Bound by the traffic of the logits once arithmetic is out of the way: a sigmoid is
+// 2 transcendental instructions and 3 others.
+#include "lanes.hpp"
 #include "launch.hpp"
 #include "mfma.hpp"
+
+#include <type_traits>
 
 namespace moe {
 
 namespace {
 
-constexpr int kWaves = 4;  // tokens of a workgroup
+constexpr int kWaves = 4;  // wavefronts of a workgroup
+constexpr float kLog2e = 1.44269504088896341f;
+constexpr float kUlp = 5.9604644775390625e-8f;  // 2^-24
+__device__ __forceinline__ float neg_inf() { return -__builtin_inff(); }
+
+// LDS written by lanes of this wavefront is read by others of it
+__device__ __forceinline__ void wave_lds_order()
+{
+    __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+}
 
 __device__ __forceinline__ double wave_sum_f64(double v)
 {
@@ -18,36 +46,35 @@ __device__ __forceinline__ double wave_sum_f64(double v)
     for (int h = 32; h > 0; h >>= 1) v += __shfl_xor(v, h);
     return v;
 }
-__device__ __forceinline__ float wave_max_f32(float v)
+
+// A score up to a factor that all of a row's picks share, for their ratios: softmax
+// exp(l - top); sigmoid times exp(-min(top, 0)), so that scores too small for the type
+// still add up. top: the largest of the picks' logits.
+__device__ __forceinline__ float ratio_score(bool sigmoid, float l, float top)
 {
-#pragma unroll
-    for (int h = 32; h > 0; h >>= 1) v = __builtin_fmaxf(v, __shfl_xor(v, h));
-    return v;
-}
-__device__ __forceinline__ float wave_sum_f32(float v)
-{
-#pragma unroll
-    for (int h = 32; h > 0; h >>= 1) v += __shfl_xor(v, h);
-    return v;
+    if (sigmoid)
+        return l >= 0.f ? 1.f / (1.f + expf(-l))
+                        : expf(l - __builtin_fminf(top, 0.f)) / (1.f + expf(l));
+    // (+inf logits share everything)
+    return top == __builtin_inff() ? (l == top ? 1.f : 0.f) : expf(l - top);
 }
 
+// Row t in 64 bits, by the whole wavefront: lane l holds experts l, l + 64, ...;
+// lds: E doubles of this wavefront (with groups).
 template <int NJ>
-__global__ __launch_bounds__(kWaves * 64) void k_route_scored(const ScoreCall p)
+__device__ __noinline__ void exact_row(const ScoreCall &p, int64_t t, double *lds)
 {
-    extern __shared__ double s_c[];  // [kWaves][E], with groups
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int64_t t = (int64_t)blockIdx.x * kWaves + wave;
-    if (t >= p.T) return;
+    const int lane = threadIdx.x & 63;
     const float *row = p.logits + t * p.E;
     const double inf = __builtin_inf();
     double s[NJ], c[NJ];
-    float l[NJ], m = -__builtin_inff();
+    float l[NJ], m = neg_inf();
     uint32_t there = 0;
 #pragma unroll
     for (int j = 0; j < NJ; ++j) {
         const int e = lane + kWave * j;
-        l[j] = e < p.E ? row[e] : -__builtin_inff();
-        if (l[j] > -__builtin_inff()) {  // not NaN
+        l[j] = e < p.E ? row[e] : neg_inf();
+        if (l[j] > neg_inf()) {  // not NaN
             there |= 1u << j;
             m = __builtin_fmaxf(m, l[j]);
         }
@@ -56,11 +83,10 @@ __global__ __launch_bounds__(kWaves * 64) void k_route_scored(const ScoreCall p)
 #pragma unroll
         for (int j = 0; j < NJ; ++j) s[j] = (there >> j & 1) ? 1.0 / (1.0 + exp(-(double)l[j])) : 0.0;
     } else {
-        m = wave_max_f32(m);
+        m = group_max<64>(m);
         double sum = 0.0;
 #pragma unroll
         for (int j = 0; j < NJ; ++j) {
-            // (+inf logits share everything)
             s[j] = !(there >> j & 1) ? 0.0
                    : m == __builtin_inff() ? (l[j] == m ? 1.0 : 0.0) : exp((double)l[j] - (double)m);
             sum += s[j];
@@ -75,24 +101,23 @@ __global__ __launch_bounds__(kWaves * 64) void k_route_scored(const ScoreCall p)
         c[j] = s[j];
         if (p.bias && e < p.E) {
             const float b = p.bias[e];
-            if (!(b > -__builtin_inff())) there &= ~(1u << j);
+            if (!(b > neg_inf())) there &= ~(1u << j);
             c[j] += (double)b;
         }
     }
     if (p.groups > 1) {
-        double *mine = s_c + (int64_t)wave * p.E;
+        wave_lds_order();  // (what the fast path left there is read)
 #pragma unroll
         for (int j = 0; j < NJ; ++j) {
             const int e = lane + kWave * j;
-            if (e < p.E) mine[e] = (there >> j & 1) ? c[j] : -inf;
+            if (e < p.E) lds[e] = (there >> j & 1) ? c[j] : -inf;
         }
-        __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
-        __builtin_amdgcn_wave_barrier();
+        wave_lds_order();
         const int n = p.E / p.groups;
         double worth = -inf, next = -inf;
         if (lane < p.groups)
             for (int i = 0; i < n; ++i) {
-                const double v = mine[lane * n + i];
+                const double v = lds[lane * n + i];
                 if (v > worth) {
                     next = worth;
                     worth = v;
@@ -100,6 +125,7 @@ __global__ __launch_bounds__(kWaves * 64) void k_route_scored(const ScoreCall p)
                     next = v;
                 }
             }
+        wave_lds_order();
         if (p.group_top > 1 && next > -inf) worth += next;
         int before = 0;
         for (int g = 0; g < p.groups; ++g) {
@@ -113,13 +139,13 @@ __global__ __launch_bounds__(kWaves * 64) void k_route_scored(const ScoreCall p)
             if (e < p.E && !(kept >> (e / n) & 1)) there &= ~(1u << j);
         }
     }
-    double my_s = 0.0, total = 0.0;
-    float my_l = 0.f, top_l = 0.f;
-    int my_id = -1;
-    if (!p.bias) {  // by the logits, of which the score is a rising function
+    if (!p.bias) {  // by the logits
 #pragma unroll
         for (int j = 0; j < NJ; ++j) c[j] = (double)l[j];
     }
+    double my_s = 0.0;
+    float my_l = 0.f, top = 0.f;
+    int my_id = -1;
     for (int k = 0; k < p.K; ++k) {
         double best = -inf;
         int id = 0x7fffffff;
@@ -156,133 +182,411 @@ __global__ __launch_bounds__(kWaves * 64) void k_route_scored(const ScoreCall p)
             my_s = v;
             my_l = q;
         }
-        top_l = k == 0 ? q : __builtin_fmaxf(top_l, q);
+        top = k == 0 ? q : __builtin_fmaxf(top, q);
     }
-    if (p.renorm && my_id >= 0) {
-        // a common factor for scores that are all too small to add up
-        const double base = p.sigmoid ? (double)__builtin_fminf(top_l, 0.f) : (double)top_l;
-        if (p.sigmoid)
-            my_s = my_l >= 0.f ? my_s : exp((double)my_l - base) / (1.0 + exp((double)my_l));
-        else
-            my_s = top_l == __builtin_inff() ? (my_l == top_l ? 1.0 : 0.0)
-                                             : exp((double)my_l - base);
+    double total = 1.0;
+    if (p.renorm) {
+        my_s = my_id >= 0 ? (double)ratio_score(p.sigmoid, my_l, top) : 0.0;
+        total = wave_sum_f64(my_s);
     }
-    total = p.renorm ? wave_sum_f64(my_id >= 0 ? my_s : 0.0) : 1.0;
     if (lane < p.K) {
         p.ids[t * p.K + lane] = my_id;
         p.w[t * p.K + lane] = my_id >= 0 ? (float)((double)p.scale * (my_s / total)) : 0.f;
     }
 }
 
-template <typename T, int NJ>
-__global__ __launch_bounds__(kWaves * 64) void k_route_scored_backward(const ScoreBackwardCall p)
+struct Candidate {
+    float key, logit, bias;
+    int col;
+};
+
+// LDS of a wavefront: the scores of its rows (R rows of at most 16 L columns: 4 KB),
+// then its candidates (64); or a row in 64 bits
+constexpr int kLdsBytes = 8192;
+
+template <int L, int NJ, int V>
+__global__ __launch_bounds__(kWaves * 64) void k_route_scored(const ScoreCall p, uint32_t magic)
 {
-    extern __shared__ float s_row[];  // [kWaves][E]
+    constexpr int R = 64 / L;
+    static_assert(R * L * NJ * 4 <= 4096 && 4096 + 64 * sizeof(Candidate) <= kLdsBytes, "LDS");
+    __shared__ double s_all[kWaves][kLdsBytes / 8];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int64_t t = (int64_t)blockIdx.x * kWaves + wave;
-    if (t >= p.T) return;
-    float *mine = s_row + (int64_t)wave * p.E;
-    const float *row = p.logits + t * p.E;
+    const int r = lane / L, sub = lane & (L - 1);
+    double *lds = s_all[wave];
+    float *s_c = reinterpret_cast<float *>(lds) + r * (L * NJ);
+    Candidate *cand = reinterpret_cast<Candidate *>(lds + 512) + r * L;
+    const int64_t t0 = ((int64_t)blockIdx.x * kWaves + wave) * R;
+    if (t0 >= p.T) return;  // (the whole wavefront)
+    const bool have = t0 + r < p.T;
+    const int64_t t = have ? t0 + r : p.T - 1;
     const float inf = __builtin_inff();
-    for (int e = lane; e < p.E; e += 64) mine[e] = 0.f;
-    const int id = lane < p.K ? p.ids[t * p.K + lane] : -1;
-    bool ok = (unsigned)id < (unsigned)p.E;
-    const float l = ok ? row[id] : -inf;
-    ok = ok && l > -inf;
-    const float u = ok ? p.scale * p.dw[t * p.K + lane] : 0.f;
-    float g = 0.f, total = 0.f;
-    // softmax over all experts
-    float pr[NJ], m = -inf, sum = 0.f;
-    const bool dense = !p.sigmoid && !p.renorm;
-    if (dense) {
+
+    float l[NJ], b[NJ], key[NJ];
+    load_row<L, NJ, V>(p.logits + t * p.E, p.E, sub, l);
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) l[j] = __builtin_fmaxf(l[j], -inf);  // NaN: absent
+    if (p.bias) {
+        load_row<L, NJ, V>(p.bias, p.E, sub, b);
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) b[j] = __builtin_fmaxf(b[j], -inf);
+    }
+    // largest logit, and the softmax's denominator where it counts
+    float m = l[0], sum = 1.f, tol = 0.f;
+#pragma unroll
+    for (int j = 1; j < NJ; ++j) m = __builtin_fmaxf(m, l[j]);
+    m = group_max<L>(m);
+    const bool scored = p.bias || p.groups > 1;  // every expert's score is needed
+    if (!p.sigmoid && (scored || !p.renorm)) {
+        sum = 0.f;
 #pragma unroll
         for (int j = 0; j < NJ; ++j) {
-            const int e = lane + kWave * j;
-            pr[j] = e < p.E ? __builtin_fmaxf(row[e], -inf) : -inf;
-            m = __builtin_fmaxf(m, pr[j]);
+            const float x = m == inf    ? (l[j] == inf ? 1.f : 0.f)
+                            : m == -inf ? 0.f
+                                        : __builtin_amdgcn_exp2f((l[j] - m) * kLog2e);
+            key[j] = x;
+            sum += x;
         }
-        m = wave_max_f32(m);
+        sum = group_sum<L>(sum);
+    }
+    if (scored) {
+        // s in 32 bits. How far it may be off, with smax the row's largest score:
+        // sigmoid, the argument's rounding and four of an ulp or less, relative
+        // (1 - s) (1.5 |l| + 2) + 3 half-ulps, and s (1 - s) |l| <= 0.28 where l > -1.3;
+        // softmax, arguments 2.5 |l - m| (with p |l - m| <= 0.37 pmax, and ln E on
+        // average in the sum), 22 additions, and the rest below 6
+        if (p.sigmoid) {
+#pragma unroll
+            for (int j = 0; j < NJ; ++j)
+                key[j] = __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-l[j] * kLog2e));
+            const float smax = __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-m * kLog2e));
+            tol = kUlp * smax * (8.f + 1.5f * __builtin_fmaxf(0.f, -m)) + 0x1p-120f;
+        } else {
+            const float inv = sum > 0.f ? 1.f / sum : 0.f;
+#pragma unroll
+            for (int j = 0; j < NJ; ++j) key[j] *= inv;
+            tol = kUlp * inv * 48.f + 0x1p-120f;
+        }
+    }
+    bool unsure = false;
+    // c of every expert (-inf: absent)
+    auto there = [&](int j) { return l[j] > -inf && (!p.bias || b[j] > -inf); };
+    if (scored) {
 #pragma unroll
         for (int j = 0; j < NJ; ++j) {
-            pr[j] = m == -inf ? 0.f : m == inf ? (pr[j] == inf ? 1.f : 0.f) : expf(pr[j] - m);
-            sum += pr[j];
+            if (p.bias) key[j] += b[j];
+            key[j] = there(j) ? key[j] : -inf;
         }
-        sum = wave_sum_f32(sum);
+    }
+    if (p.groups > 1) {
+        float big = 0.f;
 #pragma unroll
-        for (int j = 0; j < NJ; ++j) pr[j] = sum > 0.f ? pr[j] / sum : 0.f;
+        for (int j = 0; j < NJ; ++j) {
+            const int e = column<L, V>(sub, j);
+            if (e < p.E) s_c[e] = key[j];
+            big = __builtin_fmaxf(big, key[j] == -inf ? 0.f : __builtin_fabsf(key[j]));
+        }
+        big = group_max<L>(big);
+        wave_lds_order();
+        // P lanes a group, each a share of its experts: the two largest
+        const int n = p.E / p.groups;
+        int P = L;
+        while (P > 1 && P * p.groups > L) P >>= 1;
+        // (more groups than lanes: each lane takes several, P = 1)
+        const int per = P * p.groups > L ? (p.groups + L - 1) / L : 1;
+        float worth[4];
+        const int g0 = P > 1 ? sub / P : sub;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            worth[q] = -inf;
+            const int g = g0 + q * L;
+            if (q >= per) continue;
+            float a = -inf, c2 = -inf;
+            if (g < p.groups)
+                for (int i = P > 1 ? sub & (P - 1) : 0; i < n; i += P) {
+                    const float v = s_c[g * n + i];
+                    c2 = __builtin_fmaxf(c2, __builtin_fminf(a, v));
+                    a = __builtin_fmaxf(a, v);
+                }
+            for (int h = 1; h < P; h <<= 1) {
+                const float oa = __shfl_xor(a, h), oc = __shfl_xor(c2, h);
+                c2 = __builtin_fmaxf(__builtin_fmaxf(c2, oc), __builtin_fminf(a, oa));
+                a = __builtin_fmaxf(a, oa);
+            }
+            worth[q] = p.group_top > 1 && c2 > -inf ? a + c2 : a;
+        }
+        // groups before each, and whether the border is too near to call
+        int before[4] = {0, 0, 0, 0};
+        for (int g = 0; g < p.groups; ++g) {
+            const int src = (lane & ~(L - 1)) + (P > 1 ? g * P : g & (L - 1));
+            const float mine = g < L ? worth[0] : g < 2 * L ? worth[1] : g < 3 * L ? worth[2] : worth[3];
+            const float o = __shfl(mine, src);
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                before[q] += o > worth[q] || (o == worth[q] && g < g0 + q * L);
+        }
+        float low = inf, high = -inf;  // the least kept, the best of the others
+        uint64_t kept = 0;             // bit g
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const bool in = q < per && g0 + q * L < p.groups;
+            const bool stay = in && before[q] < p.keep;
+            if (stay) low = __builtin_fminf(low, worth[q]);
+            if (in && !stay) high = __builtin_fmaxf(high, worth[q]);
+            const uint64_t bits = group_bits<L>(__ballot(stay), lane);
+            if (P == 1) {
+                kept |= bits << (q * L & 63);
+            } else if (q == 0) {
+                for (int g = 0; g < p.groups; ++g) kept |= (bits >> (g * P) & 1) << g;
+            }
+        }
+        low = -group_max<L>(-low);
+        high = group_max<L>(high);
+        // (an absent group that stays has nobody to pick)
+        unsure = high > -inf && !(low - high > 4.f * tol + 4.f * kUlp * big);
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) {
+            const int e = column<L, V>(sub, j);
+            const int g = n == 1 ? e : (int)__umulhi((uint32_t)e, magic);
+            const bool open = e < p.E && (kept >> (g & 63) & 1);
+            if (!p.bias) key[j] = there(j) ? l[j] : -inf;
+            key[j] = open ? key[j] : -inf;
+        }
+    } else if (!p.bias) {
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) key[j] = l[j];
+    }
+
+    // a bound of the K-th largest key: the K-th largest of the lanes' maxima
+    float best = key[0], bound = -inf;
+#pragma unroll
+    for (int j = 1; j < NJ; ++j) best = __builtin_fmaxf(best, key[j]);
+    for (int k = 0; k < p.K; ++k) {
+        bound = group_max<L>(best);
+        best = best == bound ? -inf : best;
+    }
+    // two keys of biased scores are apart if they differ by more than this and kUlp
+    // times 4 their size; the candidates reach so far below the bound
+    const float far = 2.f * tol;
+    const float from = p.bias ? bound - (far + 4.f * kUlp * __builtin_fabsf(bound)) : bound;
+    int count = 0;
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) count += key[j] > -inf && !(key[j] < from);
+    const int upto = wave_inclusive_scan(count, lane);
+    const int prior = __shfl(upto, r == 0 ? 0 : r * L - 1);
+    const int start = r == 0 ? 0 : prior;
+    const int n = __shfl(upto, r * L + L - 1) - start;  // of this row
+    unsure |= n > L;
+    wave_lds_order();
+    if (n <= L) {
+        int at = upto - count - start;
+#pragma unroll
+        for (int j = 0; j < NJ; ++j)
+            if (key[j] > -inf && !(key[j] < from)) {
+                cand[at] = Candidate{key[j], l[j], p.bias ? b[j] : 0.f, column<L, V>(sub, j)};
+                ++at;
+            }
+    }
+    wave_lds_order();
+    const bool mine_ok = n <= L && sub < n;
+    Candidate me = {0.f, 0.f, 0.f, 0};
+    if (mine_ok) me = cand[sub];
+    const float apart = far + 4.f * kUlp * __builtin_fabsf(me.key);
+    int place = 0;
+    bool near = false;
+    const int most = wave_max(n <= L ? n : 0);
+    for (int i = 0; i < most; ++i) {
+        if (i < n && mine_ok) {
+            const Candidate o = cand[i];
+            place += o.key > me.key || (o.key == me.key && o.col < me.col);
+            near |= i != sub && !(__builtin_fabsf(o.key - me.key) > apart) &&
+                    !(o.logit == me.logit && o.bias == me.bias);
+        }
+    }
+    const bool pick = mine_ok && place < p.K;
+    unsure |= p.bias && group_bits<L>(__ballot(pick && near), lane) != 0;
+
+    const float top = group_max<L>(pick ? me.logit : -inf);
+    float s = 0.f;
+    if (pick) {
+        if (p.renorm)
+            s = ratio_score(p.sigmoid, me.logit, top);
+        else if (p.sigmoid)
+            s = 1.f / (1.f + expf(-me.logit));
+        else
+            s = ratio_score(false, me.logit, m) / sum;
     }
     if (p.renorm) {
-        const float top = wave_max_f32(ok ? l : -inf);
-        const float base = p.sigmoid ? __builtin_fminf(top, 0.f) : top;
-        float s = 0.f;
-        if (ok) {
-            if (p.sigmoid)
-                s = l >= 0.f ? 1.f / (1.f + expf(-l)) : expf(l - base) / (1.f + expf(l));
-            else
-                s = top == inf ? (l == inf ? 1.f : 0.f) : expf(l - base);
-        }
-        const float S = wave_sum_f32(s);
-        s = S > 0.f ? s / S : 0.f;
-        g = s * (u - wave_sum_f32(s * u));
-        if (p.sigmoid && ok) g *= 1.f / (1.f + expf(l));
-    } else if (p.sigmoid) {
-        if (ok) g = u * (1.f / (1.f + expf(-l))) * (1.f / (1.f + expf(l)));
-    } else {
-        if (ok) g = u * (m == inf ? (l == inf ? 1.f : 0.f) : expf(l - m)) / sum;
-        total = wave_sum_f32(g);
+        const float total = group_sum<L>(s);
+        s = pick ? s / total : 0.f;
     }
-    __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-    if (ok) atomicAdd(mine + id, g);  // (one instruction: lanes of one address in order)
-    __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-#pragma unroll
-    for (int j = 0; j < NJ; ++j) {
-        const int e = lane + kWave * j;
-        if (e >= p.E) continue;
-        float v = mine[e];
-        if (dense) v -= pr[j] * total;
-        if (p.add) v += to_f32(static_cast<const T *>(p.add)[t * p.E + e]);
-        static_cast<T *>(p.dlogits)[t * p.E + e] = from_f32<T>(v);
+    if (have && !unsure) {
+        if (pick) {
+            p.ids[t * p.K + place] = me.col;
+            p.w[t * p.K + place] = p.scale * s;
+        } else if (sub >= n && sub < p.K) {  // (fewer experts than picks: n < K)
+            p.ids[t * p.K + sub] = -1;
+            p.w[t * p.K + sub] = 0.f;
+        }
+    }
+    uint64_t again = __ballot(unsure && have && sub == 0);
+    while (again) {
+        const int first = __ffsll((unsigned long long)again) - 1;
+        again &= again - 1;
+        exact_row<L * NJ / 64>(p, t0 + first / L, lds);
     }
 }
 
-template <typename T, int NJ> hipError_t backward_t(const ScoreBackwardCall &c, hipStream_t s)
+template <int L, int NJ> hipError_t scored_t(const ScoreCall &c, hipStream_t s)
 {
-    hipLaunchKernelGGL((k_route_scored_backward<T, NJ>), dim3((c.T + kWaves - 1) / kWaves),
-                       dim3(kWaves * 64), kWaves * (size_t)c.E * 4, s, c);
+    const int rows = kWaves * (64 / L);
+    const dim3 grid((unsigned)((c.T + (int64_t)rows - 1) / rows)), block(kWaves * 64);
+    const int n = c.E / c.groups;
+    const uint32_t magic = n > 1 ? (uint32_t)((((uint64_t)1 << 32) + n - 1) / n) : 0;
+    if (c.E % 4 == 0 && reinterpret_cast<uintptr_t>(c.logits) % 16 == 0 &&
+        reinterpret_cast<uintptr_t>(c.bias) % 16 == 0)
+        hipLaunchKernelGGL((k_route_scored<L, NJ, 4>), grid, block, 0, s, c, magic);
+    else
+        hipLaunchKernelGGL((k_route_scored<L, NJ, 1>), grid, block, 0, s, c, magic);
     return hipGetLastError();
 }
-template <int NJ> hipError_t backward_any(const ScoreBackwardCall &c, hipStream_t s)
+
+// ---- gradient ------------------------------------------------------------------
+// L lanes hold a row of dlogits; the picks' terms are added through a row of LDS (one
+// instruction a round of L picks, lanes of one address in order). Bound by the traffic
+// of dlogits and `add`; the logits are read at the picks alone but for softmax weights
+// that are not renormalised.
+
+template <typename T, int L, int NJ, int V>
+__global__ __launch_bounds__(kWaves * 64) void k_route_scored_backward(const ScoreBackwardCall p)
 {
-    return c.dtype == 0   ? backward_t<float, NJ>(c, s)
-           : c.dtype == 1 ? backward_t<_Float16, NJ>(c, s)
-                          : backward_t<__bf16, NJ>(c, s);
+    constexpr int R = 64 / L;
+    __shared__ float s_all[kWaves][R * L * NJ];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int r = lane / L, sub = lane & (L - 1);
+    float *mine = s_all[wave] + r * (L * NJ);
+    const int64_t t0 = ((int64_t)blockIdx.x * kWaves + wave) * R;
+    if (t0 >= p.T) return;  // (the whole wavefront)
+    const bool have = t0 + r < p.T;
+    const int64_t t = have ? t0 + r : p.T - 1;
+    const float *row = p.logits + t * p.E;
+    const float inf = __builtin_inff();
+    const int id = sub < p.K ? p.ids[t * p.K + sub] : -1;  // (K <= L)
+    bool ok = (unsigned)id < (unsigned)p.E;
+    const float l = ok ? row[id] : -inf;
+    ok = ok && l > -inf;
+    const float u = ok ? p.scale * p.dw[t * p.K + sub] : 0.f;
+    float add[NJ];
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) add[j] = 0.f;
+    if (p.add) {
+        const T *q = static_cast<const T *>(p.add) + t * p.E;
+#pragma unroll
+        for (int j = 0; j < NJ; j += V) {
+            const int e = column<L, V>(sub, j);
+            if (e >= p.E) continue;
+            float x[V];
+            Vec<T, V>::load(q + e, x);
+#pragma unroll
+            for (int i = 0; i < V; ++i) add[j + i] = x[i];
+        }
+    }
+    float pr[NJ], m = -inf, sum = 0.f, g = 0.f, total = 0.f;
+    const bool dense = !p.sigmoid && !p.renorm;
+    if (dense) {
+        load_row<L, NJ, V>(row, p.E, sub, pr);
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) {
+            pr[j] = __builtin_fmaxf(pr[j], -inf);
+            m = __builtin_fmaxf(m, pr[j]);
+        }
+        m = group_max<L>(m);
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) {
+            pr[j] = m == inf    ? (pr[j] == inf ? 1.f : 0.f)
+                    : m == -inf ? 0.f
+                                : __builtin_amdgcn_exp2f((pr[j] - m) * kLog2e);
+            sum += pr[j];
+        }
+        sum = group_sum<L>(sum);
+        if (ok) g = u * ratio_score(false, l, m) / sum;
+        total = group_sum<L>(g) / (sum > 0.f ? sum : 1.f);
+    } else if (p.renorm) {
+        const float top = group_max<L>(ok ? l : -inf);
+        float s = ok ? ratio_score(p.sigmoid, l, top) : 0.f;
+        const float S = group_sum<L>(s);
+        s = S > 0.f ? s / S : 0.f;
+        g = s * (u - group_sum<L>(s * u));
+        if (p.sigmoid && ok) g *= 1.f / (1.f + expf(l));
+    } else if (ok) {
+        g = u * (1.f / (1.f + expf(-l))) * (1.f / (1.f + expf(l)));
+    }
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) mine[column<L, V>(sub, j)] = 0.f;
+    wave_lds_order();
+    if (ok) atomicAdd(mine + id, g);
+    wave_lds_order();
+    if (!have) return;
+    T *out = static_cast<T *>(p.dlogits) + t * p.E;
+#pragma unroll
+    for (int j = 0; j < NJ; j += V) {
+        const int e = column<L, V>(sub, j);
+        if (e >= p.E) continue;
+        float x[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            x[i] = mine[e + i] + add[j + i];
+            if (dense) x[i] -= pr[j + i] * total;
+        }
+        Vec<T, V>::store(out + e, x);
+    }
+}
+
+template <typename T, int L, int NJ> hipError_t backward_t(const ScoreBackwardCall &c, hipStream_t s)
+{
+    const int rows = kWaves * (64 / L);
+    const dim3 grid((unsigned)((c.T + (int64_t)rows - 1) / rows)), block(kWaves * 64);
+    if (c.E % 4 == 0 && reinterpret_cast<uintptr_t>(c.logits) % 16 == 0 &&
+        reinterpret_cast<uintptr_t>(c.add) % 16 == 0 &&
+        reinterpret_cast<uintptr_t>(c.dlogits) % 16 == 0)
+        hipLaunchKernelGGL((k_route_scored_backward<T, L, NJ, 4>), grid, block, 0, s, c);
+    else
+        hipLaunchKernelGGL((k_route_scored_backward<T, L, NJ, 1>), grid, block, 0, s, c);
+    return hipGetLastError();
+}
+
+// lanes of a row and columns of a lane, for E experts and K picks: the fewest lanes
+// that hold a row with 16 columns each, and a pick each
+template <typename F> hipError_t with_lanes(int E, int K, F run)
+{
+    using std::integral_constant;
+    if (K <= 16 && E <= 256)
+        return E <= 64    ? run(integral_constant<int, 16>(), integral_constant<int, 4>())
+               : E <= 128 ? run(integral_constant<int, 16>(), integral_constant<int, 8>())
+                          : run(integral_constant<int, 16>(), integral_constant<int, 16>());
+    if (K <= 32 && E <= 512)
+        return E <= 256 ? run(integral_constant<int, 32>(), integral_constant<int, 8>())
+                        : run(integral_constant<int, 32>(), integral_constant<int, 16>());
+    return E <= 256 ? run(integral_constant<int, 64>(), integral_constant<int, 4>())
+                    : run(integral_constant<int, 64>(), integral_constant<int, 16>());
 }
 
 }  // namespace
 
 hipError_t launch_route_scored(const ScoreCall &c, hipStream_t s)
 {
-    const dim3 grid((c.T + kWaves - 1) / kWaves), block(kWaves * 64);
-    const size_t lds = c.groups > 1 ? kWaves * (size_t)c.E * 8 : 0;
-    if (c.E <= 2 * kWave)
-        hipLaunchKernelGGL(k_route_scored<2>, grid, block, lds, s, c);
-    else if (c.E <= 4 * kWave)
-        hipLaunchKernelGGL(k_route_scored<4>, grid, block, lds, s, c);
-    else if (c.E <= 8 * kWave)
-        hipLaunchKernelGGL(k_route_scored<8>, grid, block, lds, s, c);
-    else
-        hipLaunchKernelGGL(k_route_scored<16>, grid, block, lds, s, c);
-    return hipGetLastError();
+    return with_lanes(c.E, c.K, [&](auto lanes, auto columns) {
+        return scored_t<decltype(lanes)::value, decltype(columns)::value>(c, s);
+    });
 }
 
 hipError_t launch_route_scored_backward(const ScoreBackwardCall &c, hipStream_t s)
 {
-    return c.E <= 2 * kWave   ? backward_any<2>(c, s)
-           : c.E <= 4 * kWave ? backward_any<4>(c, s)
-           : c.E <= 8 * kWave ? backward_any<8>(c, s)
-                              : backward_any<16>(c, s);
+    return with_lanes(c.E, c.K, [&](auto lanes, auto columns) {
+        constexpr int L = decltype(lanes)::value, NJ = decltype(columns)::value;
+        return c.dtype == 0   ? backward_t<float, L, NJ>(c, s)
+               : c.dtype == 1 ? backward_t<_Float16, L, NJ>(c, s)
+                              : backward_t<__bf16, L, NJ>(c, s);
+    });
 }
 
 }  // namespace moe
