@@ -11,11 +11,13 @@
 //    K to 2 K of them, one a lane, through LDS.
 //  * A candidate's place is the number of candidates before it, so ordering them takes
 //    one compare each, not K rounds over the row.
-//  * Two candidates (or groups' worths) that lie within the errors of their 32-bit
-//    values are too near to call, unless logit and bias are the same. Such rows, and
-//    those with more candidates than lanes, are taken again in 64 bits, one row a
-//    wavefront, a round per pick (exact_row). Without a bias experts are compared by
-//    their logits, which are exact.
+//  * What lies within the errors of its 32-bit values is too near to call: groups are
+//    chosen again from 64-bit scores, a sigmoid's candidates placed again by theirs,
+//    one a lane (2 rows of 1,000 at 512 experts). Rows where a softmax's biased scores
+//    lie so near, and those with more candidates than lanes (many equal logits), are
+//    taken again as a whole in 64 bits, one row a wavefront, a round per pick
+//    (exact_row). Without a bias experts are compared by their logits, which are
+//    exact.
 // Bound by the traffic of the logits once arithmetic is out of the way: a sigmoid is
 // 2 transcendental instructions and 3 others.
 #include "lanes.hpp"
@@ -106,7 +108,6 @@ __device__ __noinline__ void exact_row(const ScoreCall &p, int64_t t, double *ld
         }
     }
     if (p.groups > 1) {
-        wave_lds_order();  // (what the fast path left there is read)
 #pragma unroll
         for (int j = 0; j < NJ; ++j) {
             const int e = lane + kWave * j;
@@ -196,19 +197,119 @@ __device__ __noinline__ void exact_row(const ScoreCall &p, int64_t t, double *ld
 }
 
 struct Candidate {
-    float key, logit, bias;
+    float key;
     int col;
 };
 
-// LDS of a wavefront: the scores of its rows (R rows of at most 16 L columns: 4 KB),
-// then its candidates (64); or a row in 64 bits
+// LDS of a wavefront: the scores of its rows (R rows of at most 16 L columns: 4 KB in
+// 32 bits, 8 in 64), later its candidates (64) and their scores in 64 bits behind 4 KB
 constexpr int kLdsBytes = 8192;
+
+// an image of a float (not NaN) that orders as it does among whole numbers, and back
+__device__ __forceinline__ int order_of(float v)
+{
+    const int b = __float_as_int(v);
+    return b ^ ((b >> 31) & 0x7fffffff);
+}
+__device__ __forceinline__ float value_of(int k)
+{
+    return __int_as_float(k ^ ((k >> 31) & 0x7fffffff));
+}
+template <int L> __device__ __forceinline__ int lanes_max(int v)
+{
+    constexpr int lo = -2147483647 - 1;  // (the identity: moves fold into the maxima)
+    v = max(v, dpp_move<kQuadXor1>(v, lo));
+    v = max(v, dpp_move<kQuadXor2>(v, lo));
+    v = max(v, dpp_move<kRowHalfMirror>(v, lo));
+    v = max(v, dpp_move<kRowMirror>(v, lo));
+    if constexpr (L >= 32) {
+        const float2 h = both_halves<16>(__int_as_float(v));
+        v = max(__float_as_int(h.x), __float_as_int(h.y));
+    }
+    if constexpr (L >= 64) {
+        const float2 h = both_halves<32>(__int_as_float(v));
+        v = max(__float_as_int(h.x), __float_as_int(h.y));
+    }
+    return v;
+}
+
+// The groups that stay, of the c in LDS (s: this row's E values; groups <= L, one
+// wavefront's lanes): bit g P of the result for group g, with P lanes a group. near (in
+// 32 bits): whether the least worth that stays and the best that does not are too near
+// to call when each c is off by tol and a rounding of itself.
+template <int L, typename F>
+__device__ __forceinline__ uint64_t choose_groups(const ScoreCall &p, const F *s, int P, float tol,
+                                                  bool *near)
+{
+    const int lane = threadIdx.x & 63, sub = lane & (L - 1);
+    const int n = p.E / p.groups, g0 = sub / P;
+    const F inf = (F)__builtin_inf();
+    F worth = -inf, next = -inf;
+    if (g0 < p.groups) {
+        const F *q = s + g0 * n;
+#pragma unroll 4
+        for (int i = sub & (P - 1); i < n; i += P) {  // the two largest
+            const F v = q[i];
+            const F less = v > worth ? worth : v;
+            next = less > next ? less : next;
+            worth = v > worth ? v : worth;
+        }
+    }
+    for (int h = 1; h < P; h <<= 1) {
+        const F oa = __shfl_xor(worth, h), oc = __shfl_xor(next, h);
+        const F less = oa > worth ? worth : oa;
+        next = oc > next ? oc : next;
+        next = less > next ? less : next;
+        worth = oa > worth ? oa : worth;
+    }
+    const F size = worth > -inf ? __builtin_fabs(worth) + (next > -inf ? __builtin_fabs(next) : 0) : 0;
+    if (p.group_top > 1 && next > -inf) worth += next;
+    int before = 0;
+    for (int g = 0; g < p.groups; ++g) {
+        const F o = __shfl(worth, (lane & ~(L - 1)) + g * P);
+        before += o > worth || (o == worth && g < g0);
+    }
+    const bool in = g0 < p.groups, stay = in && before < p.keep;
+    if constexpr (sizeof(F) == 4) {
+        const float low = -group_max<L>(stay ? -worth : -inf);
+        const float high = group_max<L>(in && !stay ? worth : -inf);
+        // (high -inf: no group is left out, or absent ones)
+        *near = high > -inf && !(low - high > 4.f * tol + 4.f * kUlp * group_max<L>(size));
+    }
+    return group_bits<L>(__ballot(stay), lane);
+}
+
+// c of a row in 64 bits into s, by the row's L lanes
+template <int L>
+__device__ __forceinline__ void exact_scores(const ScoreCall &p, const float *row, float m,
+                                             double *s)
+{
+    const int sub = threadIdx.x & (L - 1);
+    double sum = 1.;
+    auto softmax = [&](float l) {
+        return !(l > neg_inf())         ? 0.
+               : m == __builtin_inff() ? (l == m ? 1. : 0.)
+                                       : exp((double)l - (double)m);
+    };
+    if (!p.sigmoid) {
+        sum = 0.;
+        for (int e = sub; e < p.E; e += L) sum += softmax(row[e]);
+#pragma unroll
+        for (int h = 1; h < L; h <<= 1) sum += __shfl_xor(sum, h);
+    }
+    for (int e = sub; e < p.E; e += L) {
+        const float l = row[e], b = p.bias ? p.bias[e] : 0.f;
+        const double c = p.sigmoid ? 1. / (1. + exp(-(double)l)) : softmax(l) / sum;
+        s[e] = l > neg_inf() && b > neg_inf() ? c + (double)b : -__builtin_inf();
+    }
+}
 
 template <int L, int NJ, int V>
 __global__ __launch_bounds__(kWaves * 64) void k_route_scored(const ScoreCall p, uint32_t magic)
 {
     constexpr int R = 64 / L;
-    static_assert(R * L * NJ * 4 <= 4096 && 4096 + 64 * sizeof(Candidate) <= kLdsBytes, "LDS");
+    static_assert(R * L * NJ * 8 <= kLdsBytes && 4096 + 64 * (sizeof(Candidate) + 8) <= kLdsBytes,
+                  "LDS");
     __shared__ double s_all[kWaves][kLdsBytes / 8];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int r = lane / L, sub = lane & (L - 1);
@@ -268,88 +369,48 @@ __global__ __launch_bounds__(kWaves * 64) void k_route_scored(const ScoreCall p,
         }
     }
     bool unsure = false;
-    // c of every expert (-inf: absent)
-    auto there = [&](int j) { return l[j] > -inf && (!p.bias || b[j] > -inf); };
-    if (scored) {
+    if (scored) {  // c of every expert; -inf: absent
 #pragma unroll
         for (int j = 0; j < NJ; ++j) {
             if (p.bias) key[j] += b[j];
-            key[j] = there(j) ? key[j] : -inf;
+            key[j] = l[j] > -inf ? key[j] : -inf;
         }
     }
-    if (p.groups > 1) {
-        float big = 0.f;
+    if (p.groups > 1) {  // (at most L)
 #pragma unroll
-        for (int j = 0; j < NJ; ++j) {
+        for (int j = 0; j < NJ; j += V) {
             const int e = column<L, V>(sub, j);
-            if (e < p.E) s_c[e] = key[j];
-            big = __builtin_fmaxf(big, key[j] == -inf ? 0.f : __builtin_fabsf(key[j]));
+#pragma unroll
+            for (int i = 0; i < V; ++i) s_c[e + i] = key[j + i];
         }
-        big = group_max<L>(big);
         wave_lds_order();
-        // P lanes a group, each a share of its experts: the two largest
         const int n = p.E / p.groups;
-        int P = L;
-        while (P > 1 && P * p.groups > L) P >>= 1;
-        // (more groups than lanes: each lane takes several, P = 1)
-        const int per = P * p.groups > L ? (p.groups + L - 1) / L : 1;
-        float worth[4];
-        const int g0 = P > 1 ? sub / P : sub;
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            worth[q] = -inf;
-            const int g = g0 + q * L;
-            if (q >= per) continue;
-            float a = -inf, c2 = -inf;
-            if (g < p.groups)
-                for (int i = P > 1 ? sub & (P - 1) : 0; i < n; i += P) {
-                    const float v = s_c[g * n + i];
-                    c2 = __builtin_fmaxf(c2, __builtin_fminf(a, v));
-                    a = __builtin_fmaxf(a, v);
-                }
-            for (int h = 1; h < P; h <<= 1) {
-                const float oa = __shfl_xor(a, h), oc = __shfl_xor(c2, h);
-                c2 = __builtin_fmaxf(__builtin_fmaxf(c2, oc), __builtin_fminf(a, oa));
-                a = __builtin_fmaxf(a, oa);
-            }
-            worth[q] = p.group_top > 1 && c2 > -inf ? a + c2 : a;
+        int P = L;  // lanes of a group
+        while (P * p.groups > L) P >>= 1;
+        bool near = false;
+        uint64_t kept = choose_groups<L>(p, s_c, P, tol, &near);
+        if (__ballot(near)) {
+            double *c = lds + r * (L * NJ);
+            wave_lds_order();
+            exact_scores<L>(p, p.logits + t * p.E, m, c);
+            wave_lds_order();
+            kept = choose_groups<L>(p, c, P, 0.f, &near);
+            wave_lds_order();
         }
-        // groups before each, and whether the border is too near to call
-        int before[4] = {0, 0, 0, 0};
-        for (int g = 0; g < p.groups; ++g) {
-            const int src = (lane & ~(L - 1)) + (P > 1 ? g * P : g & (L - 1));
-            const float mine = g < L ? worth[0] : g < 2 * L ? worth[1] : g < 3 * L ? worth[2] : worth[3];
-            const float o = __shfl(mine, src);
+        if (!p.bias) {  // by the logits
 #pragma unroll
-            for (int q = 0; q < 4; ++q)
-                before[q] += o > worth[q] || (o == worth[q] && g < g0 + q * L);
+            for (int j = 0; j < NJ; ++j) key[j] = l[j];
         }
-        float low = inf, high = -inf;  // the least kept, the best of the others
-        uint64_t kept = 0;             // bit g
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            const bool in = q < per && g0 + q * L < p.groups;
-            const bool stay = in && before[q] < p.keep;
-            if (stay) low = __builtin_fminf(low, worth[q]);
-            if (in && !stay) high = __builtin_fmaxf(high, worth[q]);
-            const uint64_t bits = group_bits<L>(__ballot(stay), lane);
-            if (P == 1) {
-                kept |= bits << (q * L & 63);
-            } else if (q == 0) {
-                for (int g = 0; g < p.groups; ++g) kept |= (bits >> (g * P) & 1) << g;
-            }
-        }
-        low = -group_max<L>(-low);
-        high = group_max<L>(high);
-        // (an absent group that stays has nobody to pick)
-        unsure = high > -inf && !(low - high > 4.f * tol + 4.f * kUlp * big);
+        const bool quads = V == 4 && n % 4 == 0;  // 4 columns lie in one group
+        bool open = false;
 #pragma unroll
         for (int j = 0; j < NJ; ++j) {
-            const int e = column<L, V>(sub, j);
-            const int g = n == 1 ? e : (int)__umulhi((uint32_t)e, magic);
-            const bool open = e < p.E && (kept >> (g & 63) & 1);
-            if (!p.bias) key[j] = there(j) ? l[j] : -inf;
-            key[j] = open ? key[j] : -inf;
+            if (j % V == 0 || !quads) {
+                const int e = column<L, V>(sub, j);
+                const int g = n == 1 ? e : (int)__umulhi((uint32_t)e, magic);
+                open = kept >> (g * P & 63) & 1;
+            }
+            key[j] = open ? key[j] : -inf;  // (columns past E have -inf)
         }
     } else if (!p.bias) {
 #pragma unroll
@@ -357,63 +418,89 @@ __global__ __launch_bounds__(kWaves * 64) void k_route_scored(const ScoreCall p,
     }
 
     // a bound of the K-th largest key: the K-th largest of the lanes' maxima
-    float best = key[0], bound = -inf;
+    float best = key[0];
 #pragma unroll
     for (int j = 1; j < NJ; ++j) best = __builtin_fmaxf(best, key[j]);
+    const int none = order_of(-inf);
+    int mine_best = order_of(best), bound_k = none;
     for (int k = 0; k < p.K; ++k) {
-        bound = group_max<L>(best);
-        best = best == bound ? -inf : best;
+        bound_k = lanes_max<L>(mine_best);
+        mine_best = mine_best == bound_k ? none : mine_best;
     }
+    const float bound = value_of(bound_k);
     // two keys of biased scores are apart if they differ by more than this and kUlp
     // times 4 their size; the candidates reach so far below the bound
     const float far = 2.f * tol;
     const float from = p.bias ? bound - (far + 4.f * kUlp * __builtin_fabsf(bound)) : bound;
+    const float least = __builtin_fmaxf(from, -__FLT_MAX__);  // (not -inf: absent)
     int count = 0;
 #pragma unroll
-    for (int j = 0; j < NJ; ++j) count += key[j] > -inf && !(key[j] < from);
+    for (int j = 0; j < NJ; ++j) count += key[j] >= least;
     const int upto = wave_inclusive_scan(count, lane);
     const int prior = __shfl(upto, r == 0 ? 0 : r * L - 1);
     const int start = r == 0 ? 0 : prior;
     const int n = __shfl(upto, r * L + L - 1) - start;  // of this row
-    unsure |= n > L;
+    unsure |= n > L || __builtin_isnan(from);
     wave_lds_order();
     if (n <= L) {
-        int at = upto - count - start;
+        Candidate *at = cand + (upto - count - start);
 #pragma unroll
         for (int j = 0; j < NJ; ++j)
-            if (key[j] > -inf && !(key[j] < from)) {
-                cand[at] = Candidate{key[j], l[j], p.bias ? b[j] : 0.f, column<L, V>(sub, j)};
-                ++at;
-            }
+            if (key[j] >= least) *at++ = Candidate{key[j], column<L, V>(sub, j)};
     }
     wave_lds_order();
     const bool mine_ok = n <= L && sub < n;
-    Candidate me = {0.f, 0.f, 0.f, 0};
+    Candidate me = {0.f, 0};
     if (mine_ok) me = cand[sub];
+    const float *row = p.logits + t * p.E;
+    const float my_l = mine_ok ? row[me.col] : -inf;
     const float apart = far + 4.f * kUlp * __builtin_fabsf(me.key);
-    int place = 0;
-    bool near = false;
+    int place = 0, close = 0;  // (close counts the candidate itself)
     const int most = wave_max(n <= L ? n : 0);
     for (int i = 0; i < most; ++i) {
-        if (i < n && mine_ok) {
-            const Candidate o = cand[i];
-            place += o.key > me.key || (o.key == me.key && o.col < me.col);
-            near |= i != sub && !(__builtin_fabsf(o.key - me.key) > apart) &&
-                    !(o.logit == me.logit && o.bias == me.bias);
+        const Candidate o = cand[i < L ? i : 0];
+        const bool in = i < n;
+        place += in && (o.key > me.key || (o.key == me.key && o.col < me.col));
+        close += in && !(__builtin_fabsf(o.key - me.key) > apart);
+    }
+    bool pick = mine_ok && place < p.K;
+    if (p.bias && __ballot(pick && close > 1)) {
+        // too near to call in 32 bits
+        if (p.sigmoid) {  // a candidate's c in 64 bits needs its logit and bias alone
+            double *exact = lds + 512 + 64 + r * L;
+            double c = 0.;
+            if (mine_ok) {
+                c = 1. / (1. + exp(-(double)my_l)) + (double)p.bias[me.col];
+                exact[sub] = c;
+            }
+            wave_lds_order();
+            place = 0;
+            for (int i = 0; i < n && n <= L; ++i)
+                place += exact[i] > c || (exact[i] == c && cand[i].col < me.col);
+            pick = mine_ok && place < p.K;
+        } else {  // the whole row, but for experts of the same logit and bias
+            bool near = false;
+            if (pick && close > 1) {
+                const float my_b = p.bias[me.col];
+                for (int i = 0; i < n; ++i) {
+                    const Candidate o = cand[i];
+                    if (i != sub && !(__builtin_fabsf(o.key - me.key) > apart))
+                        near |= !(row[o.col] == my_l && p.bias[o.col] == my_b);
+                }
+            }
+            unsure |= group_bits<L>(__ballot(near), lane) != 0;
         }
     }
-    const bool pick = mine_ok && place < p.K;
-    unsure |= p.bias && group_bits<L>(__ballot(pick && near), lane) != 0;
 
-    const float top = group_max<L>(pick ? me.logit : -inf);
+    const float top = group_max<L>(pick ? my_l : -inf);
     float s = 0.f;
     if (pick) {
         if (p.renorm)
-            s = ratio_score(p.sigmoid, me.logit, top);
+            s = ratio_score(p.sigmoid, my_l, top);
         else if (p.sigmoid)
-            s = 1.f / (1.f + expf(-me.logit));
+            s = 1.f / (1.f + expf(-my_l));
         else
-            s = ratio_score(false, me.logit, m) / sum;
+            s = ratio_score(false, my_l, m) / sum;
     }
     if (p.renorm) {
         const float total = group_sum<L>(s);
@@ -432,7 +519,8 @@ __global__ __launch_bounds__(kWaves * 64) void k_route_scored(const ScoreCall p,
     while (again) {
         const int first = __ffsll((unsigned long long)again) - 1;
         again &= again - 1;
-        exact_row<L * NJ / 64>(p, t0 + first / L, lds);
+        const ScoreCall cold = p;  // (by address: p itself stays in scalar registers)
+        exact_row<L * NJ / 64>(cold, t0 + first / L, lds);
     }
 }
 
@@ -554,8 +642,8 @@ template <typename T, int L, int NJ> hipError_t backward_t(const ScoreBackwardCa
     return hipGetLastError();
 }
 
-// lanes of a row and columns of a lane, for E experts and K picks: the fewest lanes
-// that hold a row with 16 columns each, and a pick each
+// lanes of a row and columns of a lane, for E experts: the fewest lanes that hold a row
+// with 16 columns each, and one of K things each (picks, groups)
 template <typename F> hipError_t with_lanes(int E, int K, F run)
 {
     using std::integral_constant;
@@ -574,7 +662,7 @@ template <typename F> hipError_t with_lanes(int E, int K, F run)
 
 hipError_t launch_route_scored(const ScoreCall &c, hipStream_t s)
 {
-    return with_lanes(c.E, c.K, [&](auto lanes, auto columns) {
+    return with_lanes(c.E, c.K > c.groups ? c.K : c.groups, [&](auto lanes, auto columns) {
         return scored_t<decltype(lanes)::value, decltype(columns)::value>(c, s);
     });
 }
