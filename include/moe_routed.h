@@ -367,10 +367,11 @@ int moe_forward_packed(const void *x, const int32_t *ids, const float *w, const 
  *
  * moe_forward_mx4 -- moe_forward_packed with such weights (pw_gate, pw_up:
  * MOE_W_GATE_UP; pw_down: MOE_W_DOWN) and 16-bit activations: a weight is its
- * value in dtype, products are summed in fp32 and h is kept in dtype, so that the
- * result is moe_forward_packed's on the dequantised weights -- bit for bit with
- * MOE_BF16 and out_dtype MOE_F32; with MOE_F16 the expert outputs are kept in fp32
- * rows (as in the four calls), not in the compact format.
+ * value in dtype, products are summed in fp32 and h is kept in dtype: the layer on
+ * the dequantised weights, though sums may be cut along the reduction elsewhere than
+ * moe_forward_packed cuts them. With MOE_BF16 the expert outputs are kept in the
+ * compact format of moe_forward, with MOE_F16 in fp32 (that format's rounding is as
+ * large as fp16's own).
  * In:  x, ids, w as moe_forward; dtype MOE_F16 or MOE_BF16.
  * Out: out [T][d] of out_dtype (dtype or MOE_F32; one rounding of the fp32 sum).
  * workspace: moe_forward_workspace() bytes.

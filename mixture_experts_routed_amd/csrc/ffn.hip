@@ -689,6 +689,25 @@ namespace {
 
 unsigned reduce_blocks(int64_t rows, int N) { return (unsigned)((rows * (N / 4) + 255) / 256); }
 
+// Narrow cells take a launch of 4-bit weights with fewer wide cells than this and, on
+// average, fewer rows an item than that (both by the plan's bounds): they read an item's
+// weights again for each 16 rows. Layers in a graph, us, narrow against wide cells (2,816
+// x 704, 128 experts, top-8, bf16): 1 token 19 / 25, 4 tokens 29 / 33, 8 tokens 38 / 51;
+// down cells of 16 to 64 tokens (966 to 1,002 by the bound) 66 to 106 / 64 to 99; gate/up
+// cells of 8 to 64 tokens over 512 experts (303 to 1,929) are 4 to 9 us faster narrow.
+constexpr int64_t kNarrowBelowGateUp = 2048, kNarrowBelowDown = 512, kNarrowBelowRows = 24;
+
+// workgroups of a launch of narrow cells, or 0: wide cells
+int64_t narrow_blocks(const FfnShape &z, int wf, int N, bool gateup)
+{
+    const int64_t gs = (N + group_cols(gateup) - 1) / group_cols(gateup);
+    if (wf != kMx4 || z.max_items * gs >= (gateup ? kNarrowBelowGateUp : kNarrowBelowDown) ||
+        z.max_rows >= kNarrowBelowRows * z.max_items)
+        return 0;
+    const int slice = group_cols(gateup) / kWavesPerBlock;
+    return (z.max_items * ((N + slice - 1) / slice) + 7) / 8 * 8;
+}
+
 // gate/up in the weight layout wf (fp32 has no 4-bit form: the caller refuses it)
 template <typename T>
 hipError_t gateup_any(const FfnShape &z, int dtype, int wf, const void *a, int a_rows,
@@ -717,12 +736,15 @@ hipError_t gateup_any(const FfnShape &z, int dtype, int wf, const void *a, int a
                                    ctl_of(scratch), items_of(scratch));
         }
     }
+    const int64_t narrow = narrow_blocks(z, wf, f, true);
+    if (narrow) p.nsplit = 1;
     hipError_t e =
-        wf == kMx4      ? gateup_cells_mx4(dtype, p, z.blocks_gu, gathered, scratch, wp, s)
+        wf == kMx4      ? gateup_cells_mx4(dtype, p, narrow ? narrow : z.blocks_gu, narrow != 0,
+                                           gathered, scratch, wp, s)
         : wf == kPacked ? gateup_cells<T, kPacked>(p, z.blocks_gu, gathered, scratch, wp, s)
                         : gateup_cells<T, kRowMajor>(p, z.blocks_gu, gathered, scratch, wp, s);
     if (e != hipSuccess) return e;
-    if (z.split_gu > 1) {
+    if (p.nsplit > 1) {
         e = reduce_gateup<T>(p.nsplit, dim3(reduce_blocks(z.max_rows, f)), s, p.part, p.plane, f,
                              stok, meta, z.max_rows, static_cast<T *>(h));
         if (e != hipSuccess) return e;
@@ -754,11 +776,14 @@ hipError_t down_any(const FfnShape &z, int dtype, int wf, const void *h, const v
                                dim3(kBigThreads), 0, s, p, ctl_of(scratch), items_of(scratch));
         }
     }
-    hipError_t e = wf == kMx4      ? down_cells_mx4(dtype, p, z.blocks_dn, scratch, s)
+    const int64_t narrow = narrow_blocks(z, wf, d, false);
+    if (narrow) p.nsplit = 1;
+    hipError_t e = wf == kMx4      ? down_cells_mx4(dtype, p, narrow ? narrow : z.blocks_dn,
+                                                    narrow != 0, scratch, s)
                    : wf == kPacked ? down_cells<T, kPacked>(p, z.blocks_dn, scratch, s)
                                    : down_cells<T, kRowMajor>(p, z.blocks_dn, scratch, s);
     if (e != hipSuccess) return e;
-    if (z.split_dn > 1) {
+    if (p.nsplit > 1) {
         e = p.yexp ? reduce_down_y16(p.nsplit,
                                      dim3((unsigned)((z.max_rows * nyb * 32 + 255) / 256)), s,
                                      p.part, p.plane, d, stok, sw, meta, z.max_rows,

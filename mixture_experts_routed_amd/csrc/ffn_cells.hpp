@@ -1206,10 +1206,11 @@ hipError_t down_cells(const GemmArgs &p, int64_t blocks, const void *scratch, hi
     return hipGetLastError();
 }
 
-// the cells of 4-bit weights (ffn_mx4.hip; dtype: the C ABI's code, not fp32)
-hipError_t gateup_cells_mx4(int dtype, const GemmArgs &p, int64_t blocks, bool gathered,
-                            const void *scratch, const WavePlan *wp, hipStream_t s);
-hipError_t down_cells_mx4(int dtype, const GemmArgs &p, int64_t blocks, const void *scratch,
-                          hipStream_t s);
+// the cells of 4-bit weights (ffn_mx4.hip; dtype: the C ABI's code, not fp32); narrow: one
+// column slice a workgroup, unsplit
+hipError_t gateup_cells_mx4(int dtype, const GemmArgs &p, int64_t blocks, bool narrow,
+                            bool gathered, const void *scratch, const WavePlan *wp, hipStream_t s);
+hipError_t down_cells_mx4(int dtype, const GemmArgs &p, int64_t blocks, bool narrow,
+                          const void *scratch, hipStream_t s);
 
 }  // namespace moe

@@ -7,7 +7,7 @@ import torch
 import block_ref as ref
 import oracle
 from gpu_util import TOL, TORCH16, abi, custom, dev, host, make_case, rel_err, say, synth
-from test_gpu_packed import CASES as PACKED_CASES
+from test_gpu_packed import BIG, CASES as PACKED_CASES
 
 pytestmark = pytest.mark.gpu
 F32, F16, BF16 = torch.float32, torch.float16, torch.bfloat16
@@ -140,23 +140,84 @@ LAYERS = [c for c in PACKED_CASES if c.dtype != "f32"] + [
 ]
 
 
+def reference(case, ids, values):
+    """(out [T, d], how far it may be off) in 64 bits. Products are summed in fp32 (at most
+    d or f terms one after another), silu has 16 roundings' worth, h is rounded once to the
+    type, y to fp32 and, for bf16, to binary16 with an exponent per block."""
+    cfg = case.cfg
+    U, half = ref.U32, ref.HALF[TORCH16[cfg.dtype]]
+    x = ref.f64(case.d("x"))
+    wg, wu, wd = (ref.f64(values[k]) for k in ("gate", "up", "down"))
+    out, tol = np.zeros((cfg.T, cfg.d)), np.zeros((cfg.T, cfg.d))
+    for e in range(cfg.E):
+        t, k = np.nonzero(ids == e)
+        if not len(t):
+            continue
+        g, u = x[t] @ wg[e], x[t] @ wu[e]
+        eg, eu = ((np.abs(x[t]) @ np.abs(m[e])) * cfg.d * U for m in (wg, wu))
+        sig = 1 / (1 + np.exp(-g))
+        h = g * sig * u
+        eh = np.abs(h) * (half + 16 * U) + (1.1 * eg * np.abs(u) + np.abs(g * sig) * eu) + 2.0 ** -25
+        w = case.w[t, k][:, None].astype(np.float64)
+        y = h @ wd[e]
+        ey = eh @ np.abs(wd[e]) + (np.abs(h) @ np.abs(wd[e])) * cfg.f * U
+        ey += (2.0 ** -11 if cfg.dtype == "bf16" else U) * (np.abs(y) + ey) + U * np.abs(y)
+        np.add.at(out, t, w * y)
+        np.add.at(tol, t, w * (ey + (cfg.K + 2) * U * np.abs(y)))
+    return out, tol + 2.0 ** -40 * np.abs(out).max()
+
+
 @pytest.mark.parametrize("cfg", LAYERS, ids=lambda c: c.name)
-def test_layer_is_the_packed_layer_on_the_values(cfg):
+def test_layer(cfg):
     say(f"[mx4] layer {cfg.name}")
     case = make_case(cfg)
     packed, values = four_bits(case)
     x, ids, w = case.d("x"), case.d("ids"), case.d("w")
     out, ws = abi.forward_mx4(x, ids, w, packed, cfg.E, cfg.f, tm=cfg.tm, out_dtype=F32)
+    want, tol = reference(case, case.ids, values)
+    off = np.abs(ref.f64(out) - want)
+    assert (off <= tol).all(), np.max(off / tol)
+    # the output's type: one rounding of the same sums; another workspace's contents
+    ws.fill_(0xC3)
+    half, _ = abi.forward_mx4(x, ids, w, packed, cfg.E, cfg.f, tm=cfg.tm, workspace=ws)
+    assert torch.equal(half, out.to(x.dtype))
+
+
+@pytest.mark.parametrize("cfg", [c for c in BIG if c.dtype != "f32"], ids=lambda c: c.name)
+def test_layer_of_many_rows_is_the_packed_layer_on_the_values(cfg):
+    say(f"[mx4] layer bits {cfg.name}")
+    case = make_case(cfg)
+    packed, values = four_bits(case)
+    x, ids, w = case.d("x"), case.d("ids"), case.d("w")
+    out, _ = abi.forward_mx4(x, ids, w, packed, cfg.E, cfg.f, tm=cfg.tm, out_dtype=F32)
     if cfg.dtype == "bf16":
         want, _ = abi.forward(x, ids, w, values["gate"], values["up"], values["down"], tm=cfg.tm,
                               packed=abi.pack(values["gate"], values["up"], values["down"]))
     else:
         want = four_calls(x, ids, w, values, cfg)
     assert torch.equal(out, want)
-    # the output's type: one rounding of the same sums; another workspace's contents
-    ws.fill_(0xC3)
-    half, _ = abi.forward_mx4(x, ids, w, packed, cfg.E, cfg.f, tm=cfg.tm, workspace=ws)
-    assert torch.equal(half, want.to(x.dtype))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("T,tm", [(1, 16), (3, 16), (8, 16), (16, 16), (17, 16), (33, 1), (64, 16)])
+def test_small_batches(T, tm, dtype):
+    """calls planned inside the first launch and calls that are not, with rows beyond 16 of
+    one expert (every token goes to expert 3, some twice)"""
+    say(f"[mx4] small {T} {tm} {dtype}")
+    cfg = custom(f"small_{T}", T=T, d=328, E=40, K=3, f=200, dtype=dtype, tm=tm, x_std=1.0)
+    case = make_case(cfg)
+    case.ids[:, 1] = 3
+    case.ids[::2, 2] = 3
+    if T > 2:
+        case.ids[2] = -1
+        case.ids[1, 0] = cfg.E
+    case.drop_device()
+    packed, values = four_bits(case)
+    out, _ = abi.forward_mx4(case.d("x"), case.d("ids"), case.d("w"), packed, cfg.E, cfg.f, tm=tm,
+                             out_dtype=F32)
+    want, tol = reference(case, case.ids, values)
+    off = np.abs(ref.f64(out) - want)
+    assert (off <= tol).all(), np.max(off / tol)
 
 
 @pytest.mark.parametrize("name", ["decode_bf16", "small_f16", "skipped_bf16"])
