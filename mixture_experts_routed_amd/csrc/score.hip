@@ -250,8 +250,12 @@ __device__ __forceinline__ uint64_t choose_groups(const ScoreCall &p, const F *s
 #pragma unroll 4
         for (int i = sub & (P - 1); i < n; i += P) {  // the two largest
             const F v = q[i];
-            const F less = v > worth ? worth : v;
-            next = less > next ? less : next;
+            if constexpr (sizeof(F) == 4) {  // (the median of the three is the second largest)
+                next = __builtin_amdgcn_fmed3f(worth, next, v);
+            } else {
+                const F less = v > worth ? worth : v;
+                next = less > next ? less : next;
+            }
             worth = v > worth ? v : worth;
         }
     }
@@ -322,15 +326,12 @@ __global__ __launch_bounds__(kWaves * 64) void k_route_scored(const ScoreCall p,
     const int64_t t = have ? t0 + r : p.T - 1;
     const float inf = __builtin_inff();
 
+    // (a NaN logit fails l > -inf, a NaN bias b > -inf: absent, like -inf)
     float l[NJ], b[NJ], key[NJ];
     load_row<L, NJ, V>(p.logits + t * p.E, p.E, sub, l);
 #pragma unroll
-    for (int j = 0; j < NJ; ++j) l[j] = __builtin_fmaxf(l[j], -inf);  // NaN: absent
-    if (p.bias) {
-        load_row<L, NJ, V>(p.bias, p.E, sub, b);
-#pragma unroll
-        for (int j = 0; j < NJ; ++j) b[j] = __builtin_fmaxf(b[j], -inf);
-    }
+    for (int j = 0; j < NJ; ++j) b[j] = 0.f;
+    if (p.bias) load_row<L, NJ, V>(p.bias, p.E, sub, b);
     // largest logit, and the softmax's denominator where it counts
     float m = l[0], sum = 1.f, tol = 0.f;
 #pragma unroll
@@ -341,9 +342,9 @@ __global__ __launch_bounds__(kWaves * 64) void k_route_scored(const ScoreCall p,
         sum = 0.f;
 #pragma unroll
         for (int j = 0; j < NJ; ++j) {
-            const float x = m == inf    ? (l[j] == inf ? 1.f : 0.f)
-                            : m == -inf ? 0.f
-                                        : __builtin_amdgcn_exp2f((l[j] - m) * kLog2e);
+            const float x = m == inf       ? (l[j] == inf ? 1.f : 0.f)
+                            : l[j] > -inf ? __builtin_amdgcn_exp2f((l[j] - m) * kLog2e)
+                                          : 0.f;
             key[j] = x;
             sum += x;
         }
@@ -371,10 +372,7 @@ __global__ __launch_bounds__(kWaves * 64) void k_route_scored(const ScoreCall p,
     bool unsure = false;
     if (scored) {  // c of every expert; -inf: absent
 #pragma unroll
-        for (int j = 0; j < NJ; ++j) {
-            if (p.bias) key[j] += b[j];
-            key[j] = l[j] > -inf ? key[j] : -inf;
-        }
+        for (int j = 0; j < NJ; ++j) key[j] = l[j] > -inf && b[j] > -inf ? key[j] + b[j] : -inf;
     }
     if (p.groups > 1) {  // (at most L)
 #pragma unroll
@@ -397,7 +395,7 @@ __global__ __launch_bounds__(kWaves * 64) void k_route_scored(const ScoreCall p,
             kept = choose_groups<L>(p, c, P, 0.f, &near);
             wave_lds_order();
         }
-        if (!p.bias) {  // by the logits
+        if (!p.bias) {  // by the logits (NaN is never a candidate)
 #pragma unroll
             for (int j = 0; j < NJ; ++j) key[j] = l[j];
         }
@@ -408,7 +406,7 @@ __global__ __launch_bounds__(kWaves * 64) void k_route_scored(const ScoreCall p,
             if (j % V == 0 || !quads) {
                 const int e = column<L, V>(sub, j);
                 const int g = n == 1 ? e : (int)__umulhi((uint32_t)e, magic);
-                open = kept >> (g * P & 63) & 1;
+                open = L <= 32 ? (uint32_t)kept >> (g * P & 31) & 1 : kept >> (g * P & 63) & 1;
             }
             key[j] = open ? key[j] : -inf;  // (columns past E have -inf)
         }
