@@ -10,12 +10,18 @@
 // the even code. A block with a value that is not finite gets the byte 255 and
 // reads back as NaN.
 //
-// Layout: packed_geom in ffn.hip, tiles of 32 x 64 weights, [64 lanes][4 columns]
+// Layout: packed_geom in ffn_cells.hpp, tiles of 32 x 64 weights, [64 lanes][4 columns]
 // [8 K-values] of 4 bits and then 64 scale bytes: what one wavefront of the grouped
 // FFN multiplies in one step. A wavefront here makes one tile: lane (nq, kg) reads
 // rows 8 kg .. + 7 of columns 4 nq .. + 3 (a row's 16 lanes cover 64 columns),
 // which are the lane's own 32 codes, and the block's maximum is 8 rows in
-// registers and two lane exchanges. Bound by HBM.
+// registers and two lane exchanges.
+//
+// Both ways are bound by HBM. Measured at 128 experts of 2816 x 704, bf16 (642 MB either
+// way): quantising 117 us (5.5 TB/s), back 95.5 us (6.7 TB/s); a copy of 2 GiB moves 4.9
+// TB/s. Weights are read and written past the caches (a line is used once, by one
+// wavefront): quantising 145 -> 117 us, back 100 -> 95.5. The codes are not (they stay
+// for whoever reads them next): quantising would gain 9 us, reading back lose 15.
 #include "launch.hpp"
 #include "mfma.hpp"
 
@@ -27,20 +33,30 @@ constexpr int kMinExp = -110, kMaxExp = 120;
 
 struct Mx4Tiles {
     int Kd, N, gs, nst, nm;
-    int64_t total;  // tiles of all experts
 };
 
-// the tile's expert, its first row and its first column
-__device__ __forceinline__ void place(const Mx4Tiles &z, int64_t t, int64_t *e, int *k0, int *n0)
+// A workgroup has the four wavefronts' tiles of one K-step and column slice of an expert
+// (blockIdx.y). All of it is the same for a wavefront, so one scalar division finds it:
+// with a running tile number, divided in 64 bits per lane, quantising took 178 us, not 162.
+struct Mx4Place {
+    int k0, n0;   // the tile's first row and column
+    int64_t src;  // the expert's first weight
+    int64_t dst;  // the tile
+};
+
+__device__ __forceinline__ Mx4Place place(const Mx4Tiles &z)
 {
-    const int m = (int)(t % z.nm);
-    t /= z.nm;
-    const int w = (int)(t & 3);
-    t >>= 2;
-    *k0 = (int)(t % z.nst) * 32;
-    t /= z.nst;
-    *n0 = ((int)(t % z.gs) * 4 + w) * 64 * z.nm + 64 * m;
-    *e = t / z.gs;
+    const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const unsigned x = blockIdx.x;
+    const int m = z.nm == 2 ? x & 1 : 0;
+    const unsigned u = z.nm == 2 ? x >> 1 : x;
+    const unsigned slice = u / (unsigned)z.nst, step = u - slice * z.nst;
+    Mx4Place at;
+    at.k0 = (int)step * 32;
+    at.n0 = ((int)slice * 4 + w) * 64 * z.nm + 64 * m;
+    at.src = (int64_t)blockIdx.y * z.Kd * z.N;
+    at.dst = ((int64_t)blockIdx.y * z.gs * z.nst + u) * (4 * z.nm) + w * z.nm + m;
+    return at;
 }
 
 template <typename T>
@@ -48,48 +64,48 @@ __global__ __launch_bounds__(256) void k_mx4_quantize(const T *__restrict__ src,
                                                       unsigned char *__restrict__ dst)
 {
     const int lane = threadIdx.x & 63, nq = lane & 15, kg = lane >> 4;
-    for (int64_t t = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); t < z.total;
-         t += (int64_t)gridDim.x * 4) {
-        int64_t e;
-        int k0, n0;
-        place(z, t, &e, &k0, &n0);
-        const int n = n0 + 4 * nq, k = k0 + 8 * kg;
-        // (N is a multiple of 8: a lane's 4 columns are all inside or all outside)
-        float v[8][4];
+    const Mx4Place at = place(z);
+    const int n = at.n0 + 4 * nq, k = at.k0 + 8 * kg;
+    // (N is a multiple of 8: a lane's 4 columns are all inside or all outside.) Rows and
+    // columns past the matrix read its last row or first columns and count as 0, so that
+    // all eight loads are in flight at once.
+    typename Vec<T, 4>::type raw[8];
+    const T *from = src + at.src + (n < z.N ? n : 0);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < 8; ++i)
+        raw[i] = __builtin_nontemporal_load(reinterpret_cast<const typename Vec<T, 4>::type *>(
+            from + (int64_t)min(k + i, z.Kd - 1) * z.N));
+    float v[8][4];
 #pragma unroll
-            for (int c = 0; c < 4; ++c) v[i][c] = 0.f;
-            if (k + i < z.Kd && n < z.N)
-                Vec<T, 4>::load(src + ((e * z.Kd + k + i) * (int64_t)z.N + n), v[i]);
-        }
-        uint32_t word[4], scales = 0;
+    for (int i = 0; i < 8; ++i)
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-            int m = 0;  // magnitudes order as their bits, what is not finite last
+        for (int c = 0; c < 4; ++c) v[i][c] = k + i < z.Kd && n < z.N ? to_f32(raw[i][c]) : 0.f;
+    uint32_t word[4], scales = 0;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) m = max(m, __float_as_int(v[i][c]) & 0x7fffffff);
-            m = max(m, __shfl_xor(m, 16));
-            m = max(m, __shfl_xor(m, 32));
-            const bool odd = m >= 0x7f800000;
-            const float M = __int_as_float(m);
-            const int x = __builtin_amdgcn_frexp_expf(M);
-            int ex = __builtin_amdgcn_frexp_mantf(M) <= 0.75f ? x - 3 : x - 2;
-            ex = m == 0 || odd ? kMinExp : min(max(ex, kMinExp), kMaxExp);
-            const float inv = pow2f(-ex);
-            uint32_t o = 0;
-            o = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(o, v[0][c] * inv, v[1][c] * inv, 1.f, 0);
-            o = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(o, v[2][c] * inv, v[3][c] * inv, 1.f, 1);
-            o = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(o, v[4][c] * inv, v[5][c] * inv, 1.f, 2);
-            o = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(o, v[6][c] * inv, v[7][c] * inv, 1.f, 3);
-            word[c] = o;
-            scales |= (odd ? 255u : (uint32_t)(ex + 127)) << (8 * c);
-        }
-        unsigned char *tile = dst + t * kMx4Tile;
-        *reinterpret_cast<uint4 *>(tile + 16 * lane) =
-            make_uint4(word[0], word[1], word[2], word[3]);
-        if (kg == 0) *reinterpret_cast<uint32_t *>(tile + kMx4Codes + 4 * nq) = scales;
+    for (int c = 0; c < 4; ++c) {
+        int m = 0;  // magnitudes order as their bits, what is not finite last
+#pragma unroll
+        for (int i = 0; i < 8; ++i) m = max(m, __float_as_int(v[i][c]) & 0x7fffffff);
+        m = max(m, __shfl_xor(m, 16));
+        m = max(m, __shfl_xor(m, 32));
+        const bool odd = m >= 0x7f800000;
+        const float M = __int_as_float(m);
+        const int x = __builtin_amdgcn_frexp_expf(M);
+        int ex = __builtin_amdgcn_frexp_mantf(M) <= 0.75f ? x - 3 : x - 2;
+        ex = m == 0 || odd ? kMinExp : min(max(ex, kMinExp), kMaxExp);
+        const float inv = pow2f(-ex);
+        uint32_t o = 0;
+        o = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(o, v[0][c] * inv, v[1][c] * inv, 1.f, 0);
+        o = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(o, v[2][c] * inv, v[3][c] * inv, 1.f, 1);
+        o = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(o, v[4][c] * inv, v[5][c] * inv, 1.f, 2);
+        o = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(o, v[6][c] * inv, v[7][c] * inv, 1.f, 3);
+        word[c] = o;
+        scales |= (odd ? 255u : (uint32_t)(ex + 127)) << (8 * c);
     }
+    unsigned char *tile = dst + at.dst * kMx4Tile;
+    *reinterpret_cast<uint4 *>(tile + 16 * lane) =
+        make_uint4(word[0], word[1], word[2], word[3]);
+    if (kg == 0) *reinterpret_cast<uint32_t *>(tile + kMx4Codes + 4 * nq) = scales;
 }
 
 // codes 2 j and 2 j + 1 of a word times their scale
@@ -105,35 +121,30 @@ __global__ __launch_bounds__(256) void k_mx4_dequantize(const unsigned char *__r
                                                         const Mx4Tiles z, T *__restrict__ dst)
 {
     const int lane = threadIdx.x & 63, nq = lane & 15, kg = lane >> 4;
-    for (int64_t t = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); t < z.total;
-         t += (int64_t)gridDim.x * 4) {
-        int64_t e;
-        int k0, n0;
-        place(z, t, &e, &k0, &n0);
-        const int n = n0 + 4 * nq, k = k0 + 8 * kg;
-        if (n >= z.N) continue;
-        const unsigned char *tile = src + t * kMx4Tile;
-        const uint4 q = *reinterpret_cast<const uint4 *>(tile + 16 * lane);
-        const uint32_t scales = *reinterpret_cast<const uint32_t *>(tile + kMx4Codes + 4 * nq);
-        const uint32_t word[4] = {q.x, q.y, q.z, q.w};
-        float v[8][4];
+    const Mx4Place at = place(z);
+    const int n = at.n0 + 4 * nq, k = at.k0 + 8 * kg;
+    if (n >= z.N) return;
+    const unsigned char *tile = src + at.dst * kMx4Tile;
+    const uint4 q = *reinterpret_cast<const uint4 *>(tile + 16 * lane);
+    const uint32_t scales = *reinterpret_cast<const uint32_t *>(tile + kMx4Codes + 4 * nq);
+    const uint32_t word[4] = {q.x, q.y, q.z, q.w};
+    float v[8][4];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-            const float s = __uint_as_float(((scales >> (8 * c)) & 0xffu) << 23);
-            const float2 a = decode2<0>(word[c], s), b = decode2<1>(word[c], s);
-            const float2 g = decode2<2>(word[c], s), h = decode2<3>(word[c], s);
-            const float col[8] = {a.x, a.y, b.x, b.y, g.x, g.y, h.x, h.y};
+    for (int c = 0; c < 4; ++c) {
+        const float s = __uint_as_float(((scales >> (8 * c)) & 0xffu) << 23);
+        const float2 a = decode2<0>(word[c], s), b = decode2<1>(word[c], s);
+        const float2 g = decode2<2>(word[c], s), h = decode2<3>(word[c], s);
+        const float col[8] = {a.x, a.y, b.x, b.y, g.x, g.y, h.x, h.y};
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i][c] = col[i];
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (k + i < z.Kd)
-                Vec<T, 4>::store(dst + ((e * z.Kd + k + i) * (int64_t)z.N + n), v[i]);
+        for (int i = 0; i < 8; ++i) v[i][c] = col[i];
     }
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        if (k + i < z.Kd)
+            Vec<T, 4>::template store<true>(dst + at.src + ((int64_t)(k + i) * z.N + n), v[i]);
 }
 
-Mx4Tiles mx4_tiles(int E, int Kd, int N, bool gateup)
+Mx4Tiles mx4_tiles(int Kd, int N, bool gateup)
 {
     Mx4Tiles z;
     z.Kd = Kd;
@@ -141,36 +152,33 @@ Mx4Tiles mx4_tiles(int E, int Kd, int N, bool gateup)
     z.nm = gateup ? 1 : 2;
     z.gs = (N + 256 * z.nm - 1) / (256 * z.nm);
     z.nst = (Kd + 31) / 32;
-    z.total = (int64_t)E * z.gs * z.nst * 4 * z.nm;
     return z;
 }
 
-dim3 mx4_grid(const Mx4Tiles &z)
-{
-    const int64_t want = (z.total + 3) / 4;
-    return dim3((unsigned)(want < (1 << 18) ? want : 1 << 18));
-}
+// (a matrix of at most 2^30 weights has fewer than 2^24 tiles)
+dim3 mx4_grid(const Mx4Tiles &z, int E) { return dim3((unsigned)z.gs * z.nst * z.nm, E); }
 
 }  // namespace
 
 size_t mx4_weight_bytes(int E, int Kd, int N, bool gateup)
 {
-    return (size_t)mx4_tiles(E, Kd, N, gateup).total * kMx4Tile;
+    const Mx4Tiles z = mx4_tiles(Kd, N, gateup);
+    return (size_t)E * z.gs * z.nst * 4 * z.nm * kMx4Tile;
 }
 
 hipError_t launch_mx4_quantize(int dtype, const void *src, int E, int Kd, int N, bool gateup,
                                void *dst, hipStream_t s)
 {
-    const Mx4Tiles z = mx4_tiles(E, Kd, N, gateup);
+    const Mx4Tiles z = mx4_tiles(Kd, N, gateup);
     unsigned char *o = static_cast<unsigned char *>(dst);
     if (dtype == 0)
-        hipLaunchKernelGGL(k_mx4_quantize<float>, mx4_grid(z), dim3(256), 0, s,
+        hipLaunchKernelGGL(k_mx4_quantize<float>, mx4_grid(z, E), dim3(256), 0, s,
                            static_cast<const float *>(src), z, o);
     else if (dtype == 1)
-        hipLaunchKernelGGL(k_mx4_quantize<_Float16>, mx4_grid(z), dim3(256), 0, s,
+        hipLaunchKernelGGL(k_mx4_quantize<_Float16>, mx4_grid(z, E), dim3(256), 0, s,
                            static_cast<const _Float16 *>(src), z, o);
     else
-        hipLaunchKernelGGL(k_mx4_quantize<__bf16>, mx4_grid(z), dim3(256), 0, s,
+        hipLaunchKernelGGL(k_mx4_quantize<__bf16>, mx4_grid(z, E), dim3(256), 0, s,
                            static_cast<const __bf16 *>(src), z, o);
     return hipGetLastError();
 }
@@ -178,16 +186,16 @@ hipError_t launch_mx4_quantize(int dtype, const void *src, int E, int Kd, int N,
 hipError_t launch_mx4_dequantize(int dtype, const void *src, int E, int Kd, int N, bool gateup,
                                  void *dst, hipStream_t s)
 {
-    const Mx4Tiles z = mx4_tiles(E, Kd, N, gateup);
+    const Mx4Tiles z = mx4_tiles(Kd, N, gateup);
     const unsigned char *i = static_cast<const unsigned char *>(src);
     if (dtype == 0)
-        hipLaunchKernelGGL(k_mx4_dequantize<float>, mx4_grid(z), dim3(256), 0, s, i, z,
+        hipLaunchKernelGGL(k_mx4_dequantize<float>, mx4_grid(z, E), dim3(256), 0, s, i, z,
                            static_cast<float *>(dst));
     else if (dtype == 1)
-        hipLaunchKernelGGL(k_mx4_dequantize<_Float16>, mx4_grid(z), dim3(256), 0, s, i, z,
+        hipLaunchKernelGGL(k_mx4_dequantize<_Float16>, mx4_grid(z, E), dim3(256), 0, s, i, z,
                            static_cast<_Float16 *>(dst));
     else
-        hipLaunchKernelGGL(k_mx4_dequantize<__bf16>, mx4_grid(z), dim3(256), 0, s, i, z,
+        hipLaunchKernelGGL(k_mx4_dequantize<__bf16>, mx4_grid(z, E), dim3(256), 0, s, i, z,
                            static_cast<__bf16 *>(dst));
     return hipGetLastError();
 }
