@@ -360,7 +360,8 @@ int moe_forward_packed(const void *x, const int32_t *ids, const float *w, const 
  * even code: no value is clamped but magnitudes above 6 * 2^120. The relative error
  * is at most 1/5 for magnitudes of at least 2^e, the absolute one at most 2^(e-2)
  * below that. A block with a value that is not finite has s = 255. Weights that are
- * values of this format already (whatever rule chose their scales) are kept exactly.
+ * values of this format already, by scales from 2^-110 to 2^120 (whatever rule chose
+ * them), are kept exactly.
  *
  * moe_mx4_dequantize -- the values that packed weights stand for, row-major, in
  * dtype (rounded to nearest even where the type does not hold them).

@@ -42,6 +42,10 @@
 //    long prompt planned as one call): runs of 4 items x 256 weight columns on
 //    8 wavefronts, operands loaded straight into LDS (k_big, below), which
 //    turns those experts from weight streaming into matrix-core work.
+//  * Weights in microscaled 4 bits (moe_mx4_quantize): tiles in the packed
+//    order, made into operands in registers. Every item is a wide cell, or in
+//    small launches a set of narrow ones (ffn_mx4.hip).
+// The cells are in ffn_cells.hpp.
 #include "ffn_cells.hpp"
 
 namespace moe {
@@ -705,7 +709,7 @@ int64_t narrow_blocks(const FfnShape &z, int wf, int N, bool gateup)
         z.max_rows >= kNarrowBelowRows * z.max_items)
         return 0;
     const int slice = group_cols(gateup) / kWavesPerBlock;
-    return (z.max_items * ((N + slice - 1) / slice) + 7) / 8 * 8;
+    return z.max_items * ((N + slice - 1) / slice);
 }
 
 // gate/up in the weight layout wf (fp32 has no 4-bit form: the caller refuses it)

@@ -675,6 +675,13 @@ __device__ __forceinline__ void wide_cells(const GemmArgs &p, const WorkItem it,
 //  * a wavefront keeps S - 1 steps (of 1 KB and 64 bytes a stream) in flight: two
 //    registers' worth of loads an operand, in place of 16.
 // Steps past the range load zeros (code 0, scale 2^-127), which add nothing.
+// Measured, 2,048 tokens, 512 experts, top-10, 2,560 x 768, fp16: gate/up 256 us (1.07 GB
+// of weights: 4.2 TB/s), down 159 us (0.53 GB, and 210 MB of fp32 written). In the form
+// that 16-bit weights' cells have, with a conversion in front, 379 and 222. Stamps show
+// what bounds them: routing is uneven (99 experts have more than 64 rows, and each of
+// their items reads the weights again), and of a workgroup's 16 to 25 us the item, the
+// row list and the first loads take 3, the last sums 1.4 (down: 5, its stores).
+// Workgroups that take cell after cell (512, 1,024 or 1,536 of them) were slower.
 constexpr int mx4_stages(int nmt) { return nmt >= 4 ? 4 : 6; }
 
 template <typename T, bool GATEUP, bool GATHERED, int NMT>
@@ -1052,27 +1059,25 @@ __device__ __forceinline__ void gemm_cell(const GemmArgs &p, const WorkItem *__r
                                           int ke, int split, uint4 *__restrict__ lds,
                                           float2 *__restrict__ rinfo)
 {
-    const int run = it.run & 0xff, j = (it.run >> 8) & 0xff;
+    [[maybe_unused]] const int run = it.run & 0xff, j = (it.run >> 8) & 0xff;
     if constexpr (WF == kMx4) {
         // items in runs too: their weights come from L2 the second time, and a wide
         // cell takes less time than a tall one of the same work (down projection of
         // the prefill layer, 64 rows each: 25 against 30 us)
         single_cell<T, GATEUP, GATHERED, WF, DEEP>(p, it, g, kb, ke, split, lds, rinfo, nullptr);
-        return;
-    } else
-    // a run of 4 is taken as two runs of 2 (4-item cells, one column slice of
-    // 256 rows each: the skewed long prompt's layer 0.8% slower)
-    if (run == 4 && j < 4 && i >= j) {
-        tall_cells<T, GATEUP, GATHERED, WF, DEEP, 2>(p, items, i - (j & 1), nitems, g, j & 1, kb,
-                                                     ke, split, lds, rinfo);
-        return;
+    } else {
+        // a run of 4 is taken as two runs of 2 (4-item cells, one column slice of
+        // 256 rows each: the skewed long prompt's layer 0.8% slower)
+        if (run == 4 && j < 4 && i >= j)
+            tall_cells<T, GATEUP, GATHERED, WF, DEEP, 2>(p, items, i - (j & 1), nitems, g, j & 1,
+                                                         kb, ke, split, lds, rinfo);
+        else if (run == 2 && j < 2 && i >= j)
+            tall_cells<T, GATEUP, GATHERED, WF, DEEP, 2>(p, items, i - j, nitems, g, j, kb, ke,
+                                                         split, lds, rinfo);
+        else
+            single_cell<T, GATEUP, GATHERED, WF, DEEP>(p, it, g, kb, ke, split, lds, rinfo,
+                                                       nullptr);
     }
-    if (run == 2 && j < 2 && i >= j) {
-        tall_cells<T, GATEUP, GATHERED, WF, DEEP, 2>(p, items, i - j, nitems, g, j, kb, ke, split,
-                                                     lds, rinfo);
-        return;
-    }
-    single_cell<T, GATEUP, GATHERED, WF, DEEP>(p, it, g, kb, ke, split, lds, rinfo, nullptr);
 }
 
 // One workgroup per (work item, group of 4 column slices, K split).

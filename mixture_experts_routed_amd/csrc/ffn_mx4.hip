@@ -62,7 +62,8 @@ __global__ __launch_bounds__(256, 3) void k_narrow(const GemmArgs p,
         it = s_item;
     } else {
         // (no workgroup shares another's weights: block order, so that the item is asked for
-        // with the count and not after it)
+        // with the count and not after it; the grid is the list's capacity times the slices,
+        // so there is an item to read, if one without meaning)
         lb = blockIdx.x;
         it = items[lb / slices];
         if (lb >= ctl[0] * slices) return;  // whole workgroup: no barrier reached
@@ -179,9 +180,10 @@ hipError_t gateup_mx4_t(const GemmArgs &p, int64_t blocks, bool narrow, bool gat
     const dim3 grid((unsigned)blocks), block(256);
     const int32_t *ctl = ctl_of(scratch);
     const WorkItem *items = items_of(scratch);
-    if (gathered && wp && wp->ids)
-        hipLaunchKernelGGL((k_narrow<T, true, true, true>), dim3(grid.x + 8), block, 0, s, p, ctl,
-                           items, *wp);
+    if (gathered && wp && wp->ids)  // planned here: 8 workgroups before the cells', which
+                                    // are dealt to the XCDs: a multiple of 8
+        hipLaunchKernelGGL((k_narrow<T, true, true, true>), dim3((grid.x + 7) / 8 * 8 + 8), block,
+                           0, s, p, ctl, items, *wp);
     else if (gathered)
         hipLaunchKernelGGL((k_narrow<T, true, true, false>), grid, block, 0, s, p, ctl, items,
                            WavePlan{});

@@ -12,6 +12,13 @@
 // The weights' gradients are summed per thread over the group's rows, written as one
 // partial row per group, and added over the groups in order by a second launch:
 // results do not depend on timing. Longer rows are read again for each pass.
+//
+// Measured: 32,768 rows of 2,560, fp32 y and residual, fp16 h: 244 us (1.17 GB, 4.8 TB/s;
+// read again for each pass 669). Gradients of 8,192 rows of 4,096, bf16, a gate per
+// element, 102 us (537 MB, 5.3 TB/s) and 5 to 6 for the second launch (read again for
+// each pass, 2,115 in all). 4 rows of 2,816: 3.5 us. A copy of 2 GiB moves 4.9 TB/s.
+// Not taken: loads or stores past the caches (forward 5 to 7% slower), columns in two
+// runs of 4 a thread (forward with fp32 rows 5% faster, gradients 10 to 38% slower).
 #include "lanes.hpp"
 #include "launch.hpp"
 #include "mfma.hpp"
