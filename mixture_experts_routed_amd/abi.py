@@ -947,12 +947,15 @@ def _gate(gate, kind, name, dev, T, d, dtype, channel=None):
                 else dtype, 16), 0
 
 
-def _norm_dtype(*given):
-    """the type that the weights and the gate share, or the first matrix's"""
-    for t in given:
+def _norm_dtype(r, y, *weights):
+    """the type that the weights and the gate share; without any, that of y, or of the
+    residual stream r next to an fp32 y"""
+    for t in weights:
         if t is not None:
             return t.dtype
-    raise ValueError("y or w_pre is needed")
+    if y is None:
+        raise ValueError("y or w_pre is needed")
+    return y.dtype if y.dtype is not torch.float32 else r.dtype
 
 
 def norm(r, y=None, w_post=None, gate=None, gate_kind: str = "none", w_pre=None,
@@ -967,7 +970,7 @@ def norm(r, y=None, w_post=None, gate=None, gate_kind: str = "none", w_pre=None,
     with _On(r, "r", stream) as at:
         dev, R = at.index, r.dtype
         T, d = _matrix_shape(r, "r")
-        D = _norm_dtype(w_pre, w_post, gate, y)
+        D = _norm_dtype(r, y, w_pre, w_post, gate)
         kind = _named("gate_kind", gate_kind, GATES)
         got = {}
         if y is not None:
@@ -1003,18 +1006,19 @@ def norm_backward(z, stats, dz=None, dh=None, y=None, w_post=None, gate=None,
     """Gradients of norm() from dz (of z, from behind; or None) and dh (of h, given with
     w_pre), with its z (r where there was no y), stats and other arguments. Returns (dict,
     workspace): dr, and those of dy, dgate, dw_post, dw_pre that apply (or that `grads`
-    names); dr may be dz itself. dw_post, dw_pre and a per-channel dgate are in
+    names or a tensor is given for); dr may be dz itself. dw_post, dw_pre and a per-channel dgate are in
     grad_dtype (the weights' type, or torch.float32)."""
     with _On(z, "z", stream) as at:
         dev, R, F = at.index, z.dtype, torch.float32
         T, d = _matrix_shape(z, "z")
-        D = _norm_dtype(w_pre, w_post, gate, y)
+        D = _norm_dtype(z, y, w_pre, w_post, gate)
         kind = _named("gate_kind", gate_kind, GATES)
         given = {"dr": dr, "dy": dy, "dgate": dgate, "dw_post": dw_post, "dw_pre": dw_pre}
         able = {"dr": True, "dy": y is not None, "dgate": gate is not None,
                 "dw_post": w_post is not None, "dw_pre": w_pre is not None}
         ask = set(k for k in able if able[k]) if grads is None else set(grads) | {"dr"}
-        for k in ask | {k for k in given if given[k] is not None}:
+        ask |= {k for k in given if given[k] is not None}
+        for k in ask:
             if not able.get(k):
                 raise ValueError(f"{k}: there is no such gradient in this call")
         sums = [given[k].dtype for k in ("dw_post", "dw_pre") if given[k] is not None]

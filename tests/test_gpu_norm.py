@@ -219,3 +219,33 @@ def test_rows_next_to_the_ends_of_the_range():
         assert np.array_equal(np.isnan(x), np.isnan(y)), k
         t = tol[k] + np.abs(y) * ref.U32 + 2.0 ** -126
         assert (np.abs(x - y)[fine] <= t[fine]).all(), k
+
+
+def test_residual_alone_gives_the_type():
+    """an fp32 output onto a 16-bit residual stream, nothing else that names a type"""
+    say("[norm] no weights, fp32 y")
+    a, g = make(9, 264, BF16, F32, BF16, "none", False, False)
+    got = abi.norm(a["r"], y=a["y"], alpha=0.5)
+    assert set(got) == {"z"}
+    want = ref.f64(a["r"]) + 0.5 * ref.f64(a["y"])
+    off = np.abs(ref.f64(got["z"]) - want)
+    assert (off <= np.abs(want) * ref.HALF[BF16] + 2.0 ** -20).all()
+    dz = rows(g, 9, 264, BF16)
+    grads, _ = abi.norm_backward(got["z"], torch.zeros((9, 2), device="cuda"), dz=dz, y=a["y"],
+                                 alpha=0.5)
+    assert set(grads) == {"dr", "dy"} and grads["dy"].dtype is F32
+    assert torch.equal(grads["dr"], dz) and torch.equal(grads["dy"], 0.5 * dz.float())
+
+
+def test_a_given_gradient_is_asked_for():
+    say("[norm] given gradients")
+    a, g = make(20, 264, BF16, F32, F32, "token", True, True)
+    got, _ = check_forward(a, "token", BF16)
+    dz, dh = rows(g, 20, 264, F32), rows(g, 20, 264, BF16)
+    kw = dict(dz=dz, dh=dh, **{k: v for k, v in a.items() if k != "r"}, gate_kind="token")
+    every, _ = abi.norm_backward(got["z"], got["stats"], **kw)
+    mine = torch.full((264,), 7.0, dtype=BF16, device="cuda")
+    some, _ = abi.norm_backward(got["z"], got["stats"], grads=["dy"], dw_pre=mine, **kw)
+    assert set(some) == {"dr", "dy", "dw_pre"} and some["dw_pre"] is mine
+    for k in some:
+        assert torch.equal(some[k], every[k]), k
