@@ -40,7 +40,8 @@ PROFILES = os.path.join(ROOT, "profiles")
 TRAFFIC_RECORD = os.path.join(PROFILES, "prefill_fp16_hbm_traffic.md")
 TIMER_EVERY = 5  # timed steps that also record the gate/up kernel's HIP events
 GEMM_SOURCES = ["mixture_experts_routed_amd/csrc/ffn.hip", "mixture_experts_routed_amd/csrc/common.hpp",
-                "mixture_experts_routed_amd/csrc/plan_wave.hpp"]
+                "mixture_experts_routed_amd/csrc/plan_wave.hpp",
+                "mixture_experts_routed_amd/csrc/ffn_cells.hpp"]
 COPY_KERNEL = "__amd_rocclr_copyBuffer"
 
 
@@ -138,14 +139,14 @@ def gemm_source_hash() -> str:
 
 
 def gemm_flags(name: str):
-    """k_expert_gemm<T, GATEUP, GATHERED, PACKED>: the three flags from the (mangled
-    or demangled) kernel name, or None"""
+    """k_expert_gemm<T, GATEUP, GATHERED, LAYOUT>: the two flags, and whether the weights'
+    layout (row-major or packed, as a number or a flag) is packed, from the (mangled or
+    demangled) kernel name, or None"""
     import re
-    m = re.search(r"k_expert_gemmI(?:DF16_|DF16b|f)Lb([01])ELb([01])ELb([01])E", name)
-    if m:
-        return tuple(g == "1" for g in m.groups())
-    m = re.search(r"k_expert_gemm<[^,]+,\s*(true|false),\s*(true|false),\s*(true|false)", name)
-    return tuple(g == "true" for g in m.groups()) if m else None
+    m = (re.search(r"k_expert_gemmI(?:DF16_|DF16b|f)Lb([01])ELb([01])EL[bi]([01])E", name) or
+         re.search(r"k_expert_gemm<[^,]+,\s*(true|false),\s*(true|false),\s*(true|false|[01])\b",
+                   name))
+    return tuple(g in ("1", "true") for g in m.groups()) if m else None
 
 
 def gemm_is_gateup(name: str) -> bool:
