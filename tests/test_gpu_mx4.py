@@ -251,3 +251,36 @@ def test_a_block_that_is_not_finite_reaches_its_column_only():
     out, _ = abi.forward_mx4(case.d("x"), case.d("ids"), case.d("w"), packed, 2, 40, out_dtype=F32)
     bad = out.isnan()
     assert bad[:, 17].all() and bad.sum() == 20
+
+
+@pytest.mark.parametrize("T,d,E,f", [(131072, 8192, 4, 64), (512, 1 << 21, 32, 8)])
+def test_activations_of_2_gib(T, d, E, f):
+    """x past what one buffer descriptor addresses: its rows are gathered first, and the
+    wide cells (many rows of an expert) or the narrow ones (few) read those. Offsets into
+    x, y and the weights pass 32 bits. Of sampled tokens, h is rounded once to fp16
+    (2^-11); the sums' roundings are a random walk of at most d / 128 steps of 2^-24 (the
+    narrow cells cut d in four), 2^-17 at the most."""
+    say(f"[mx4] activations of 2 GiB {T} {d}")
+    assert T * d * 2 >= 1 << 31
+    g = torch.Generator(device="cuda").manual_seed(T)
+    x = torch.randn((T, d), generator=g, device="cuda", dtype=F16)
+    ids = torch.randint(0, E, (T, 1), generator=g, device="cuda", dtype=torch.int32)
+    w = torch.rand((T, 1), generator=g, device="cuda") + 0.5
+    packed = {}
+    for k, kind in (("gate", "gate"), ("up", "gate"), ("down", "down")):
+        shape = (E, d, f) if kind == "gate" else (E, f, d)
+        m = torch.randn(shape, generator=g, device="cuda", dtype=F16) * shape[1] ** -0.5
+        packed[k] = abi.mx4_quantize(m, kind)
+        del m
+    out, _ = abi.forward_mx4(x, ids, w, packed, E, f, out_dtype=F32)
+    toks = [0, 1, T // 2 + 1, T - 2, T - 1]
+    rows, eid, wt = x[toks].cpu().double(), ids[toks, 0].tolist(), w[toks, 0].cpu().double()
+    got = out[toks].cpu().double()
+    del x, out
+    values = {k: abi.mx4_dequantize(packed[k], E, d, f, kind, dtype=F16)
+              for k, kind in (("gate", "gate"), ("up", "gate"), ("down", "down"))}
+    for i, e in enumerate(eid):
+        wg, wu, wd = (values[k][e].cpu().double() for k in ("gate", "up", "down"))
+        a = rows[i] @ wg
+        want = wt[i] * ((a * torch.sigmoid(a) * (rows[i] @ wu)) @ wd)
+        assert (got[i] - want).norm() <= 2.0 ** -10 * want.norm(), toks[i]
