@@ -249,3 +249,34 @@ def test_a_given_gradient_is_asked_for():
     assert set(some) == {"dr", "dy", "dw_pre"} and some["dw_pre"] is mine
     for k in some:
         assert torch.equal(some[k], every[k]), k
+
+
+@pytest.mark.parametrize("d", [264, 1003, 9000])
+def test_offsets_past_32_bits(d):
+    """rows 2^20 elements apart, past 2^31 in all, give what rows next to each other give"""
+    say(f"[norm] far rows {d}")
+    T, ld = 2052, 1 << 20
+    a, g = make(T, d, BF16, BF16, BF16, "full", True, True)
+    far = torch.empty((T - 1) * ld + d, dtype=BF16, device="cuda").as_strided((T, d), (ld, 1))
+    dz, dh = rows(g, T, d, BF16), rows(g, T, d, BF16)
+    rest = {k: v for k, v in a.items() if k not in ("r", "y", "gate")}
+    near = abi.norm(a["r"], y=a["y"], gate=a["gate"], gate_kind="full", stats=True, **rest)
+    back, _ = abi.norm_backward(near["z"], near["stats"], dz=dz, dh=dh, y=a["y"], gate=a["gate"],
+                                gate_kind="full", **rest)
+    for name in ("r", "y", "gate", "z", "h"):
+        t = {**a, **near}[name]
+        far.copy_(t)
+        kw = dict(a, stats=True, gate_kind="full")
+        out = {name: far} if name in ("z", "h") else {}
+        kw.update(out or {name: far})
+        got = abi.norm(kw.pop("r"), **kw)
+        for k in near:
+            assert torch.equal(got[k], near[k]), (name, k)
+    for name in ("dz", "dh", "z", "y", "gate", "dr", "dy", "dgate"):
+        kw = dict(z=near["z"], dz=dz, dh=dh, y=a["y"], gate=a["gate"], **rest)
+        if name in kw:
+            far.copy_(kw[name])
+        kw[name] = far
+        got, _ = abi.norm_backward(kw.pop("z"), near["stats"], gate_kind="full", **kw)
+        for k in back:
+            assert torch.equal(got[k], back[k]), (name, k)

@@ -216,3 +216,29 @@ def test_gradient_of_odd_rows(score, renorm):
     logits[9, :3], ids[9] = 200.0, [0, 1, 5, 6, 7]
     dw[0], dw[2, 1:] = NAN, INF          # of entries that lead nowhere
     check_backward(logits, ids, dw, score=score, renorm=renorm, scale=0.5)
+
+
+@pytest.mark.parametrize("E", [512, 513])
+def test_offsets_past_32_bits(E):
+    """2^31 logits and more: the last tokens' rows as in a call of their own"""
+    say(f"[route_scored] many tokens {E}")
+    T, K, n = (1 << 31) // 512 + 5, 2, 300
+    g = torch.Generator(device="cuda").manual_seed(E)
+    logits = torch.zeros((T, E), device="cuda")
+    logits[:, 3], logits[:, 70] = 2.0, 1.0
+    logits[-n:] = torch.randn((n, E), generator=g, device="cuda")
+    bias = torch.randn(E, generator=g, device="cuda") * 0.05
+    dw = torch.rand((T, K), generator=g, device="cuda")
+    kw = dict(bias=bias, score="sigmoid")
+    ids, w = abi.route_scored(logits, K, **kw)
+    last = logits[-n:].clone()
+    few_ids, few_w = abi.route_scored(last, K, **kw)
+    assert torch.equal(ids[-n:], few_ids) and torch.equal(w[-n:], few_w)
+    got = abi.route_scored_backward(logits, ids, dw, renorm=False, out_dtype=torch.bfloat16)
+    assert torch.equal(got[-n:], abi.route_scored_backward(
+        last, few_ids, dw[-n:].clone(), renorm=False, out_dtype=torch.bfloat16))
+    del got
+    add = torch.ones((T, E), device="cuda")  # onto another gradient, in place
+    assert abi.route_scored_backward(logits, ids, dw, renorm=False, add=add, out=add) is add
+    assert torch.equal(add[-n:], abi.route_scored_backward(
+        last, few_ids, dw[-n:].clone(), renorm=False, add=torch.ones((n, E), device="cuda")))
