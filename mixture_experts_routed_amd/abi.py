@@ -34,6 +34,7 @@ MOE_GRAD_X, MOE_GRAD_W, MOE_GRAD_BIAS = 1, 2, 4
 ACT8_BLOCK = 32  # MOE_ACT8_BLOCK
 SCORES = {"softmax": 0, "sigmoid": 1}  # enum moe_score
 GATES = {"none": 0, "token": 1, "channel": 2, "full": 3}  # enum moe_gate
+NORM_GRADS = frozenset(("dr", "dy", "dgate", "dw_post", "dw_pre"))
 MX4_KINDS = {"gate": MOE_W_GATE_UP, "down": MOE_W_DOWN}  # gate: gate and up matrices
 STAGES = ("hist", "scan", "place", "gather", "worklist", "gateup", "down", "combine")
 TORCH_DTYPE = {MOE_F32: torch.float32, MOE_F16: torch.float16, MOE_BF16: torch.bfloat16}
@@ -1013,40 +1014,52 @@ def norm_backward(z, stats, dz=None, dh=None, y=None, w_post=None, gate=None,
         T, d = _matrix_shape(z, "z")
         D = _norm_dtype(z, y, w_pre, w_post, gate)
         kind = _named("gate_kind", gate_kind, GATES)
-        given = {"dr": dr, "dy": dy, "dgate": dgate, "dw_post": dw_post, "dw_pre": dw_pre}
-        able = {"dr": True, "dy": y is not None, "dgate": gate is not None,
-                "dw_post": w_post is not None, "dw_pre": w_pre is not None}
-        ask = set(k for k in able if able[k]) if grads is None else set(grads) | {"dr"}
-        ask |= {k for k in given if given[k] is not None}
-        for k in ask:
-            if not able.get(k):
-                raise ValueError(f"{k}: there is no such gradient in this call")
-        sums = [given[k].dtype for k in ("dw_post", "dw_pre") if given[k] is not None]
-        if given["dgate"] is not None and gate_kind == "channel":
-            sums.append(given["dgate"].dtype)
-        G = grad_dtype or (sums[0] if sums else D)
+        every = grads is None
+
+        def asked(name, given, able):
+            if given is None and not (able if every else name in grads):
+                return False
+            if not able:
+                raise ValueError(f"{name}: there is no such gradient in this call")
+            return True
+
+        if not every and not NORM_GRADS.issuperset(grads):
+            raise ValueError(f"grads: expected some of {', '.join(sorted(NORM_GRADS))}")
+        per_channel = gate is not None and gate_kind == "channel"
+        G = grad_dtype
+        if G is None:
+            G = next((t.dtype for t in (dw_post, dw_pre, dgate if per_channel else None)
+                      if t is not None), D)
         if G is not D and G is not F:
             raise TypeError(f"grad_dtype: expected {D} or torch.float32, got {G}")
-        like = {"dr": ((T, d), R), "dy": ((T, d), y.dtype if y is not None else D),
-                "dgate": (((T,), (d,), (T, d))[max(kind, 1) - 1], G if gate_kind == "channel" else D),
-                "dw_post": ((d,), G), "dw_pre": ((d,), G)}
-        got = {k: at.empty(*like[k]) if given[k] is None else given[k] for k in like if k in ask}
+        Y = D if y is None else y.dtype
+        got = {"dr": at.empty((T, d), R) if dr is None else dr}
+        if asked("dy", dy, y is not None):
+            got["dy"] = dy = at.empty((T, d), Y) if dy is None else dy
+        if asked("dgate", dgate, gate is not None):
+            if dgate is None:
+                dgate = at.empty(((T,), (d,), (T, d))[kind - 1], G if per_channel else D)
+            got["dgate"] = dgate
+        if asked("dw_post", dw_post, w_post is not None):
+            got["dw_post"] = dw_post = at.empty((d,), G) if dw_post is None else dw_post
+        if asked("dw_pre", dw_pre, w_pre is not None):
+            got["dw_pre"] = dw_pre = at.empty((d,), G) if dw_pre is None else dw_pre
         pdz, lddz = _mat(dz, "dz", dev, T, d, R)
         pdh, lddh = _mat(dh, "dh", dev, T, d, D)
         pz, ldz = _mat(z, "z", dev, T, d, D, F)
         py, ldy = _mat(y, "y", dev, T, d, D, F)
         pg, ldg = _gate(gate, kind, "gate", dev, T, d, D)
         pdr, lddr = _mat(got["dr"], "dr", dev, T, d, R)
-        pdy, lddy = _mat(got.get("dy"), "dy", dev, T, d, like["dy"][1])
-        pdg, lddg = _gate(got.get("dgate"), kind, "dgate", dev, T, d, D, G)
+        pdy, lddy = _mat(dy, "dy", dev, T, d, Y)
+        pdg, lddg = _gate(dgate, kind, "dgate", dev, T, d, D, G)
         workspace, ws, have = at.workspace(workspace, moe_norm_backward_workspace(T, d))
         dtype = _dtype("the weights", D)
         rc = lib().moe_norm_backward(
             pdz, lddz, pdh, lddh, pz, ldz, _dtype("z", R), py, ldy,
-            dtype if y is None else _dtype("y", y.dtype), _vec(w_post, "w_post", dev, d, D, 16),
-            pg, ldg, kind, _vec(w_pre, "w_pre", dev, d, D, 16),
-            _vec(stats, "stats", dev, 2 * T, F), dtype, T, d, alpha, ws, have, pdr, lddr, pdy,
-            lddy, pdg, lddg, _vec(got.get("dw_post"), "dw_post", dev, d, G, 16),
-            _vec(got.get("dw_pre"), "dw_pre", dev, d, G, 16), DTYPE_OF[G], at.handle)
+            _dtype("y", Y), _vec(w_post, "w_post", dev, d, D, 16), pg, ldg, kind,
+            _vec(w_pre, "w_pre", dev, d, D, 16), _vec(stats, "stats", dev, 2 * T, F), dtype, T, d,
+            alpha, ws, have, pdr, lddr, pdy, lddy, pdg, lddg,
+            _vec(dw_post, "dw_post", dev, d, G, 16), _vec(dw_pre, "dw_pre", dev, d, G, 16),
+            DTYPE_OF[G], at.handle)
     _check("moe_norm_backward", rc)
     return got, workspace
