@@ -789,6 +789,7 @@ def _ckpt(dev, ckpt, T, f, gated):
 
 # ------------------------------------- operators around the routed layer's block --
 
+@functools.lru_cache(maxsize=1024)
 def moe_mx4_weight_bytes(E: int, d: int, f: int, kind: int) -> int:
     v = ctypes.c_size_t()
     _check("moe_mx4_weight_bytes", lib().moe_mx4_weight_bytes(E, d, f, kind, ctypes.byref(v)))
@@ -917,7 +918,8 @@ def forward_mx4(x, ids, w, packed, E: int, f: int, tm: int = 16, out_dtype=None,
         elif out_dtype is not None and out.dtype is not out_dtype:
             raise TypeError(f"out: expected {out_dtype}, got {out.dtype}")
         dtype = _dtype("x", D)
-        bgu, bdn = _mx4_bytes(E, d, f)
+        bgu = moe_mx4_weight_bytes(E, d, f, MOE_W_GATE_UP)
+        bdn = moe_mx4_weight_bytes(E, d, f, MOE_W_DOWN)
         workspace, ws, have = at.workspace(workspace, _forward_workspace(T, K, E, d, f, tm, dtype))
         rc = lib().moe_forward_mx4(
             _vec(x, "x", dev, T * d, D, 16), _vec(ids, "ids", dev, T * K, torch.int32),
@@ -929,12 +931,6 @@ def forward_mx4(x, ids, w, packed, E: int, f: int, tm: int = 16, out_dtype=None,
             _dtype("out", out.dtype), at.handle)
     _check("moe_forward_mx4", rc)
     return out, workspace
-
-
-@functools.lru_cache(maxsize=1024)
-def _mx4_bytes(E, d, f):
-    return (moe_mx4_weight_bytes(E, d, f, MOE_W_GATE_UP),
-            moe_mx4_weight_bytes(E, d, f, MOE_W_DOWN))
 
 
 def _gate(gate, kind, name, dev, T, d, dtype, channel=None):
