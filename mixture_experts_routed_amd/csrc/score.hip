@@ -333,11 +333,15 @@ __global__ __launch_bounds__(kWaves * 64) void k_route_scored(const ScoreCall p,
     const int64_t t = have ? t0 + r : p.T - 1;
     const float inf = __builtin_inff();
 
-    // (a NaN logit fails l > -inf, a NaN bias b > -inf: absent, like -inf)
+    // Absent: -inf. A NaN logit becomes it here, before anything is compared (its image
+    // among whole numbers would lie above every score's); a NaN bias fails b > -inf.
     float l[NJ], b[NJ], key[NJ];
     load_row<L, NJ, V>(p.logits + t * p.E, p.E, sub, l);
 #pragma unroll
-    for (int j = 0; j < NJ; ++j) b[j] = 0.f;
+    for (int j = 0; j < NJ; ++j) {
+        l[j] = __builtin_fmaxf(l[j], -inf);
+        b[j] = 0.f;
+    }
     if (p.bias) load_row<L, NJ, V>(p.bias, p.E, sub, b);
     // largest logit, and the softmax's denominator where it counts
     float m = -inf, sum = 1.f, tol = 0.f;
@@ -403,7 +407,7 @@ __global__ __launch_bounds__(kWaves * 64) void k_route_scored(const ScoreCall p,
             kept = choose_groups<L>(p, c, P, 0.f, &near);
             wave_lds_order();
         }
-        if (!p.bias) {  // by the logits (NaN is never a candidate)
+        if (!p.bias) {  // by the logits
 #pragma unroll
             for (int j = 0; j < NJ; ++j) key[j] = l[j];
         }
