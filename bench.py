@@ -139,14 +139,17 @@ def gemm_source_hash() -> str:
 
 
 def gemm_flags(name: str):
-    """k_expert_gemm<T, GATEUP, GATHERED, LAYOUT>: the two flags, and whether the weights'
-    layout (row-major or packed, as a number or a flag) is packed, from the (mangled or
+    """k_expert_gemm<T, GATEUP, GATHERED, LAYOUT>: the two flags and the weights' layout (0
+    row-major, 1 packed, as a number or a flag; 2 packed 4-bit), from the (mangled or
     demangled) kernel name, or None"""
     import re
-    m = (re.search(r"k_expert_gemmI(?:DF16_|DF16b|f)Lb([01])ELb([01])EL[bi]([01])E", name) or
-         re.search(r"k_expert_gemm<[^,]+,\s*(true|false),\s*(true|false),\s*(true|false|[01])\b",
+    m = (re.search(r"k_expert_gemmI(?:DF16_|DF16b|f)Lb([01])ELb([01])EL[bi]([0-2])E", name) or
+         re.search(r"k_expert_gemm<[^,]+,\s*(true|false),\s*(true|false),\s*(true|false|[0-2])\b",
                    name))
-    return tuple(g in ("1", "true") for g in m.groups()) if m else None
+    if not m:
+        return None
+    gateup, gathered, layout = (int(g) if g.isdigit() else int(g == "true") for g in m.groups())
+    return bool(gateup), bool(gathered), layout
 
 
 def gemm_is_gateup(name: str) -> bool:
@@ -156,13 +159,13 @@ def gemm_is_gateup(name: str) -> bool:
 
 
 def kernel_short_name(name: str) -> str:
-    """a kernel's name in the traffic record: k_expert_gemm/gateup or /down (packed
-    weights; _rowmajor with row-major ones), else the kernel's own name with its
+    """a kernel's name in the traffic record: k_expert_gemm/gateup or /down (packed weights;
+    _rowmajor with row-major ones, _mx4 with 4-bit ones), else the kernel's own name with its
     template arguments"""
     import re
-    if "k_expert_gemm" in name:
-        f = gemm_flags(name) or (False, False, True)
-        return f"k_expert_gemm/{'gateup' if f[0] else 'down'}{'' if f[2] else '_rowmajor'}"
+    f = gemm_flags(name)
+    if f:
+        return f"k_expert_gemm/{'gateup' if f[0] else 'down'}{('_rowmajor', '', '_mx4')[f[2]]}"
     m = re.search(r"moe::(k_\w+(?:<[^>]*>)?)|_ZN3moe(\d+)(k_\w+?)I", name)
     if m:
         return m.group(1) or m.group(3)
