@@ -78,16 +78,12 @@ __global__ __launch_bounds__(256, 3) void k_narrow(const GemmArgs p,
 
     // this wavefront's steps [s0, s0 + n) of the slice's tiles; loads of later steps are
     // outside its range: zeros, no memory traffic
-    const PackedGeom z = packed_geom(Kd, p.N, GATEUP, 2, true);
-    const int per = (z.nst + 3) / 4, s0 = wave * per;
-    const int n = max(0, min(per, z.nst - s0));
-    const int g = slice >> 2, w = slice & 3;
-    const size_t tb = ((((size_t)it.expert * z.gs + g) * z.nst + s0) * 4 + w) * z.m * kMx4Tile;
-    const uint32_t span = (uint32_t)n * z.step_bytes;
-    const uint32_t r0 = (uint32_t)__builtin_amdgcn_readfirstlane(
-        (int)(n > 0 ? span - (uint32_t)(w * z.m) * kMx4Tile : 0u));
-    const uint32_t r1 = (uint32_t)__builtin_amdgcn_readfirstlane(
-        (int)(n > 0 ? span - (uint32_t)(w * z.m + z.m - 1) * kMx4Tile : 0u));
+    const Mx4Quarter q4 = mx4_quarter(mx4_tiles(Kd, p.N, GATEUP), it.expert, slice, wave);
+    constexpr uint32_t kStep = 4 * (GATEUP ? 1 : 2) * kMx4Tile;  // bytes from step to step
+    const int s0 = q4.first, n = q4.count;
+    const size_t tb = q4.at;
+    const uint32_t r0 = (uint32_t)__builtin_amdgcn_readfirstlane((int)q4.bytes[0]);
+    const uint32_t r1 = (uint32_t)__builtin_amdgcn_readfirstlane((int)q4.bytes[1]);
     const char *b0c = static_cast<const char *>(p.B0);
     const __amdgpu_buffer_rsrc_t rb0 = make_rsrc(b0c + tb, r0);
     const __amdgpu_buffer_rsrc_t rb1 =
@@ -108,8 +104,8 @@ __global__ __launch_bounds__(256, 3) void k_narrow(const GemmArgs p,
         part.nrows = min(16, it.nrows - row);
         Stage st[S];
         auto load_b = [&](Stage &q, int s) {
-            q.b[0] = load_mx4(rb0, (uint32_t)s * z.step_bytes, lane);
-            q.b[1] = load_mx4(rb1, (uint32_t)s * z.step_bytes, lane);
+            q.b[0] = load_mx4(rb0, (uint32_t)s * kStep, lane);
+            q.b[1] = load_mx4(rb1, (uint32_t)s * kStep, lane);
         };
 #pragma unroll
         for (int j = 0; j < S - 1; ++j) load_b(st[j], j);

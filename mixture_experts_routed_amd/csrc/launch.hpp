@@ -6,6 +6,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include "mx4_index.hpp"
+
 namespace moe {
 
 // ---- plan: histogram, scan + pad fill, placement ----
@@ -84,8 +86,6 @@ bool wave_plan_fits(int64_t nent, int tm);
 // Layout of the expert weights that the grouped FFN reads: as given, in MFMA order
 // (moe_pack_weights), or in MFMA order as microscaled 4-bit codes (16-bit types)
 enum : int { kRowMajor = 0, kPacked = 1, kMx4 = 2 };
-// bytes of the codes, and of codes and scales, of a 32 x 64 tile of 4-bit weights
-constexpr uint32_t kMx4Codes = 1024, kMx4Tile = 1088;
 
 // runs_first: the items in runs of 4 first (item_slot), for the big cells
 hipError_t launch_worklist(const int32_t *eoff, int E, int64_t max_rows, void *scratch,

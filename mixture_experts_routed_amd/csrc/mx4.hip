@@ -31,32 +31,13 @@ namespace {
 
 constexpr int kMinExp = -110, kMaxExp = 120;
 
-struct Mx4Tiles {
-    int Kd, N, gs, nst, nm;
-};
-
-// A workgroup has the four wavefronts' tiles of one K-step and column slice of an expert
-// (blockIdx.y). All of it is the same for a wavefront, so one scalar division finds it:
-// with a running tile number, divided in 64 bits per lane, quantising took 178 us, not 162.
-struct Mx4Place {
-    int k0, n0;   // the tile's first row and column
-    int64_t src;  // the expert's first weight
-    int64_t dst;  // the tile
-};
-
+// All of a tile's place is the same for a wavefront (mx4_index.hpp), so one scalar division
+// finds it: with a running tile number, divided in 64 bits per lane, quantising took 178 us,
+// not 162.
 __device__ __forceinline__ Mx4Place place(const Mx4Tiles &z)
 {
-    const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const unsigned x = blockIdx.x;
-    const int m = z.nm == 2 ? x & 1 : 0;
-    const unsigned u = z.nm == 2 ? x >> 1 : x;
-    const unsigned slice = u / (unsigned)z.nst, step = u - slice * z.nst;
-    Mx4Place at;
-    at.k0 = (int)step * 32;
-    at.n0 = ((int)slice * 4 + w) * 64 * z.nm + 64 * m;
-    at.src = (int64_t)blockIdx.y * z.Kd * z.N;
-    at.dst = ((int64_t)blockIdx.y * z.gs * z.nst + u) * (4 * z.nm) + w * z.nm + m;
-    return at;
+    return mx4_place(z, blockIdx.x, blockIdx.y,
+                     __builtin_amdgcn_readfirstlane(threadIdx.x >> 6));
 }
 
 template <typename T>
@@ -144,26 +125,14 @@ __global__ __launch_bounds__(256) void k_mx4_dequantize(const unsigned char *__r
             Vec<T, 4>::template store<true>(dst + at.src + ((int64_t)(k + i) * z.N + n), v[i]);
 }
 
-Mx4Tiles mx4_tiles(int Kd, int N, bool gateup)
-{
-    Mx4Tiles z;
-    z.Kd = Kd;
-    z.N = N;
-    z.nm = gateup ? 1 : 2;
-    z.gs = (N + 256 * z.nm - 1) / (256 * z.nm);
-    z.nst = (Kd + 31) / 32;
-    return z;
-}
-
 // (a matrix of at most 2^30 weights has fewer than 2^24 tiles)
-dim3 mx4_grid(const Mx4Tiles &z, int E) { return dim3((unsigned)z.gs * z.nst * z.nm, E); }
+dim3 mx4_grid(const Mx4Tiles &z, int E) { return dim3(mx4_blocks(z), E); }
 
 }  // namespace
 
 size_t mx4_weight_bytes(int E, int Kd, int N, bool gateup)
 {
-    const Mx4Tiles z = mx4_tiles(Kd, N, gateup);
-    return (size_t)E * z.gs * z.nst * 4 * z.nm * kMx4Tile;
+    return mx4_bytes(mx4_tiles(Kd, N, gateup), E);
 }
 
 hipError_t launch_mx4_quantize(int dtype, const void *src, int E, int Kd, int N, bool gateup,
