@@ -3,26 +3,37 @@
 //   groups of E / G experts: worth = sum of the group_top largest c; `keep` stay
 //   the K largest c of those, ties to the lower index; w = scale s (/ sum of s)
 //
-// Choices are those of 64-bit arithmetic, and nearly all of them are made in 32: L
-// lanes hold a row of logits, each with 4 consecutive columns at a time where rows
-// are whole 16-byte chunks.
+// Choices are those of 64-bit arithmetic, made in 32 bits where those tell: L lanes hold a
+// row of logits, each with 4 consecutive columns at a time where rows are whole 16-byte
+// chunks.
 //  * The K-th largest of the lanes' own maxima bounds the K-th largest c from below.
-//    What reaches the bound, less what 32 bits may be off, are the candidates: about
-//    K to 2 K of them, one a lane, through LDS.
+//    What reaches the bound, less what 32 bits may be off, are the candidates, one a lane,
+//    through LDS.
 //  * A candidate's place is the number of candidates before it, so ordering them takes
 //    one compare each, not K rounds over the row.
 //  * What lies within the errors of its 32-bit values is too near to call: groups are
 //    chosen again from 64-bit scores, a sigmoid's candidates placed again by theirs,
 //    one a lane (2 rows of 1,000 at 512 experts). Rows where a softmax's biased scores
-//    lie so near, and those with more candidates than lanes (many equal logits), are
-//    taken again as a whole in 64 bits, one row a wavefront, a round per pick
-//    (exact_row). Without a bias experts are compared by their logits, which are
-//    exact.
+//    lie so near, and those with more candidates than lanes, are taken again as a whole
+//    in 64 bits, one row a wavefront, a round per pick (exact_row). Without a bias experts
+//    are compared by their logits, which are exact.
+//
+// Candidates stay few while K is at most half of the lanes: 11.6 for 10 picks of 512 experts
+// (32 lanes), 10.3 for 8 of 128 (16 lanes). As K nears the number of lanes with columns (32
+// experts have 8), the least of their maxima count and the bound falls; where open columns
+// lie in fewer than K lanes (one group of 32 columns: 8 lanes) there is none. Shares of rows
+// of normal logits that exact_row takes (a model of the bound), and the time of 32,768 such
+// rows without a bias: 128 experts, 8 picks 0.6%, 23 us; 10 picks 16%, 63 us; 12 picks 75%,
+// 120 us; 256 experts, 10 picks 20%, 80 us; 16 picks all, 181 us; 512 experts, 32 picks all,
+// 389 us; 1,024 experts, 64 picks all, 1,594 us. Equal logits in more columns than lanes
+// do the same: 96 us for 128 experts, 8 picks, 165 for 512, 10 picks. moe_route_topk, K rounds
+// a row whatever the logits, takes 34, 42, 49, 49, 75, 192, 564, 34 and 66 us there.
 //
 // Bound by vector arithmetic, and the gradient by HBM. Measured at 32,768 tokens, 512
-// experts, 10 picks: sigmoid scores with a bias, 4 of 8 groups by their two best, 41 us
-// (1,140 vector instructions a wavefront of two rows are 30 us of it; the 70 MB would
-// copy in 14); gradient of softmax scores, onto an fp16 output with another added, 28 us
+// experts, 10 picks: sigmoid scores with a bias, 4 of 8 groups by their two best, 41 us a
+// call in a row of calls (46 on another GPU; a kernel trace from an idle one has 44 at least,
+// 45 on average; 1,155 vector instructions a wavefront of two rows are 30 us of it; the 70 MB
+// would copy in 14); gradient of softmax scores, onto an fp16 output with another added, 28 us
 // (137 MB, 4.9 TB/s). 4 tokens, 128 experts: 3.8 us.
 // What the steps were worth: a round over the row a pick, 158 us; candidates by the bound,
 // ordered by counting, 91; groups and sigmoids settled within the row's lanes, not the
@@ -653,7 +664,8 @@ template <typename T, int L, int NJ> hipError_t backward_t(const ScoreBackwardCa
 }
 
 // lanes of a row and columns of a lane, for E experts: the fewest lanes that hold a row
-// with 16 columns each, and one of K things each (picks, groups)
+// with 16 columns each, and one of K things each (picks, groups). (As many picks as that
+// make most rows exact_row's: figures at the head.)
 template <typename F> hipError_t with_lanes(int E, int K, F run)
 {
     using std::integral_constant;
