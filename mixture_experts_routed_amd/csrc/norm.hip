@@ -4,19 +4,25 @@
 //
 // Everything is read and written once, so these kernels are bound by HBM. Up to
 // kMaxCols columns a row lies in registers, 8 columns a thread: a group of threads (a
-// wavefront, or a workgroup just wide enough) takes row after row, keeps the weights
-// of its columns, and issues the next row's loads before it reduces this one. Row
-// sums are lane moves and, between wavefronts, one LDS word each and one barrier.
-// Rows whose strides or addresses are not whole 16-byte chunks are taken a column at
-// a time (V = 1), thread t the columns t, t + n, ..., so that loads stay contiguous.
-// The weights' gradients are summed per thread over the group's rows, written as one
-// partial row per group, and added over the groups in order by a second launch:
-// results do not depend on timing. Longer rows are read again for each pass.
+// wavefront, or a workgroup just wide enough) takes row after row and keeps the weights
+// of its columns; up to 4,096 columns it issues the next row's loads before it reduces
+// this one. (Of the gradients' rows above 4,096 columns some lie in scratch: threads_of.)
+// Row sums are lane moves and, between wavefronts, one LDS word each and one barrier.
+// Rows whose length, strides or addresses are not whole 16-byte chunks are taken an
+// element a load (V = 1), thread t the columns t, t + n, ..., so that a wavefront's loads
+// lie together. The weights' gradients are summed per thread over the group's rows,
+// written as one partial row per group, and added over the groups in order by a second
+// launch: results do not depend on timing. Longer rows are read again for each pass, an
+// element a load.
 //
-// Measured: 32,768 rows of 2,560, fp32 y and residual, fp16 h: 244 us (1.17 GB, 4.8 TB/s;
-// read again for each pass 669). Gradients of 8,192 rows of 4,096, bf16, a gate per
-// element, 102 us (537 MB, 5.3 TB/s) and 5 to 6 for the second launch (read again for
-// each pass, 2,115 in all). 4 rows of 2,816: 3.5 us. A copy of 2 GiB moves 4.9 TB/s.
+// Measured: 32,768 rows of 2,560, fp32 y and residual, fp16 h: 245 us (1.17 GB, 4.8 TB/s;
+// read again for each pass 669); in bf16 148 us (4.5 TB/s), gradients 305 (3.3). Gradients
+// of 8,192 rows of 4,096, bf16, a gate per element, 102 us (537 MB, 5.3 TB/s) and 6 for the
+// second launch (read again for each pass, 2,115 in all). 4 rows of 2,816: 3.5 us. A copy of
+// 2 GiB moves 4.9 TB/s. Off that path, forward and gradients: 8,192 rows of 4,091, fp32 116
+// and 182 us (4.6 and 4.4 TB/s), bf16 115 and 491 (2.3 and 0.8: the same number of loads for
+// half the bytes, and 2-byte stores); 4,000 of 8,192, fp32 102 and 242 (5.1 and 3.2), bf16 47
+// and 89; 2,048 of 16,384, fp32 246 and 1,406 (2.2 and 0.6), bf16 393 and 2,123.
 // Not taken: loads or stores past the caches (forward 5 to 7% slower), columns in two
 // runs of 4 a thread (forward with fp32 rows 5% faster, gradients 10 to 38% slower).
 #include "lanes.hpp"
@@ -150,8 +156,11 @@ template <bool WAVE> struct Team {
     }
 };
 
-// most threads of a workgroup: those of the larger ones hold one row at a time (a
-// row ahead would not fit their registers)
+// Most threads of a workgroup. The larger ones (more than 512 threads, at most 128 registers
+// each) hold one row at a time. The forward kernels fit (71 to 121 registers); the gradients'
+// hold three column sums beside the row and spill, by the compiler's count: whole chunks in
+// fp32 76 registers, with 16-bit weights and an fp32 residual 16 to 23, with a 16-bit one none;
+// an element a load 62 to 102, in fp32 397.
 constexpr int threads_of(bool wave, bool ahead) { return wave ? 256 : ahead ? 512 : 1024; }
 
 template <typename T, typename Y, typename R, int V, bool WAVE, bool AHEAD>
@@ -554,7 +563,8 @@ hipError_t norm_rows(const NormCall &c, hipStream_t s)
                            dim3(nt), 0, s, c);
         return hipGetLastError();
     }
-    // as many workgroups as the GPU holds at once (2,048 threads a unit)
+    // 2,048 threads a unit: about twice what runs at once, since the kernels have 71 to 138
+    // registers a thread (3 to 6 wavefronts a SIMD, not 8); the others begin as those end
     const int most = 256 * (2048 / nt);
     const dim3 grid((unsigned)(c.T < most ? c.T : most));
     if (nt <= 512)
