@@ -10,6 +10,21 @@
 
 namespace moe {
 
+// Threads that one launch takes here at most. HIP starts a grid of 2^32 threads or more
+// modulo 2^32, without an error, so that work past it would be left out: what has more
+// rows is launched in parts, or refused.
+constexpr int64_t kMostThreads = (int64_t)1 << 31;
+
+// run(first, rows) for parts of T rows, at most `most` each, until one fails
+template <typename F> hipError_t in_parts(int64_t T, int64_t most, F run)
+{
+    for (int64_t t = 0; t < T; t += most) {
+        const hipError_t rc = run(t, T - t < most ? T - t : most);
+        if (rc != hipSuccess) return rc;
+    }
+    return hipSuccess;
+}
+
 // ---- plan: histogram, scan + pad fill, placement ----
 hipError_t launch_hist(const int32_t *ids, int nent, int E, int nblk, int32_t *bcnt, hipStream_t s);
 hipError_t launch_scan(const int32_t *bcnt, int nblk, int E, int K, int tm, int nent, int32_t *cnt,

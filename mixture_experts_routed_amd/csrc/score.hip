@@ -545,18 +545,32 @@ __global__ __launch_bounds__(kWaves * 64) void k_route_scored(const ScoreCall p,
     }
 }
 
+// workgroups for rows of L lanes each
+template <int L> unsigned row_blocks(int64_t rows)
+{
+    constexpr int per = kWaves * (64 / L);
+    return (unsigned)((rows + per - 1) / per);
+}
+
 template <int L, int NJ> hipError_t scored_t(const ScoreCall &c, hipStream_t s)
 {
-    const int rows = kWaves * (64 / L);
-    const dim3 grid((unsigned)((c.T + (int64_t)rows - 1) / rows)), block(kWaves * 64);
     const int n = c.E / c.groups;
     const uint32_t magic = n > 1 ? (uint32_t)((((uint64_t)1 << 32) + n - 1) / n) : 0;
-    if (c.E % 4 == 0 && reinterpret_cast<uintptr_t>(c.logits) % 16 == 0 &&
-        reinterpret_cast<uintptr_t>(c.bias) % 16 == 0)
-        hipLaunchKernelGGL((k_route_scored<L, NJ, 4>), grid, block, 0, s, c, magic);
-    else
-        hipLaunchKernelGGL((k_route_scored<L, NJ, 1>), grid, block, 0, s, c, magic);
-    return hipGetLastError();
+    const bool quads = c.E % 4 == 0 && reinterpret_cast<uintptr_t>(c.logits) % 16 == 0 &&
+                       reinterpret_cast<uintptr_t>(c.bias) % 16 == 0;
+    return in_parts(c.T, kMostThreads / L, [&](int64_t t, int64_t rows) {
+        ScoreCall p = c;
+        p.logits += t * c.E;
+        p.ids += t * c.K;
+        p.w += t * c.K;
+        p.T = (int)rows;
+        const dim3 grid(row_blocks<L>(rows)), block(kWaves * 64);
+        if (quads)
+            hipLaunchKernelGGL((k_route_scored<L, NJ, 4>), grid, block, 0, s, p, magic);
+        else
+            hipLaunchKernelGGL((k_route_scored<L, NJ, 1>), grid, block, 0, s, p, magic);
+        return hipGetLastError();
+    });
 }
 
 // ---- gradient ------------------------------------------------------------------
@@ -652,15 +666,24 @@ __global__ __launch_bounds__(kWaves * 64) void k_route_scored_backward(const Sco
 
 template <typename T, int L, int NJ> hipError_t backward_t(const ScoreBackwardCall &c, hipStream_t s)
 {
-    const int rows = kWaves * (64 / L);
-    const dim3 grid((unsigned)((c.T + (int64_t)rows - 1) / rows)), block(kWaves * 64);
-    if (c.E % 4 == 0 && reinterpret_cast<uintptr_t>(c.logits) % 16 == 0 &&
-        reinterpret_cast<uintptr_t>(c.add) % 16 == 0 &&
-        reinterpret_cast<uintptr_t>(c.dlogits) % 16 == 0)
-        hipLaunchKernelGGL((k_route_scored_backward<T, L, NJ, 4>), grid, block, 0, s, c);
-    else
-        hipLaunchKernelGGL((k_route_scored_backward<T, L, NJ, 1>), grid, block, 0, s, c);
-    return hipGetLastError();
+    const bool quads = c.E % 4 == 0 && reinterpret_cast<uintptr_t>(c.logits) % 16 == 0 &&
+                       reinterpret_cast<uintptr_t>(c.add) % 16 == 0 &&
+                       reinterpret_cast<uintptr_t>(c.dlogits) % 16 == 0;
+    return in_parts(c.T, kMostThreads / L, [&](int64_t t, int64_t rows) {
+        ScoreBackwardCall p = c;
+        p.logits += t * c.E;
+        p.ids += t * c.K;
+        p.dw += t * c.K;
+        if (p.add) p.add = static_cast<const T *>(p.add) + t * c.E;
+        p.dlogits = static_cast<T *>(p.dlogits) + t * c.E;
+        p.T = (int)rows;
+        const dim3 grid(row_blocks<L>(rows)), block(kWaves * 64);
+        if (quads)
+            hipLaunchKernelGGL((k_route_scored_backward<T, L, NJ, 4>), grid, block, 0, s, p);
+        else
+            hipLaunchKernelGGL((k_route_scored_backward<T, L, NJ, 1>), grid, block, 0, s, p);
+        return hipGetLastError();
+    });
 }
 
 // lanes of a row and columns of a lane, for E experts: the fewest lanes that hold a row

@@ -1,0 +1,37 @@
+"""Calls whose rows make a grid of 2^32 threads and more, which one launch does not hold: HIP
+starts such a grid modulo 2^32, without an error. Every row is computed."""
+import pytest
+import torch
+
+from gpu_util import abi, say
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("T,E,K", [((1 << 28) + 21, 1, 1), ((1 << 28) + 37, 4, 2)])
+def test_routing_by_scores(T, E, K):
+    """16 lanes a row: 2^28 rows are 2^32 threads"""
+    say(f"[threads] route_scored {T} {E} {K}")
+    logits = torch.zeros((T, E), device="cuda")
+    logits[:, E - 1] = 1.0
+    logits[T // 2:, 0] = 2.0
+    ids, w = torch.full((T, K), -7, dtype=torch.int32, device="cuda"), torch.full((T, K), -7.0,
+                                                                                  device="cuda")
+    abi.route_scored(logits, K, ids=ids, w=w)
+    for t in (0, 1, T // 2 - 1, T // 2, T - 30, T - 1):
+        one, v = abi.route_scored(logits[t:t + 1].clone(), K)
+        assert torch.equal(ids[t:t + 1], one) and torch.equal(w[t:t + 1], v), t
+    # the rows of each half are all alike
+    for part in (slice(0, T // 2), slice(T // 2, T)):
+        for x in (ids, w):
+            assert bool((x[part] == x[part][0]).all())
+    del ids
+    got = torch.full((T, E), -7.0, device="cuda")
+    ids = torch.full((T, K), E - 1, dtype=torch.int32, device="cuda")
+    abi.route_scored_backward(logits, ids, w, score="sigmoid", renorm=False, out=got)
+    for t in (0, T // 2 - 1, T // 2, T - 1):
+        one = abi.route_scored_backward(logits[t:t + 1].clone(), ids[t:t + 1].clone(),
+                                        w[t:t + 1].clone(), score="sigmoid", renorm=False)
+        assert torch.equal(got[t:t + 1], one), t
+    for part in (slice(0, T // 2), slice(T // 2, T)):
+        assert bool((got[part] == got[part][0]).all())
