@@ -117,16 +117,23 @@ __global__ __launch_bounds__(256) void k_route_topk(const float *__restrict__ lo
 hipError_t launch_route_topk(const float *logits, int T, int E, int K, int32_t *ids, float *w,
                              hipStream_t s)
 {
-    const dim3 grid((T + 3) / 4), block(256);
-    if (E <= 2 * kWave)
-        hipLaunchKernelGGL(k_route_topk<2>, grid, block, 0, s, logits, T, E, K, ids, w);
-    else if (E <= 4 * kWave)
-        hipLaunchKernelGGL(k_route_topk<4>, grid, block, 0, s, logits, T, E, K, ids, w);
-    else if (E <= 8 * kWave)
-        hipLaunchKernelGGL(k_route_topk<8>, grid, block, 0, s, logits, T, E, K, ids, w);
-    else
-        hipLaunchKernelGGL(k_route_topk<16>, grid, block, 0, s, logits, T, E, K, ids, w);
-    return hipGetLastError();
+    // a wavefront a token
+    return in_parts(T, kMostThreads / kWave, [&](int64_t t, int64_t rows) {
+        const dim3 grid((unsigned)((rows + 3) / 4)), block(256);
+        const float *l = logits + t * E;
+        int32_t *i = ids + t * K;
+        float *v = w + t * K;
+        const int n = (int)rows;
+        if (E <= 2 * kWave)
+            hipLaunchKernelGGL(k_route_topk<2>, grid, block, 0, s, l, n, E, K, i, v);
+        else if (E <= 4 * kWave)
+            hipLaunchKernelGGL(k_route_topk<4>, grid, block, 0, s, l, n, E, K, i, v);
+        else if (E <= 8 * kWave)
+            hipLaunchKernelGGL(k_route_topk<8>, grid, block, 0, s, l, n, E, K, i, v);
+        else
+            hipLaunchKernelGGL(k_route_topk<16>, grid, block, 0, s, l, n, E, K, i, v);
+        return hipGetLastError();
+    });
 }
 
 }  // namespace moe

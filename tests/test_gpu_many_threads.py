@@ -35,3 +35,18 @@ def test_routing_by_scores(T, E, K):
         assert torch.equal(got[t:t + 1], one), t
     for part in (slice(0, T // 2), slice(T // 2, T)):
         assert bool((got[part] == got[part][0]).all())
+
+
+def test_router():
+    """a wavefront a row: 2^26 rows are 2^32 threads"""
+    T, E, K = (1 << 26) + 21, 3, 2
+    say(f"[threads] route_topk {T}")
+    logits = torch.zeros((T, E), device="cuda")
+    logits[:, 2] = 1.0
+    logits[T // 2:, 0] = 2.0
+    ids = torch.full((T, K), -7, dtype=torch.int32, device="cuda")
+    w = torch.full((T, K), -7.0, device="cuda")
+    abi.moe_route_topk(logits, T, E, K, ids, w)
+    for part in (slice(0, T // 2), slice(T // 2, T)):
+        one, v = abi.route(logits[part][:1].clone(), K)
+        assert bool((ids[part] == one).all()) and bool((w[part] == v).all())
