@@ -232,16 +232,20 @@ hipError_t combine_as(const void *y, const int8_t *yexp, int64_t max_rows, const
                       int T, int K, int d, void *out, int out_dtype, hipStream_t s)
 {
     const int threads = min(1024, (d / (Y16 ? 8 : 4) + kWave - 1) / kWave * kWave);
-    if (out_dtype == 1)
-        combine_any<Y16>(K, dim3(T), dim3(threads), s, y, yexp, max_rows, d, pos, T,
-                         static_cast<_Float16 *>(out));
-    else if (out_dtype == 2)
-        combine_any<Y16>(K, dim3(T), dim3(threads), s, y, yexp, max_rows, d, pos, T,
-                         static_cast<__bf16 *>(out));
-    else
-        combine_any<Y16>(K, dim3(T), dim3(threads), s, y, yexp, max_rows, d, pos, T,
-                         static_cast<float *>(out));
-    return hipGetLastError();
+    return in_parts(T, kMostThreads / threads, [&](int64_t t, int64_t rows) {
+        const int n = (int)rows;
+        auto run = [&](auto *o) {
+            combine_any<Y16>(K, dim3((unsigned)n), dim3(threads), s, y, yexp, max_rows, d,
+                             pos + t * K, n, o + t * d);
+        };
+        if (out_dtype == 1)
+            run(static_cast<_Float16 *>(out));
+        else if (out_dtype == 2)
+            run(static_cast<__bf16 *>(out));
+        else
+            run(static_cast<float *>(out));
+        return hipGetLastError();
+    });
 }
 
 hipError_t launch_combine(const float *y, int64_t max_rows, const int32_t *pos, int T, int K,

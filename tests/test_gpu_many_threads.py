@@ -50,3 +50,19 @@ def test_router():
     for part in (slice(0, T // 2), slice(T // 2, T)):
         one, v = abi.route(logits[part][:1].clone(), K)
         assert bool((ids[part] == one).all()) and bool((w[part] == v).all())
+
+
+@pytest.mark.parametrize("T,d", [((1 << 26) + 21, 8), ((1 << 22) + 5, 4096)])
+def test_combine(T, d):
+    """a workgroup of 64 to 1,024 threads a token: 2^26 tokens of 8 columns, 2^22 of 4,096"""
+    say(f"[threads] combine {T} {d}")
+    y = torch.arange(3 * d, device="cuda", dtype=torch.float32).reshape(3, d) + 1
+    pos = torch.zeros((T, 1), dtype=torch.int32, device="cuda")
+    pos[T // 2:] = 2
+    pos[-1] = -1
+    out = torch.full((T, d), -7.0, device="cuda")
+    abi.moe_combine(y, 3, pos, T, 1, d, out)
+    for part, want in ((slice(0, T // 2), y[0]), (slice(T // 2, T - 1), y[2]),
+                       (slice(T - 1, T), torch.zeros_like(y[0]))):
+        for cut in torch.split(out[part], 1 << 20):
+            assert bool((cut == want).all())
