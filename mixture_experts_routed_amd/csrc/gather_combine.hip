@@ -28,7 +28,7 @@ __device__ __forceinline__ float4 load_nt(const float4 *p)
 }
 
 // xs[r] = x[stok[r]] (bit copy) for r < min(meta[NR], max_rows); zeros on pad
-// rows. vpr = 16-byte vectors per row.
+// rows. vpr = 16-byte vectors per row; row0: the launch's first row.
 // A token's row is copied to up to K rows, in no particular order of r. To
 // fetch each token row into one L2 only, row r is copied by the XCD
 // (stok[r] mod 8) of its token (a pad row by r mod 8): workgroup b scans the
@@ -50,11 +50,11 @@ constexpr int kGatherVec = 5;
 
 __global__ __launch_bounds__(kGatherWaves * kWave) void k_gather(
     const uint4 *__restrict__ x, int T, int vpr, const int32_t *__restrict__ stok,
-    const int32_t *__restrict__ meta, int64_t max_rows, uint4 *__restrict__ xs)
+    const int32_t *__restrict__ meta, int64_t row0, int64_t max_rows, uint4 *__restrict__ xs)
 {
     const int xcd = blockIdx.x & 7;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int64_t r0 = ((int64_t)(blockIdx.x >> 3) * kGatherWaves + wave) * kWave;
+    const int64_t r0 = row0 + ((int64_t)(blockIdx.x >> 3) * kGatherWaves + wave) * kWave;
     const int64_t nr = min((int64_t)meta[kMetaNr], max_rows);
     if (r0 >= nr) return;
     const int lane = threadIdx.x & 63;
@@ -220,11 +220,14 @@ hipError_t launch_gather(const void *x, int elem_bytes, int T, int d, const int3
 {
     const int vpr = d * elem_bytes / 16;
     constexpr int rows_per_group = kGatherWaves * kWave;
-    const int64_t blocks = (max_rows + rows_per_group - 1) / rows_per_group * 8;
-    hipLaunchKernelGGL(k_gather, dim3((unsigned)blocks), dim3(kGatherWaves * kWave), 0, s,
-                       static_cast<const uint4 *>(x), T, vpr, stok, meta, max_rows,
-                       static_cast<uint4 *>(xs));
-    return hipGetLastError();
+    // (8 workgroups a group of rows: 8 threads a row)
+    return in_parts(max_rows, kMostThreads / 8, [&](int64_t r, int64_t rows) {
+        const int64_t blocks = (rows + rows_per_group - 1) / rows_per_group * 8;
+        hipLaunchKernelGGL(k_gather, dim3((unsigned)blocks), dim3(kGatherWaves * kWave), 0, s,
+                           static_cast<const uint4 *>(x), T, vpr, stok, meta, r, max_rows,
+                           static_cast<uint4 *>(xs));
+        return hipGetLastError();
+    });
 }
 
 template <bool Y16>

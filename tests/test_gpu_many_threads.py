@@ -66,3 +66,23 @@ def test_combine(T, d):
                        (slice(T - 1, T), torch.zeros_like(y[0]))):
         for cut in torch.split(out[part], 1 << 20):
             assert bool((cut == want).all())
+
+
+def test_gather():
+    """8 threads a row: 2^29 rows are 2^32 threads"""
+    n, T, d = (1 << 29) + 77, 3, 8
+    say(f"[threads] gather {n}")
+    x = torch.arange(T * d, device="cuda", dtype=torch.float32).reshape(T, d).to(torch.bfloat16) + 1
+    stok = torch.zeros(n, dtype=torch.int32, device="cuda")
+    stok[n // 2:] = 2
+    stok[-3] = -1
+    stok[-2] = 1
+    meta = torch.zeros(abi.META_N, dtype=torch.int32, device="cuda")
+    meta[2] = n - 1  # rows of the plan (MOE_META_NR): the last one stays as it is
+    xs = torch.full((n, d), -7.0, dtype=torch.bfloat16, device="cuda")
+    abi.moe_gather(x, abi.MOE_BF16, T, d, stok, meta, n, xs)
+    for part, want in ((slice(0, n // 2), x[0]), (slice(n // 2, n - 3), x[2]),
+                       (slice(n - 3, n - 2), 0 * x[0]), (slice(n - 2, n - 1), x[1]),
+                       (slice(n - 1, n), torch.full_like(x[0], -7.0))):
+        for cut in torch.split(xs[part], 1 << 25):
+            assert bool((cut == want).all())
