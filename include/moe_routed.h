@@ -222,8 +222,11 @@ int moe_ffn_big_cells(int E, int d, int f, int tm, int64_t max_rows, int dtype, 
  * scratch: at least moe_ffn_scratch_bytes().
  * Errors: MOE_EINVAL for d or f not positive multiples of 8 or above 2^22,
  * one expert matrix of 2 GiB or more, bad dtype, NULL/misaligned pointers,
- * small scratch, tm < 1; MOE_EUNSUPPORTED for E > MOE_MAX_EXPERTS; MOE_EHIP on
- * a failed launch.
+ * small scratch, tm < 1, more workgroups than a launch of 2^32 threads holds
+ * (items of 64 rows, by max_rows, E and tm, times groups of 256 columns of h or
+ * 512 of y: 2^24 of them; packed 16-bit weights with 64 rows an expert or more,
+ * 193 rows times 128 columns of h or 256 of y: 2^23); MOE_EUNSUPPORTED for E > MOE_MAX_EXPERTS; MOE_EHIP
+ * on a failed launch.
  */
 int moe_expert_ffn(const void *xs, const void *w_gate, const void *w_up, const void *w_down,
                    int dtype, int E, int d, int f, int tm, const int32_t *eoff, const int32_t *stok,

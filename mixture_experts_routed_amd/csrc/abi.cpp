@@ -32,10 +32,21 @@ int plan_sizes(int T, int K, int E, int tm, moe_plan_sizes_t *o)
     return MOE_OK;
 }
 
+// Whether each projection's workgroups (256 threads, and 8 more where the call is planned
+// in the launch; the big cells' 512) stay below the 2^32 threads that a launch holds
+bool ffn_grids_ok(const moe::FfnShape &z, int wf)
+{
+    constexpr int64_t threads = 4294967295;
+    const int64_t cells = threads / 256 - 8, big = threads / 512;
+    return z.blocks_gu <= cells && z.blocks_dn <= cells &&
+           (wf != moe::kPacked || ((!z.big_gu || z.blocks_big_gu <= big) &&
+                                   (!z.big_dn || z.blocks_big_dn <= big)));
+}
+
 int ffn_check(const void *xs, const void *wg, const void *wu, const void *wd, int dtype, int E,
               int d, int f, int tm, const int32_t *eoff, const int32_t *stok, const float *sw,
               const int32_t *meta, int64_t max_rows, const void *h, const float *y,
-              const void *scratch, size_t scratch_bytes)
+              const void *scratch, size_t scratch_bytes, int wf)
 {
     if (!dtype_ok(dtype) || E < 1 || tm < 1 || d < 8 || f < 8 || d % 8 || f % 8 || max_rows < 1 ||
         max_rows > kI32Max - 1024)
@@ -51,9 +62,7 @@ int ffn_check(const void *xs, const void *wg, const void *wu, const void *wd, in
         !aligned(sw, 4) || !aligned(meta, 4) || !aligned(scratch, 16))
         return MOE_EINVAL;
     const moe::FfnShape z = moe::ffn_shape(E, tm, max_rows, d, f, dtype);
-    if (z.blocks_gu > kI32Max || z.blocks_dn > kI32Max || z.blocks_big_gu > kI32Max ||
-        z.blocks_big_dn > kI32Max)
-        return MOE_EINVAL;
+    if (!ffn_grids_ok(z, wf)) return MOE_EINVAL;
     if (scratch_bytes < z.scratch_bytes) return MOE_EINVAL;
     return MOE_OK;
 }
@@ -178,7 +187,7 @@ int ffn_impl(const void *xs, const void *wg, const void *wu, const void *wd, int
              const moe::WavePlan *wp = nullptr)
 {
     const int rc = ffn_check(xs, wg, wu, wd, dtype, E, d, f, tm, eoff, stok, sw, meta, max_rows, h,
-                             y, scratch, scratch_bytes);
+                             y, scratch, scratch_bytes, wf);
     if (rc != MOE_OK) return rc;
     const moe::FfnShape z = moe::ffn_shape(E, tm, max_rows, d, f, dtype);
     if (!have_items) {
@@ -349,6 +358,7 @@ int forward_impl(const void *x, const int32_t *ids, const float *w, const void *
     auto f32 = [&](size_t off) { return reinterpret_cast<float *>(b + off); };
     bool items = false;
     const moe::FfnShape fz = moe::ffn_shape(E, tm, z.max_rows, d, f, dtype);
+    if (!ffn_grids_ok(fz, wf)) return MOE_EINVAL;  // (before the plan is launched)
     // The gate/up kernel gathers its rows from x itself when x is addressable
     // by one buffer descriptor (< 2 GiB); otherwise the rows are gathered first.
     const bool fused_gather = (size_t)T * d * elem_bytes(dtype) < ((size_t)1 << 31);
